@@ -40,8 +40,9 @@
  *      W2       [E][H][I]
  *      out      [T][H]      bf16
  *    The forward calls take W1 and W2 pre-packed by moe_pack_weights (same
- *    byte size, MFMA-fragment order), through the moe_packed_weights_t
- *    descriptor that moe_pack_weights fills; everything else is row-major.
+ *    byte size, MFMA-fragment order; MXFP4: by moe_pack_weights_mxfp4), through
+ *    the moe_packed_weights_t descriptor that it fills; everything else is
+ *    row-major.
  *    bf16 is IEEE binary16-brain (1/8/7); fp8 is OCP E4M3 ("e4m3fn",
  *    max finite 448).
  *  - Stage order: [fp8: quantise x] -> gate-up GEMM -> SiLU-and-mul
@@ -82,9 +83,20 @@ typedef enum {
                                  bf16 activations */
     MOE_DTYPE_FP8_BLOCK = 5,  /* e4m3 weights with an fp32 scale per 128 x 128 block,
                                  e4m3 activations with one per 128-value row group */
-    MOE_DTYPE_INT8_W8A16 = 6  /* int8 weights (per-output-channel fp32 scales),
+    MOE_DTYPE_INT8_W8A16 = 6, /* int8 weights (per-output-channel fp32 scales),
                                  bf16 activations */
+    MOE_DTYPE_MXFP4 = 8       /* OCP MXFP4: e2m1 values with one e8m0 scale per 32
+                                 consecutive K values, weights and activations
+                                 (7 is not a dtype) */
 } moe_dtype_t;
+
+/* Element type of the rows that moe_quantize_mxfp4, moe_dispatch, moe_combine
+ * and their relatives take. */
+typedef enum {
+    MOE_ROW_BF16 = 0,
+    MOE_ROW_FP16 = 1,
+    MOE_ROW_FP32 = 2
+} moe_row_type_t;
 
 /* One row tile of the task map: rows [row_begin, row_begin + rows) of the
  * expert-sorted order, all routed to `expert`; rows <= block_m. */
@@ -150,15 +162,18 @@ typedef struct {
                            fp8 otherwise: fp32 [P][I] SiLU(gate)*up before
                            requantisation; unused on bf16 outside tiling 2
                            with split_k1 > 1 */
-    size_t h;           /* bf16 [P][I] SiLU(gate)*up (bf16), or uint8 e4m3 codes [P][I] (fp8) */
+    size_t h;           /* bf16 [P][I] SiLU(gate)*up (bf16), or uint8 e4m3 codes [P][I] (fp8);
+                           MXFP4: codes and scale codes of every task's rows, in the
+                           order in which the down GEMM reads them (x_scale likewise) */
     size_t h_scale;     /* fp8: fp32  [P]      per-row scales of h */
     size_t y;           /* tiling 2 with split_k2 > 1: fp32 [split_k2][P][H]
                            unweighted down partial sums; otherwise bf16
                            [P][H] unweighted down rows (fp8, tilings 0 and 2:
                            weight scales only); unused (SIZE_MAX) on bf16,
                            fp8 and int8 w8a8 at T = 1 with tiling 0 and an
-                           even number of 64-byte steps in an I row, where the
-                           down launch adds the token's top-k rows itself */
+                           even number of 64-byte steps in an I row, and on
+                           MXFP4 at T = 1, where the down launch adds the
+                           token's top-k rows itself */
     size_t total_bytes; /* minimum size of the workspace */
     int32_t split_k1;   /* slices of the gate-up reduction over H (1 unless tiling 2) */
     int32_t split_k2;   /* slices of the down reduction over I */
@@ -431,6 +446,112 @@ int moe_forward_mxfp8(const void *x, const float *topk_w, const void *routing,
                       const moe_packed_weights_t *w2, const uint8_t *w2_scale,
                       int T, int k, int E, int H, int I,
                       void *workspace, size_t workspace_bytes, void *out, void *stream);
+
+/* MXFP4 (OCP Microscaling; SGLang tuning guide, block shapes: gfx95 devices
+ * keep MX's [1, 32] blocks).  32 consecutive values of a row share one e8m0
+ * scale code c, meaning 2^(c - 127), and hold e2m1 codes: 0, 1/2, 1, 3/2, 2,
+ * 3, 4 or 6 with a sign (bit 3), two a byte, the lower column in the low
+ * nibble.
+ *
+ * moe_quantize_mxfp4: x (device) [rows][cols] of row_type (moe_row_type_t),
+ * rows row_stride elements apart, -> codes (device) uint8 [rows][cols/2] and
+ * scales (device) uint8 [rows][cols/32], by the OCP rule: scale 2^s, s =
+ * floor(log2(max|v|)) - 2, at least -127 (-127 for a zero block); codes are
+ * v * 2^-s rounded to nearest even, at most 6.  A block that holds an Inf or
+ * a NaN takes scale code 255 (NaN) and zero codes: all its values are NaN.
+ * Requires cols % 32 == 0, row_stride >= cols, row_stride * element size a
+ * multiple of 16 bytes, x 16-byte and codes 4-byte aligned.  rows == 0
+ * returns MOE_OK with no launch.
+ * moe_dequantize_mxfp4: the values of such codes, out (device, 16-byte
+ * aligned) [rows][cols] of row_type, rounded to nearest even where the type
+ * does not hold them (fp16: large and small scales; bf16: subnormals). */
+int moe_quantize_mxfp4(const void *x, int row_type, int64_t rows, int cols, int64_t row_stride,
+                       uint8_t *codes, uint8_t *scales, void *stream);
+int moe_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t rows, int cols,
+                         int row_type, void *out, void *stream);
+
+/* One-time pre-pack of an MXFP4 weight tensor: codes (device, 16-byte
+ * aligned) [E][rows][cols/2] and scales (device) [E][rows][cols/32], both
+ * row-major, -> packed (device, 16-byte aligned, E * rows * (cols/2 +
+ * cols/32) bytes, no overlap): codes and scale codes together in the order in
+ * which the product reads them.  desc (host) as moe_pack_weights fills it, with
+ * dtype MOE_DTYPE_MXFP4; moe_describe_packed_weights takes bytes packed here
+ * before.  Requires rows % 32 == 0 and cols % 128 == 0. */
+int moe_pack_weights_mxfp4(const uint8_t *codes, const uint8_t *scales, int E, int rows, int cols,
+                           void *packed, moe_packed_weights_t *desc /* host, out */, void *stream);
+
+/* The layer in MXFP4, weights and activations.  Routing build: as
+ * moe_build_routing_bf16, with the tile height of the MXFP4 forward.
+ * Forward: as moe_forward_bf16, with w1 / w2 (host) descriptors from
+ * moe_pack_weights_mxfp4 of W1 [E][2I][H] and W2 [E][H][I].  x is quantised
+ * per token and SiLU(gate)*up per (token, expert) row by the rule of
+ * moe_quantize_mxfp4; the products run on the scaled MFMA in its 4-bit mode
+ * with fp32 accumulation, SiLU(gate)*up is formed and quantised from the fp32
+ * sums, and the per-pair down rows are stored as bf16 (at T = 1 they are added
+ * in fp32 and not stored).  A NaN or Inf in a token's row, in a weight or in an
+ * intermediate makes the values of its block NaN, and with them the outputs
+ * that they enter.  H and I must be multiples of 128.
+ * moe_route_forward_mxfp4: both in one call, with the same results; at most
+ * 64 pairs on the register-streaming plan are routed inside the x
+ * quantisation. */
+int moe_build_routing_mxfp4(const int32_t *topk_ids, int T, int k, int E, int H, int I,
+                            void *routing, size_t routing_bytes, void *stream);
+int moe_forward_mxfp4(const void *x, const float *topk_w, const void *routing,
+                      const moe_packed_weights_t *w1, const moe_packed_weights_t *w2,
+                      int T, int k, int E, int H, int I,
+                      void *workspace, size_t workspace_bytes, void *out, void *stream);
+int moe_route_forward_mxfp4(const int32_t *topk_ids, const void *x, const float *topk_w,
+                            void *routing, size_t routing_bytes,
+                            const moe_packed_weights_t *w1, const moe_packed_weights_t *w2,
+                            int T, int k, int E, int H, int I,
+                            void *workspace, size_t workspace_bytes, void *out, void *stream);
+
+/* Token rows to expert order and back (blog section "MoE", routing & index
+ * build: the route index names each pair's row in the expert-sorted order),
+ * for experts other than the fused layer's, and their gradients.  `routing`
+ * (device, 16-byte aligned, at least moe_routing_layout().tasks bytes) is a
+ * routing buffer of any dtype's build for the same T, k and E; pair p = t*k + j
+ * with a valid id stands at sorted row r = pair_pos[p], expert e owning rows
+ * [expert_offsets[e], expert_offsets[e+1]).
+ *   moe_dispatch       xs[r] = w[p] x[t]
+ *   moe_combine        out[t] = sum over j of w[p] y[r]
+ *   moe_dispatch_grad  dx[t] = sum over j of w[p] dxs[r],  dw[p] = <dxs[r], x[t]>
+ *   moe_combine_grad   dy[r] = w[p] dout[t],               dw[p] = <y[r], dout[t]>
+ * Token rows are [T][H] and sorted rows [T*k][H], both of row_type
+ * (moe_row_type_t); topk_w and dtopk_w are fp32 [T][k].  topk_w NULL means
+ * weights of 1 (a dispatch is then a copy).  dtopk_w NULL leaves out the
+ * weights' gradient, and x of moe_dispatch_grad or y of moe_combine_grad is
+ * then not read and may be NULL; with dtopk_w, topk_w must be given.
+ * Dropped pairs add nothing, their weights are not read into any result and
+ * their dw is 0; a token whose pairs are all dropped gets a zero row.  Sorted
+ * rows behind the last valid one are neither read nor written.  Products and
+ * sums run in fp32, in ascending j (dw: in a fixed order), rounded once.
+ * Requires 1 <= k <= 16, T*k <= 65536, 1 <= E <= 511, H a multiple of 8 (at
+ * most 65536), rows 16-byte aligned, no overlap of inputs and outputs. */
+int moe_dispatch(const void *x, int row_type, const float *topk_w, const void *routing,
+                 size_t routing_bytes, int T, int k, int E, int H, void *xs, void *stream);
+int moe_combine(const void *y, int row_type, const float *topk_w, const void *routing,
+                size_t routing_bytes, int T, int k, int E, int H, void *out, void *stream);
+int moe_dispatch_grad(const void *dxs, const void *x, int row_type, const float *topk_w,
+                      const void *routing, size_t routing_bytes, int T, int k, int E, int H,
+                      void *dx, float *dtopk_w, void *stream);
+int moe_combine_grad(const void *dout, const void *y, int row_type, const float *topk_w,
+                     const void *routing, size_t routing_bytes, int T, int k, int E, int H,
+                     void *dy, float *dtopk_w, void *stream);
+
+/* Gradient of moe_router_topk: from dtopk_w (device) fp32 [T][k+n_shared],
+ * the gradient of its weights, dlogits (device) fp32 [T][E], that of the
+ * scores.  topk_ids and topk_w are what moe_router_topk wrote for the same
+ * logits.  With s = sum over the k chosen of w_j dw_j and p the softmax over
+ * the E scores:
+ *   renormalize = 1   dl[e_j] = w_j (dw_j - s), 0 for experts not chosen
+ *   renormalize = 0   dl[e] = (w_j dw_j where e = e_j) - p[e] s
+ * The choice itself is a constant, and so are the n_shared columns' weights.
+ * logits is read with renormalize = 0 only (NULL otherwise allowed); a NaN
+ * score has p = 0.  Same limits as moe_router_topk. */
+int moe_router_topk_grad(const float *logits, const int32_t *topk_ids, const float *topk_w,
+                         const float *dtopk_w, int T, int E, int k, int renormalize, int n_shared,
+                         float *dlogits, void *stream);
 
 /* int8 w8a8 with per-channel weight scales (SGLang tuning guide: the
  * int8_w8a8 dtype with per-channel quantisation).  As the fp8 pair, with

@@ -23,6 +23,13 @@ Functions carry the C names:
     moe_build_routing_int4 / moe_forward_int4   (int4 weights + group scales, bf16 activations)
     moe_build_routing_fp8_block / moe_forward_fp8_block (128x128 weight blocks, 1x128 token groups)
     moe_build_routing_int8_w8a16 / moe_forward_int8_w8a16 (int8 weights + row scales, bf16 activations)
+    moe_quantize_mxfp4(x) / moe_dequantize_mxfp4(codes, scales) -> MXFP4 codes and scale codes / values
+    moe_pack_weights_mxfp4(codes, scales)               -> PackedWeight (one-time)
+    moe_build_routing_mxfp4 / moe_forward_mxfp4         (as the bf16 pair, MXFP4 weights and activations)
+    moe_dispatch(x, routing, k, E, topk_w)              -> rows in expert order
+    moe_combine(y, routing, k, E, topk_w)               -> rows in token order
+    moe_dispatch_grad / moe_combine_grad                (gradients of the rows and of topk_w)
+    moe_router_topk_grad(logits, topk_ids, topk_w, dtopk_w) -> gradient of the router scores
 
 plus allocation helpers (alloc_routing, alloc_workspace), pack_weights() for a
 whole weight dict, and a convenience moe_layer() that runs routing + forward
@@ -46,9 +53,11 @@ MOE_DTYPE_INT8_W8A8 = 3
 MOE_DTYPE_INT4_W4A16 = 4
 MOE_DTYPE_FP8_BLOCK = 5
 MOE_DTYPE_INT8_W8A16 = 6
+MOE_DTYPE_MXFP4 = 8
 DTYPES = {"bf16": MOE_DTYPE_BF16, "fp8": MOE_DTYPE_FP8_W8A8, "mxfp8": MOE_DTYPE_MXFP8,
           "int8": MOE_DTYPE_INT8_W8A8, "int4": MOE_DTYPE_INT4_W4A16, "fp8b": MOE_DTYPE_FP8_BLOCK,
-          "int8w": MOE_DTYPE_INT8_W8A16}
+          "int8w": MOE_DTYPE_INT8_W8A16, "mxfp4": MOE_DTYPE_MXFP4}
+ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
 class MoeError(RuntimeError):
@@ -81,7 +90,8 @@ class PackedWeightsDesc(ctypes.Structure):
 class PackedWeight:
     """A weight tensor packed by moe_pack_weights together with the
     library's descriptor of it, which the forward calls take.  `tensor` is
-    the packed device tensor (same shape and dtype as the row-major one)."""
+    the packed device tensor (same shape and dtype as the row-major one; MXFP4:
+    uint8 [E][rows][cols / 2 + cols / 32], codes and scale codes)."""
 
     def __init__(self, tensor, desc):
         self.tensor = tensor
@@ -113,7 +123,10 @@ EXPORTS = ("moe_status_string", "moe_pack_weights", "moe_describe_packed_weights
            "moe_build_routing_int8_w8a16", "moe_forward_int8_w8a16", "moe_set_stage_events", "moe_device_cu_count",
            "moe_stream_read", "moe_forward_fp8_noalloc", "moe_route_forward_bf16", "moe_route_forward_fp8",
            "moe_route_forward_int8", "moe_route_forward_fp8_block", "moe_route_forward_mxfp8",
-           "moe_route_forward_int4", "moe_route_forward_int8_w8a16", "moe_tile_copy_read")
+           "moe_route_forward_int4", "moe_route_forward_int8_w8a16", "moe_tile_copy_read",
+           "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_pack_weights_mxfp4", "moe_build_routing_mxfp4",
+           "moe_forward_mxfp4", "moe_route_forward_mxfp4", "moe_dispatch", "moe_combine", "moe_dispatch_grad",
+           "moe_combine_grad", "moe_router_topk_grad")
 
 
 def _load():
@@ -180,6 +193,21 @@ def _load():
               L.moe_route_forward_int4, L.moe_route_forward_int8_w8a16):
         f.restype = i
         f.argtypes = [P, P, P, P, sz, D, P, D, P, i, i, i, i, i, P, sz, P, P]
+    i64 = ctypes.c_int64
+    for n, args in (("moe_quantize_mxfp4", [P, i, i64, i, i64, P, P, P]),
+                    ("moe_dequantize_mxfp4", [P, P, i64, i, i, P, P]),
+                    ("moe_pack_weights_mxfp4", [P, P, i, i, i, P, D, P]),
+                    ("moe_build_routing_mxfp4", [P, i, i, i, i, i, P, sz, P]),
+                    ("moe_forward_mxfp4", [P, P, P, D, D, i, i, i, i, i, P, sz, P, P]),
+                    ("moe_route_forward_mxfp4", [P, P, P, P, sz, D, D, i, i, i, i, i, P, sz, P, P]),
+                    ("moe_dispatch", [P, i, P, P, sz, i, i, i, i, P, P]),
+                    ("moe_combine", [P, i, P, P, sz, i, i, i, i, P, P]),
+                    ("moe_dispatch_grad", [P, P, i, P, P, sz, i, i, i, i, P, P, P]),
+                    ("moe_combine_grad", [P, P, i, P, P, sz, i, i, i, i, P, P, P]),
+                    ("moe_router_topk_grad", [P, P, P, P, i, i, i, i, i, P, P])):
+        f = getattr(L, n)
+        f.restype = i
+        f.argtypes = args
     return L
 
 
@@ -232,6 +260,10 @@ def moe_describe_packed_weights(packed, dtype):
     E, rows, cols = packed.shape
     if code == MOE_DTYPE_INT4_W4A16:
         cols *= 2
+    elif code == MOE_DTYPE_MXFP4:
+        if cols % 17 or not packed.is_contiguous() or packed.element_size() != 1:
+            raise ValueError("moe_describe_packed_weights: packed MXFP4 rows hold cols / 2 + cols / 32 contiguous bytes")
+        cols = cols // 17 * 32
     desc = PackedWeightsDesc()
     _check("moe_describe_packed_weights",
            _lib.moe_describe_packed_weights(_ptr(packed), E, rows, cols, code, ctypes.byref(desc)))
@@ -239,8 +271,13 @@ def moe_describe_packed_weights(packed, dtype):
 
 
 def pack_weights(weights, dtype="bf16", stream=None):
-    """Weight dict with w1/w2 packed for the forward calls (scales copied by reference)."""
+    """Weight dict with w1/w2 packed for the forward calls (scales copied by
+    reference; MXFP4: packed with the codes and left out)."""
     out = dict(weights)
+    if dtype == "mxfp4":
+        for n in ("w1", "w2"):
+            out[n] = moe_pack_weights_mxfp4(weights[n], out.pop(n + "_scale"), stream=stream)
+        return out
     out["w1"] = moe_pack_weights(weights["w1"], dtype, stream=stream)
     out["w2"] = moe_pack_weights(weights["w2"], dtype, stream=stream)
     return out
@@ -410,7 +447,7 @@ def build_routing(topk_ids, E, H, I, routing, dtype="bf16", stream=None):
     {"bf16": moe_build_routing_bf16, "fp8": moe_build_routing_fp8,
      "mxfp8": moe_build_routing_mxfp8, "int8": moe_build_routing_int8,
      "int4": moe_build_routing_int4, "fp8b": moe_build_routing_fp8_block,
-     "int8w": moe_build_routing_int8_w8a16}[dtype](
+     "int8w": moe_build_routing_int8_w8a16, "mxfp4": moe_build_routing_mxfp4}[dtype](
         topk_ids, E, H, I, routing, stream)
 
 
@@ -568,6 +605,8 @@ def route_forward(topk_ids, x, topk_w, routing, weights, workspace, out, dtype="
     W = weights
     if dtype == "bf16":
         return moe_route_forward_bf16(topk_ids, x, topk_w, routing, W["w1"], W["w2"], workspace, out, stream)
+    if dtype == "mxfp4":
+        return moe_route_forward_mxfp4(topk_ids, x, topk_w, routing, W["w1"], W["w2"], workspace, out, stream)
     fn = {"fp8": moe_route_forward_fp8, "int8": moe_route_forward_int8, "fp8b": moe_route_forward_fp8_block,
           "mxfp8": moe_route_forward_mxfp8, "int4": moe_route_forward_int4,
           "int8w": moe_route_forward_int8_w8a16}[dtype]
@@ -688,6 +727,230 @@ def moe_forward_int8(x, topk_w, routing, w1, w1_scale, w2, w2_scale, workspace, 
     return out
 
 
+def _check_device(**tensors):
+    """Every given tensor is on the current GPU (a kernel cannot take host
+    memory, and a launch goes to the current device's streams)."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if isinstance(t, PackedWeight):
+            t = t.tensor
+        if not t.is_cuda or t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name}: expected a tensor on the current GPU, got one on {t.device}")
+
+
+def _empty(shape, dtype, device, stream):
+    """An output allocated for use on `stream` (None: the current stream)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _row_type(name, t):
+    if t.dtype not in ROW_TYPES:
+        raise ValueError(f"{name}: expected bf16, fp16 or fp32 rows, got {t.dtype}")
+    return ROW_TYPES[t.dtype]
+
+
+def moe_quantize_mxfp4(x, codes=None, scales=None, stream=None):
+    """MXFP4 of rows x [..., cols] (bf16, fp16 or fp32; contiguous, or 2-D with
+    contiguous rows apart by x.stride(0)): (codes uint8 [..., cols / 2], scales
+    uint8 [..., cols / 32]).  A block that holds Inf or NaN becomes NaN."""
+    kind = _row_type("x", x)
+    if x.dim() < 1 or x.shape[-1] % 32 or x.shape[-1] == 0:
+        raise ValueError(f"x: expected rows of a multiple of 32 values, got {tuple(x.shape)}")
+    cols = x.shape[-1]
+    stride = cols
+    if not x.is_contiguous():
+        if x.dim() != 2 or x.stride(1) != 1 or x.stride(0) < cols:
+            raise ValueError(f"x: expected contiguous rows, got strides {x.stride()}")
+        stride = x.stride(0)
+    if codes is None:
+        codes = _empty((*x.shape[:-1], cols // 2), torch.uint8, x.device, stream)
+    if scales is None:
+        scales = _empty((*x.shape[:-1], cols // 32), torch.uint8, x.device, stream)
+    _check_tensor("codes", codes, torch.uint8, (*x.shape[:-1], cols // 2))
+    _check_tensor("scales", scales, torch.uint8, (*x.shape[:-1], cols // 32))
+    _check_device(x=x, codes=codes, scales=scales)
+    _check("moe_quantize_mxfp4", _lib.moe_quantize_mxfp4(
+        _ptr(x), kind, x.numel() // cols, cols, stride, _ptr(codes), _ptr(scales), _stream(stream)))
+    return codes, scales
+
+
+def moe_dequantize_mxfp4(codes, scales, dtype=torch.bfloat16, out=None, stream=None):
+    """Values [..., cols] (bf16, fp16 or fp32) of MXFP4 codes [..., cols / 2] and
+    scale codes [..., cols / 32]."""
+    if codes.dim() < 1 or codes.shape[-1] % 16 or codes.shape[-1] == 0:
+        raise ValueError(f"codes: expected rows of a multiple of 16 bytes, got {tuple(codes.shape)}")
+    lead, cols = codes.shape[:-1], 2 * codes.shape[-1]
+    if out is None:
+        out = _empty((*lead, cols), dtype, codes.device, stream)
+    kind = _row_type("out", out)
+    _check_tensor("codes", codes, torch.uint8, (*lead, cols // 2))
+    _check_tensor("scales", scales, torch.uint8, (*lead, cols // 32))
+    _check_tensor("out", out, out.dtype, (*lead, cols))
+    _check_device(codes=codes, scales=scales, out=out)
+    _check("moe_dequantize_mxfp4", _lib.moe_dequantize_mxfp4(
+        _ptr(codes), _ptr(scales), out.numel() // cols, cols, kind, _ptr(out), _stream(stream)))
+    return out
+
+
+def moe_pack_weights_mxfp4(codes, scales, out=None, stream=None):
+    """PackedWeight of row-major MXFP4 weights: codes uint8 [E][rows][cols / 2]
+    and scale codes uint8 [E][rows][cols / 32]."""
+    if codes.dim() != 3:
+        raise ValueError(f"codes: expected [E][rows][cols / 2], got {tuple(codes.shape)}")
+    E, rows, cols = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
+    _check_tensor("codes", codes, torch.uint8, (E, rows, cols // 2))
+    _check_tensor("scales", scales, torch.uint8, (E, rows, cols // 32))
+    if out is None:
+        out = _empty((E, rows, cols // 2 + cols // 32), torch.uint8, codes.device, stream)
+    _check_tensor("out", out, torch.uint8, (E, rows, cols // 2 + cols // 32))
+    _check_device(codes=codes, scales=scales, out=out)
+    desc = PackedWeightsDesc()
+    _check("moe_pack_weights_mxfp4", _lib.moe_pack_weights_mxfp4(
+        _ptr(codes), _ptr(scales), E, rows, cols, _ptr(out), ctypes.byref(desc), _stream(stream)))
+    return PackedWeight(out, desc)
+
+
+def moe_build_routing_mxfp4(topk_ids, E, H, I, routing, stream=None):
+    _build_routing(_lib.moe_build_routing_mxfp4, "moe_build_routing_mxfp4", topk_ids, E, H, I, routing, stream)
+
+
+def _mxfp4_sizes(x, topk_w, w1, w2, workspace, out):
+    """(T, k, E, H, I) of an MXFP4 forward call, its tensors checked."""
+    T, H = x.shape
+    k = topk_w.shape[1]
+    E, I2 = w1.shape[:2]
+    I = I2 // 2
+    _check_tensor("x", x, torch.bfloat16, (T, H))
+    _check_tensor("topk_w", topk_w, torch.float32, (T, k))
+    _check_tensor("w1", w1, torch.uint8, (E, 2 * I, H // 2 + H // 32))
+    _check_tensor("w2", w2, torch.uint8, (E, H, I // 2 + I // 32))
+    _check_tensor("out", out, torch.bfloat16, (T, H))
+    _check_device(x=x, topk_w=topk_w, w1=w1, w2=w2, workspace=workspace, out=out)
+    return T, k, E, H, I
+
+
+def moe_forward_mxfp4(x, topk_w, routing, w1, w2, workspace, out, stream=None):
+    T, k, E, H, I = _mxfp4_sizes(x, topk_w, w1, w2, workspace, out)
+    _check_device(routing=routing)
+    _check("moe_forward_mxfp4", _lib.moe_forward_mxfp4(
+        _ptr(x), _ptr(topk_w), _ptr(routing), _desc("w1", w1), _desc("w2", w2), T, k, E, H, I,
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out), _stream(stream)))
+    return out
+
+
+def moe_route_forward_mxfp4(topk_ids, x, topk_w, routing, w1, w2, workspace, out, stream=None):
+    """moe_build_routing_mxfp4 + moe_forward_mxfp4 in one call."""
+    T, k, E, H, I = _mxfp4_sizes(x, topk_w, w1, w2, workspace, out)
+    _check_tensor("topk_ids", topk_ids, torch.int32, (T, k))
+    _check_device(topk_ids=topk_ids, routing=routing)
+    _check("moe_route_forward_mxfp4", _lib.moe_route_forward_mxfp4(
+        _ptr(topk_ids), _ptr(x), _ptr(topk_w), _ptr(routing), routing.numel() * routing.element_size(),
+        _desc("w1", w1), _desc("w2", w2), T, k, E, H, I, _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(out), _stream(stream)))
+    return out
+
+
+def _rows(name, t, k, sorted_rows):
+    """(T, H) of token rows [T][H], or of sorted rows [T * k][H]."""
+    if k < 1 or t.dim() != 2 or (sorted_rows and t.shape[0] % k):
+        raise ValueError(f"{name}: expected {'[T * k]' if sorted_rows else '[T]'}[H] rows, got {tuple(t.shape)}, k = {k}")
+    return (t.shape[0] // k if sorted_rows else t.shape[0]), t.shape[1]
+
+
+def _move(name, fn, src, src_name, sorted_src, routing, k, E, topk_w, out, out_name, stream):
+    kind = _row_type(src_name, src)
+    T, H = _rows(src_name, src, k, sorted_src)
+    shape = (T, H) if sorted_src else (T * k, H)
+    if out is None:
+        out = _empty(shape, src.dtype, src.device, stream)
+    _check_tensor(src_name, src, src.dtype, src.shape)
+    _check_tensor(out_name, out, src.dtype, shape)
+    if topk_w is not None:
+        _check_tensor("topk_w", topk_w, torch.float32, (T, k))
+    _check_device(**{src_name: src, out_name: out}, topk_w=topk_w, routing=routing)
+    _check(name, fn(_ptr(src), kind, _ptr(topk_w), _ptr(routing), routing.numel() * routing.element_size(), T, k, E, H,
+                    _ptr(out), _stream(stream)))
+    return out
+
+
+def moe_dispatch(x, routing, k, E, topk_w=None, out=None, stream=None):
+    """Token rows x [T][H] (bf16, fp16 or fp32) to expert order: out [T * k][H],
+    row r the (weighted) token of the pair sorted there.  Rows behind the last
+    valid pair are not written."""
+    return _move("moe_dispatch", _lib.moe_dispatch, x, "x", False, routing, k, E, topk_w, out, "out", stream)
+
+
+def moe_combine(y, routing, k, E, topk_w=None, out=None, stream=None):
+    """Rows y [T * k][H] in expert order back to token order: out [T][H], the
+    (weighted) sum of each token's valid pairs."""
+    return _move("moe_combine", _lib.moe_combine, y, "y", True, routing, k, E, topk_w, out, "out", stream)
+
+
+def _move_grad(name, fn, grad, grad_name, sorted_grad, other, other_name, routing, k, E, topk_w, out, out_name, dw, stream):
+    if dw is not None and other is None:
+        raise ValueError(f"{name}: dtopk_w needs {other_name}")
+    if other is not None and topk_w is None:
+        raise ValueError(f"{name}: the gradient of topk_w needs topk_w")
+    kind = _row_type(grad_name, grad)
+    T, H = _rows(grad_name, grad, k, sorted_grad)
+    shape = (T, H) if sorted_grad else (T * k, H)
+    if out is None:
+        out = _empty(shape, grad.dtype, grad.device, stream)
+    if other is not None and dw is None:
+        dw = _empty((T, k), torch.float32, grad.device, stream)
+    _check_tensor(grad_name, grad, grad.dtype, grad.shape)
+    _check_tensor(out_name, out, grad.dtype, shape)
+    if topk_w is not None:
+        _check_tensor("topk_w", topk_w, torch.float32, (T, k))
+    if other is not None:
+        _check_tensor(other_name, other, grad.dtype, shape)
+        _check_tensor("dtopk_w", dw, torch.float32, (T, k))
+    _check_device(**{grad_name: grad, out_name: out, other_name: other}, topk_w=topk_w, dtopk_w=dw, routing=routing)
+    _check(name, fn(_ptr(grad), _ptr(other), kind, _ptr(topk_w), _ptr(routing),
+                    routing.numel() * routing.element_size(), T, k, E, H, _ptr(out), _ptr(dw), _stream(stream)))
+    return out if dw is None else (out, dw)
+
+
+def moe_dispatch_grad(dxs, routing, k, E, x=None, topk_w=None, dx=None, dtopk_w=None, stream=None):
+    """Gradient of moe_dispatch: dx [T][H] from dxs [T * k][H] (topk_w as in the
+    forward call); with the forward's x also the weights' gradient: (dx, dtopk_w)."""
+    return _move_grad("moe_dispatch_grad", _lib.moe_dispatch_grad, dxs, "dxs", True, x, "x", routing, k, E, topk_w, dx,
+                      "dx", dtopk_w, stream)
+
+
+def moe_combine_grad(dout, routing, k, E, y=None, topk_w=None, dy=None, dtopk_w=None, stream=None):
+    """Gradient of moe_combine: dy [T * k][H] from dout [T][H] (topk_w as in the
+    forward call; rows behind the last valid pair are not written); with the
+    forward's y also the weights' gradient: (dy, dtopk_w)."""
+    return _move_grad("moe_combine_grad", _lib.moe_combine_grad, dout, "dout", False, y, "y", routing, k, E, topk_w, dy,
+                      "dy", dtopk_w, stream)
+
+
+def moe_router_topk_grad(logits, topk_ids, topk_w, dtopk_w, renormalize=True, n_shared=0, dlogits=None, stream=None):
+    """Gradient of moe_router_topk's scores, fp32 [T][E], from that of its
+    weights (topk_ids, topk_w, dtopk_w: [T][k + n_shared])."""
+    if logits.dim() != 2 or topk_ids.dim() != 2:
+        raise ValueError("logits must be [T][E], topk_ids [T][k + n_shared]")
+    T, E = logits.shape
+    ncol = topk_ids.shape[1]
+    if dlogits is None:
+        dlogits = _empty((T, E), torch.float32, logits.device, stream)
+    _check_tensor("logits", logits, torch.float32, (T, E))
+    _check_tensor("topk_ids", topk_ids, torch.int32, (T, ncol))
+    _check_tensor("topk_w", topk_w, torch.float32, (T, ncol))
+    _check_tensor("dtopk_w", dtopk_w, torch.float32, (T, ncol))
+    _check_tensor("dlogits", dlogits, torch.float32, (T, E))
+    _check_device(logits=logits, topk_ids=topk_ids, topk_w=topk_w, dtopk_w=dtopk_w, dlogits=dlogits)
+    _check("moe_router_topk_grad", _lib.moe_router_topk_grad(
+        _ptr(logits), _ptr(topk_ids), _ptr(topk_w), _ptr(dtopk_w), T, E, ncol - n_shared, int(bool(renormalize)),
+        n_shared, _ptr(dlogits), _stream(stream)))
+    return dlogits
+
+
 def moe_set_stage_events(events):
     """events: list of 10 entries, each a torch.cuda.Event(enable_timing=True)
     (already recorded once) or None (stage s is recorded when entries 2s and
@@ -728,7 +991,7 @@ def moe_tile_copy_read(pattern, buf, row_bytes, reps, sink, stream=None):
 def moe_layer(x, topk_ids, topk_w, weights, dtype="bf16", out=None, stream=None):
     """Routing + forward with freshly allocated routing buffer and workspace.
 
-    weights: {"w1", "w2"} (bf16) or {"w1", "w1_scale", "w2", "w2_scale"} (fp8),
+    weights: {"w1", "w2"} (bf16, mxfp4) or {"w1", "w1_scale", "w2", "w2_scale"} (fp8),
     with w1/w2 already packed (pack_weights).  Returns (out, routing, workspace)."""
     T, H = x.shape
     k = topk_ids.shape[1]
@@ -741,6 +1004,8 @@ def moe_layer(x, topk_ids, topk_w, weights, dtype="bf16", out=None, stream=None)
     build_routing(topk_ids, E, H, I, routing, dtype, stream)
     if dtype == "bf16":
         moe_forward_bf16(x, topk_w, routing, weights["w1"], weights["w2"], ws, out, stream)
+    elif dtype == "mxfp4":
+        moe_forward_mxfp4(x, topk_w, routing, weights["w1"], weights["w2"], ws, out, stream)
     else:
         fwd = {"fp8": moe_forward_fp8, "mxfp8": moe_forward_mxfp8, "int8": moe_forward_int8,
                "int4": moe_forward_int4, "fp8b": moe_forward_fp8_block,

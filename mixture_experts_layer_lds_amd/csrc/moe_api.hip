@@ -12,6 +12,7 @@
 
 #include "moe_common.h"
 #include "decode_route.h"
+#include "mx4.h"
 
 // Workspace of moe_forward_fp8_noalloc: one array per GPU, held until the
 // process ends.  In host code its name is only a stand-in for the device
@@ -64,7 +65,7 @@ size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 bool known_dtype(int dtype) {
   return dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_FP8_W8A8 || dtype == MOE_DTYPE_MXFP8 ||
          dtype == MOE_DTYPE_INT8_W8A8 || dtype == MOE_DTYPE_INT4_W4A16 ||
-         dtype == MOE_DTYPE_FP8_BLOCK || dtype == MOE_DTYPE_INT8_W8A16;
+         dtype == MOE_DTYPE_FP8_BLOCK || dtype == MOE_DTYPE_INT8_W8A16 || dtype == MOE_DTYPE_MXFP4;
 }
 
 int check_shape(int T, int k, int E, int H, int I, int dtype = MOE_DTYPE_BF16) {
@@ -72,7 +73,8 @@ int check_shape(int T, int k, int E, int H, int I, int dtype = MOE_DTYPE_BF16) {
     return MOE_ERR_INVALID_ARG;
   if (H % 64 || I % 64 || H > 65536 || I > 65536) return MOE_ERR_UNSUPPORTED_SHAPE;
   // MX: both reductions in whole 128-value units of the scaled instruction
-  if ((dtype == MOE_DTYPE_MXFP8 || dtype == MOE_DTYPE_INT4_W4A16 || dtype == MOE_DTYPE_FP8_BLOCK) &&
+  if ((dtype == MOE_DTYPE_MXFP8 || dtype == MOE_DTYPE_INT4_W4A16 || dtype == MOE_DTYPE_FP8_BLOCK ||
+       dtype == MOE_DTYPE_MXFP4) &&
       (H % 128 || I % 128))
     return MOE_ERR_UNSUPPORTED_SHAPE;   // whole 128-value units / scale groups
   if ((long)T * k > moe::kMaxPairs) return MOE_ERR_UNSUPPORTED_SHAPE;
@@ -190,8 +192,44 @@ long expected_active(int T, int k, int E) {
   return ex < 1 ? 1 : ex;
 }
 
+// Waves per workgroup of the MXFP4 streaming kernel: the count that minimises
+// (items per workgroup slot) x (groups per wave + 1, the first loads' latency).
+int pick_mx4_waves(int groups, long items) {
+  int best = 1;
+  long best_cost = -1;
+  for (int w = 1; w <= 8 && w <= groups; w *= 2) {
+    long grid = kStreamWaves / w;
+    if (items < grid) grid = items;
+    if (grid < 1) grid = 1;
+    const long cost = (items + grid - 1) / grid * ((groups + w - 1) / w + 1);
+    if (best_cost < 0 || cost < best_cost) best = w, best_cost = cost;
+  }
+  return best;
+}
+
+// MXFP4: register streaming on 16- or 32-row tiles up to 16 mean rows per
+// expert, strips above, tiles of about twice the mean rows (as the one-byte
+// dtypes) so that the usual spread of a routing still fits one tile.
+void plan_mx4(int T, int k, int E, int H, int I, Plan* p) {
+  const long P = (long)T * k, active = std::min(P, (long)E);
+  const long avg = active > 0 ? (P + active - 1) / active : 1;
+  p->tiling = avg <= 16 ? kStreaming : kStrips;
+  p->mb = avg <= 8 ? 1 : (avg <= 16 ? 2 : (avg <= 40 ? 4 : (avg <= 96 ? 8 : 12)));
+  p->block_m = 16 * p->mb;
+  p->max_tasks = (int)(P / p->block_m + active);
+  if (p->tiling == kStrips) return;
+  auto tasks = [&](long experts) { return std::max((P + p->block_m - 1) / p->block_m, experts); };
+  p->sw1 = pick_mx4_waves(H / 128 / moe::mx4_group(H), tasks(active) * (I / 32));
+  p->sw2 = pick_mx4_waves(I / 128 / moe::mx4_group(I), tasks(std::min(active, expected_active(T, k, E))) * (H / 64));
+  p->dr_waves = T == 1 ? 8 : 0;
+}
+
 Plan make_plan(int dtype, int T, int k, int E, int H, int I) {
   Plan p;
+  if (dtype == MOE_DTYPE_MXFP4) {
+    plan_mx4(T, k, E, H, I, &p);
+    return p;
+  }
   const long P = (long)T * k;
   const long active = P < E ? P : E;
   // The down GEMM's wave split is chosen for the expected number of active
@@ -526,6 +564,17 @@ void workspace_layout(int dtype, int T, int k, int H, int I, const Plan& p,
     W->tiling = p.tiling;
     return;
   }
+  if (dtype == MOE_DTYPE_MXFP4) {   // e2m1 codes + e8m0 codes per 32 values; h in the product's blocks
+    W->xq = take((size_t)T * H / 2);
+    W->x_scale = take((size_t)T * H / 32);
+    W->x_scale_rows = W->g = W->h_scale = kNone;
+    W->h = take((size_t)p.max_tasks * p.mb * (I / 128) * moe::kMx4Unit);
+    W->y = p.dr_waves ? kNone : take(2 * P * H);   // one token: the down launch adds the top-k rows itself
+    W->total_bytes = off;
+    W->split_k1 = W->split_k2 = 1;
+    W->tiling = p.tiling;
+    return;
+  }
   if (dtype == MOE_DTYPE_MXFP8) {   // e4m3 codes + e8m0 codes per 32 values
     const int s2 = p.tiling == kStrips ? p.split2 : 1;
     W->xq = take((size_t)T * H);
@@ -848,6 +897,84 @@ int forward_mx(const void* x, const float* topk_w, const void* routing, const vo
     StageScope st(s, 4);
     e = moe_host::launch_reduce(ws + W.y, true, 1, P, topk_w, R.pair_pos, R.expert_offsets, nullptr,
                                 E, T, k, H, static_cast<uint16_t*>(out), s);
+    if (e != hipSuccess) return MOE_ERR_HIP;
+  }
+  return MOE_OK;
+}
+
+// MXFP4 forward: x to MXFP4, gate-up whose epilogue writes SiLU(gate) * up
+// as MXFP4 blocks, down (bf16 rows, or with one token the weighted sum),
+// top-k reduction.
+int forward_mx4(const void* x, const float* topk_w, const void* routing, const void* w1, const void* w2, int T, int k,
+                int E, int H, int I, void* workspace, size_t workspace_bytes, void* out, void* stream,
+                const moe_host::DecodeRouteOut* fold = nullptr) {
+  int rc = check_shape(T, k, E, H, I, MOE_DTYPE_MXFP4);
+  if (rc != MOE_OK) return rc;
+  if (T == 0) return MOE_OK;
+  if (!x || !topk_w || !routing || !w1 || !w2 || !workspace || !out) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(w1, 16) || !aligned(w2, 16) || !aligned(out, 16) || !aligned(topk_w, 4) ||
+      !aligned(routing, 16) || !aligned(workspace, 256))
+    return MOE_ERR_INVALID_ARG;
+  const Plan p = make_plan(MOE_DTYPE_MXFP4, T, k, E, H, I);
+  moe_routing_layout_t L;
+  routing_layout(T, k, E, p, &L);
+  moe_workspace_layout_t W;
+  workspace_layout(MOE_DTYPE_MXFP4, T, k, H, I, p, &W);
+  if (workspace_bytes < W.total_bytes) return MOE_ERR_BUFFER_TOO_SMALL;
+  int cus = 0;
+  if ((rc = cu_count(&cus)) != MOE_OK) return rc;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const RoutingView R = view_routing(routing, L);
+  char* ws = static_cast<char*>(workspace);
+  const int P = T * k;
+  uint8_t* xq = reinterpret_cast<uint8_t*>(ws + W.xq);
+  uint8_t* sx = reinterpret_cast<uint8_t*>(ws + W.x_scale);
+  hipError_t e;
+  {
+    StageScope st(s, 0);
+    e = moe_host::launch_mx4_quant_x(static_cast<const uint16_t*>(x), T, H, xq, sx, s, fold, P);
+    if (e != hipSuccess) return MOE_ERR_HIP;
+  }
+  moe_host::Mx4Args a{};
+  a.sorted_pairs = R.sorted_pairs;
+  a.header = R.header;
+  a.tasks = R.tasks;
+  a.topk = k;
+  a.max_tasks = p.max_tasks;
+  a.topk_w = topk_w;
+  {
+    StageScope st(s, 1);
+    a.a = xq;
+    a.a_sc = sx;
+    a.b = w1;
+    a.c = ws + W.h;
+    a.K = H;
+    a.N_out = I;
+    a.w_rows = 2 * I;
+    e = p.tiling == kStrips ? moe_host::launch_mx4_strip(a, true, p.mb, cus, s)
+                            : moe_host::launch_mx4_stream(a, true, p.mb, p.sw1,
+                                                          stream_grid((long)p.max_tasks * (I / 32), p.sw1, cus), s);
+    if (e != hipSuccess) return MOE_ERR_HIP;
+  }
+  {
+    StageScope st(s, 3);
+    a.a = ws + W.h;
+    a.a_sc = nullptr;
+    a.b = w2;
+    a.c = p.dr_waves ? out : ws + W.y;
+    a.K = I;
+    a.N_out = H;
+    a.w_rows = H;
+    if (p.tiling == kStrips) e = moe_host::launch_mx4_strip(a, false, p.mb, cus, s);
+    else if (p.dr_waves) e = moe_host::launch_mx4_down_reduce(a, s);
+    else e = moe_host::launch_mx4_stream(a, false, p.mb, p.sw2,
+                                         stream_grid((long)p.max_tasks * (H / 64), p.sw2, cus), s);
+    if (e != hipSuccess) return MOE_ERR_HIP;
+  }
+  if (!p.dr_waves) {
+    StageScope st(s, 4);
+    e = moe_host::launch_reduce(ws + W.y, true, 1, P, topk_w, R.pair_pos, R.expert_offsets, nullptr, E, T, k, H,
+                                static_cast<uint16_t*>(out), s);
     if (e != hipSuccess) return MOE_ERR_HIP;
   }
   return MOE_OK;
@@ -1262,7 +1389,8 @@ int check_forward_args(int dtype, const void* x, const float* topk_w, const void
   const bool generic = dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_FP8_W8A8;
   const int rc = generic ? check_shape(T, k, E, H, I) : check_shape(T, k, E, H, I, dtype);
   if (rc != MOE_OK || T == 0) return rc;
-  const bool scaled = dtype != MOE_DTYPE_BF16;   // per-channel, block or MX scales
+  // per-channel, block or MX scales (MXFP4: inside the packed weights)
+  const bool scaled = dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_MXFP4;
   if (!x || !topk_w || !routing || !w1 || !w2 || !workspace || !out) return MOE_ERR_INVALID_ARG;
   if (scaled && (!w1_scale || !w2_scale)) return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(w1, 16) || !aligned(w2, 16) || !aligned(out, 16) ||
@@ -1558,6 +1686,8 @@ int route_forward(int dtype, const int32_t* ids, const void* x, const float* top
         return forward_mx(x, topk_w, routing, w1, static_cast<const uint8_t*>(w1_scale), w2,
                           static_cast<const uint8_t*>(w2_scale), T, k, E, H, I, workspace, workspace_bytes,
                           out, stream, f);
+      case MOE_DTYPE_MXFP4:
+        return forward_mx4(x, topk_w, routing, w1, w2, T, k, E, H, I, workspace, workspace_bytes, out, stream, f);
       case MOE_DTYPE_INT4_W4A16:
       case MOE_DTYPE_INT8_W8A16:
         return forward_w4(dtype, x, topk_w, routing, w1, s1, w2, s2, T, k, E, H, I, workspace, workspace_bytes,
@@ -1595,12 +1725,48 @@ int route_forward(int dtype, const int32_t* ids, const void* x, const float* top
 int packed_shape(const void* packed, int E, int rows, int cols, int dtype, long* row_bytes) {
   if (!known_dtype(dtype)) return MOE_ERR_INVALID_ARG;
   if (E < 1 || rows < 1 || cols < 1) return MOE_ERR_INVALID_ARG;
+  if (dtype == MOE_DTYPE_MXFP4) {   // whole 32-row groups and 128-value units, codes and scale codes
+    if (rows % 32 || cols % 128 || rows > 2 * 65536 || cols > 65536) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (!packed || !aligned(packed, 16)) return MOE_ERR_INVALID_ARG;
+    *row_bytes = (long)cols / 32 * 17;
+    return MOE_OK;
+  }
   const long rb = dtype == MOE_DTYPE_INT4_W4A16 ? (long)cols / 2
                                                 : (long)cols * (dtype == MOE_DTYPE_BF16 ? 2 : 1);
   if (dtype == MOE_DTYPE_INT4_W4A16 && cols % 2) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (rows % 16 || rb % 64 || rows > 2 * 65536 || cols > 65536) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!packed || !aligned(packed, 16)) return MOE_ERR_INVALID_ARG;
   *row_bytes = rb;
+  return MOE_OK;
+}
+
+// Element bytes of a moe_row_type_t, 0 for any other value.
+int row_bytes_of(int row_type) {
+  return row_type == MOE_ROW_BF16 || row_type == MOE_ROW_FP16 ? 2 : (row_type == MOE_ROW_FP32 ? 4 : 0);
+}
+
+// Sizes and the routing buffer of a row operator, and its arguments from
+// them; *done: nothing to do (T == 0).
+int check_rows(int row_type, const void* routing, size_t routing_bytes, int T, int k, int E, int H,
+               moe_host::RowMoveArgs* a, bool* done) {
+  if (T < 0 || k < 1 || k > moe::kMaxTopK || E < 1 || E > moe::kMaxExperts || H <= 0 || !row_bytes_of(row_type))
+    return MOE_ERR_INVALID_ARG;
+  if (H % 8 || H > 65536 || (long)T * k > moe::kMaxPairs) return MOE_ERR_UNSUPPORTED_SHAPE;
+  *done = T == 0;
+  if (T == 0) return MOE_OK;
+  if (!routing || !aligned(routing, 16)) return MOE_ERR_INVALID_ARG;
+  // the parts up to the task map, which do not depend on the tile height
+  moe_routing_layout_t L;
+  routing_layout(T, k, E, Plan{}, &L);
+  if (routing_bytes < L.tasks) return MOE_ERR_BUFFER_TOO_SMALL;
+  const RoutingView R = view_routing(routing, L);
+  *a = moe_host::RowMoveArgs{};
+  a->pair_pos = R.pair_pos;
+  a->expert_offsets = R.expert_offsets;
+  a->T = T;
+  a->k = k;
+  a->E = E;
+  a->H = H;
   return MOE_OK;
 }
 
@@ -1648,7 +1814,7 @@ int moe_workspace_layout(int T, int k, int E, int H, int I, int dtype, moe_works
 
 int moe_pack_weights(const void* w, int E, int rows, int cols, int dtype, void* packed,
                      moe_packed_weights_t* desc, void* stream) {
-  if (!desc) return MOE_ERR_INVALID_ARG;
+  if (!desc || dtype == MOE_DTYPE_MXFP4) return MOE_ERR_INVALID_ARG;   // MXFP4: moe_pack_weights_mxfp4
   long row_bytes = 0;
   const int rc = packed_shape(packed, E, rows, cols, dtype, &row_bytes);
   if (rc != MOE_OK) return rc;
@@ -1792,6 +1958,156 @@ int moe_forward_mxfp8(const void* x, const float* topk_w, const void* routing, c
   if (rc != MOE_OK || T == 0) return rc;
   return forward_mx(x, topk_w, routing, packed_data(w1), w1_scale, packed_data(w2), w2_scale, T, k, E, H, I, workspace,
                     workspace_bytes, out, stream);
+}
+
+int moe_quantize_mxfp4(const void* x, int row_type, int64_t rows, int cols, int64_t row_stride, uint8_t* codes,
+                       uint8_t* scales, void* stream) {
+  const int esz = row_bytes_of(row_type);
+  if (!esz || rows < 0 || cols <= 0 || row_stride < cols) return MOE_ERR_INVALID_ARG;
+  if (cols % 32 || row_stride > (int64_t)1 << 40 || (row_stride * esz) % 16 || rows > (int64_t)1 << 40)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (rows == 0) return MOE_OK;
+  if (!x || !codes || !scales || !aligned(x, 16) || !aligned(codes, 4)) return MOE_ERR_INVALID_ARG;
+  const hipError_t e = moe_host::launch_mx4_quantize(x, row_type, (size_t)rows, cols, (size_t)row_stride, codes,
+                                                     scales, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols, int row_type, void* out,
+                         void* stream) {
+  if (!row_bytes_of(row_type) || rows < 0 || cols <= 0) return MOE_ERR_INVALID_ARG;
+  if (cols % 32 || rows > (int64_t)1 << 40) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (rows == 0) return MOE_OK;
+  if (!codes || !scales || !out || !aligned(codes, 4) || !aligned(out, 16)) return MOE_ERR_INVALID_ARG;
+  const hipError_t e = moe_host::launch_mx4_dequantize(codes, scales, (size_t)rows, cols, row_type, out,
+                                                       static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int moe_pack_weights_mxfp4(const uint8_t* codes, const uint8_t* scales, int E, int rows, int cols, void* packed,
+                           moe_packed_weights_t* desc, void* stream) {
+  if (!desc) return MOE_ERR_INVALID_ARG;
+  long row_bytes = 0;
+  const int rc = packed_shape(packed, E, rows, cols, MOE_DTYPE_MXFP4, &row_bytes);
+  if (rc != MOE_OK) return rc;
+  if (!codes || !scales || !aligned(codes, 16)) return MOE_ERR_INVALID_ARG;
+  const char* out = static_cast<const char*>(packed);
+  const size_t n = (size_t)E * rows;
+  auto overlaps = [&](const uint8_t* p, size_t bytes) {
+    const char* q = reinterpret_cast<const char*>(p);
+    return q < out + n * row_bytes && out < q + bytes;
+  };
+  if (overlaps(codes, n * (cols / 2)) || overlaps(scales, n * (cols / 32))) return MOE_ERR_INVALID_ARG;
+  const hipError_t e = moe_host::launch_mx4_pack(codes, scales, E, rows, cols, packed, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return MOE_ERR_HIP;
+  describe(packed, E, rows, cols, MOE_DTYPE_MXFP4, desc);
+  return MOE_OK;
+}
+
+int moe_build_routing_mxfp4(const int32_t* topk_ids, int T, int k, int E, int H, int I, void* routing,
+                            size_t routing_bytes, void* stream) {
+  return build_routing(MOE_DTYPE_MXFP4, topk_ids, T, k, E, H, I, routing, routing_bytes, stream);
+}
+
+int moe_forward_mxfp4(const void* x, const float* topk_w, const void* routing, const moe_packed_weights_t* w1,
+                      const moe_packed_weights_t* w2, int T, int k, int E, int H, int I, void* workspace,
+                      size_t workspace_bytes, void* out, void* stream) {
+  const int rc = check_packed(MOE_DTYPE_MXFP4, w1, w2, T, k, E, H, I);
+  if (rc != MOE_OK || T == 0) return rc;
+  return forward_mx4(x, topk_w, routing, packed_data(w1), packed_data(w2), T, k, E, H, I, workspace, workspace_bytes,
+                     out, stream);
+}
+
+int moe_route_forward_mxfp4(const int32_t* topk_ids, const void* x, const float* topk_w, void* routing,
+                            size_t routing_bytes, const moe_packed_weights_t* w1, const moe_packed_weights_t* w2,
+                            int T, int k, int E, int H, int I, void* workspace, size_t workspace_bytes, void* out,
+                            void* stream) {
+  const int rc = check_packed(MOE_DTYPE_MXFP4, w1, w2, T, k, E, H, I);
+  if (rc != MOE_OK || T == 0) return rc;
+  return route_forward(MOE_DTYPE_MXFP4, topk_ids, x, topk_w, routing, routing_bytes, packed_data(w1), nullptr,
+                       packed_data(w2), nullptr, T, k, E, H, I, workspace, workspace_bytes, out, stream);
+}
+
+int moe_dispatch(const void* x, int row_type, const float* topk_w, const void* routing, size_t routing_bytes, int T,
+                 int k, int E, int H, void* xs, void* stream) {
+  moe_host::RowMoveArgs a;
+  bool done;
+  const int rc = check_rows(row_type, routing, routing_bytes, T, k, E, H, &a, &done);
+  if (rc != MOE_OK || done) return rc;
+  if (!x || !xs || !aligned(x, 16) || !aligned(xs, 16) || !aligned(topk_w, 4)) return MOE_ERR_INVALID_ARG;
+  a.tokens = x;
+  a.w = topk_w;
+  a.out = xs;
+  const hipError_t e = moe_host::launch_rows_to_experts(a, row_type, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int moe_combine(const void* y, int row_type, const float* topk_w, const void* routing, size_t routing_bytes, int T,
+                int k, int E, int H, void* out, void* stream) {
+  moe_host::RowMoveArgs a;
+  bool done;
+  const int rc = check_rows(row_type, routing, routing_bytes, T, k, E, H, &a, &done);
+  if (rc != MOE_OK || done) return rc;
+  if (!y || !out || !aligned(y, 16) || !aligned(out, 16) || !aligned(topk_w, 4)) return MOE_ERR_INVALID_ARG;
+  a.rows = y;
+  a.w = topk_w;
+  a.out = out;
+  const hipError_t e = moe_host::launch_rows_to_tokens(a, row_type, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int moe_dispatch_grad(const void* dxs, const void* x, int row_type, const float* topk_w, const void* routing,
+                      size_t routing_bytes, int T, int k, int E, int H, void* dx, float* dtopk_w, void* stream) {
+  if (!dtopk_w) return moe_combine(dxs, row_type, topk_w, routing, routing_bytes, T, k, E, H, dx, stream);
+  moe_host::RowMoveArgs a;
+  bool done;
+  const int rc = check_rows(row_type, routing, routing_bytes, T, k, E, H, &a, &done);
+  if (rc != MOE_OK || done) return rc;
+  if (!dxs || !x || !dx || !topk_w || !aligned(dxs, 16) || !aligned(x, 16) || !aligned(dx, 16) ||
+      !aligned(topk_w, 4) || !aligned(dtopk_w, 4))
+    return MOE_ERR_INVALID_ARG;
+  a.tokens = x;
+  a.rows = dxs;
+  a.w = topk_w;
+  a.out = dx;
+  a.dw = dtopk_w;
+  const hipError_t e = moe_host::launch_rows_grad(a, true, row_type, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int moe_combine_grad(const void* dout, const void* y, int row_type, const float* topk_w, const void* routing,
+                     size_t routing_bytes, int T, int k, int E, int H, void* dy, float* dtopk_w, void* stream) {
+  if (!dtopk_w) return moe_dispatch(dout, row_type, topk_w, routing, routing_bytes, T, k, E, H, dy, stream);
+  moe_host::RowMoveArgs a;
+  bool done;
+  const int rc = check_rows(row_type, routing, routing_bytes, T, k, E, H, &a, &done);
+  if (rc != MOE_OK || done) return rc;
+  if (!dout || !y || !dy || !topk_w || !aligned(dout, 16) || !aligned(y, 16) || !aligned(dy, 16) ||
+      !aligned(topk_w, 4) || !aligned(dtopk_w, 4))
+    return MOE_ERR_INVALID_ARG;
+  a.tokens = dout;
+  a.rows = y;
+  a.w = topk_w;
+  a.out = dy;
+  a.dw = dtopk_w;
+  const hipError_t e = moe_host::launch_rows_grad(a, false, row_type, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int moe_router_topk_grad(const float* logits, const int32_t* topk_ids, const float* topk_w, const float* dtopk_w,
+                         int T, int E, int k, int renormalize, int n_shared, float* dlogits, void* stream) {
+  if (T < 0 || E < 1 || k < 1 || k > E || n_shared < 0 || (renormalize != 0 && renormalize != 1))
+    return MOE_ERR_INVALID_ARG;
+  if (E > moe_host::router_max_experts() || k + n_shared > moe::kMaxTopK || E + n_shared > moe::kMaxExperts)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0) return MOE_OK;
+  if (!topk_ids || !topk_w || !dtopk_w || !dlogits || (!renormalize && !logits)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) || !aligned(dtopk_w, 4) ||
+      !aligned(dlogits, 4))
+    return MOE_ERR_INVALID_ARG;
+  const hipError_t e = moe_host::launch_router_topk_grad(logits, topk_ids, topk_w, dtopk_w, T, E, k, renormalize != 0,
+                                                         n_shared, dlogits, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 int moe_build_routing_fp8_block(const int32_t* topk_ids, int T, int k, int E, int H, int I,

@@ -414,6 +414,62 @@ size_t tile_copy_bytes(int cus, int row_bytes);
 hipError_t launch_tile_copy(int pattern, const void* buf, int row_bytes, int reps, uint32_t* sink, int cus,
                             hipStream_t s);
 
+// MXFP4 (mx4.hip; the format and the packed layout are in mx4.h): rows of
+// moe_row_type_t to codes and scale codes and back; bf16 token rows as the
+// layer reads them (with route, at most 64 pairs, the launch also does the
+// routing build); row-major weights to packed blocks.
+hipError_t launch_mx4_quantize(const void* x, int row_type, size_t rows, int cols, size_t row_stride, uint8_t* codes,
+                               uint8_t* scales, hipStream_t s);
+hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, size_t rows, int cols, int row_type,
+                                 void* out, hipStream_t s);
+hipError_t launch_mx4_quant_x(const uint16_t* x, int T, int H, uint8_t* xq, uint8_t* sx, hipStream_t s,
+                              const DecodeRouteOut* route = nullptr, int P = 0);
+hipError_t launch_mx4_pack(const uint8_t* codes, const uint8_t* scales, int E, int rows, int cols, void* packed,
+                           hipStream_t s);
+
+// MXFP4 grouped GEMMs (mx4_gemm.hip: register streaming; mx4_strip.hip:
+// token rows in LDS).
+struct Mx4Args {
+  const void* a;                // gate-up: codes of the token rows [T][K/2]; down: the gate-up's output blocks
+  const uint8_t* a_sc;          // gate-up: their scale codes [T][K/128/G][4][G]
+  const void* b;                // packed weights, w_rows rows per expert
+  const int32_t* sorted_pairs;
+  const int32_t* header;
+  const moe_task_t* tasks;
+  void* c;                      // gate-up: SiLU(gate) * up as blocks of 16 rows x G units, mb blocks a task;
+                                // down: bf16 rows [P][N_out]
+  int K;                        // reduction length
+  int N_out;                    // output columns (I for gate-up, H for down)
+  int w_rows;                   // weight rows per expert (2I or H)
+  int topk;
+  int max_tasks;
+  const float* topk_w;          // one token, down: the routing weights
+};
+// (mb, waves) = 16-row blocks per tile (1 or 2), waves per workgroup (1, 2, 4, 8)
+hipError_t launch_mx4_stream(const Mx4Args& a, bool gateup, int mb, int waves, int grid, hipStream_t s);
+// One token: down GEMM and top-k weighted sum, out (bf16 [H]) in a.c.
+hipError_t launch_mx4_down_reduce(const Mx4Args& a, hipStream_t s);
+// mb in {4, 8, 12}
+hipError_t launch_mx4_strip(const Mx4Args& a, bool gateup, int mb, int grid, hipStream_t s);
+
+// Rows between token and expert order (rows.hip).
+struct RowMoveArgs {
+  const void* tokens;             // [T][H]
+  const void* rows;               // [T * k][H], expert order
+  const float* w;                 // [T][k], or null: 1
+  const int32_t* pair_pos;
+  const int32_t* expert_offsets;
+  void* out;                      // token rows or expert rows
+  float* dw;                      // [T][k]
+  int T, k, E, H;
+};
+hipError_t launch_rows_to_experts(const RowMoveArgs& a, int row_type, hipStream_t s);
+hipError_t launch_rows_to_tokens(const RowMoveArgs& a, int row_type, hipStream_t s);
+hipError_t launch_rows_grad(const RowMoveArgs& a, bool to_tokens, int row_type, hipStream_t s);
+// The router's gradient (rows.hip).
+hipError_t launch_router_topk_grad(const float* logits, const int32_t* ids, const float* w, const float* dw, int T,
+                                   int E, int k, bool renorm, int n_shared, float* dl, hipStream_t s);
+
 // fp32 rows -> e4m3 codes with the row amax held in h_scale (replaced by the scale).
 hipError_t launch_requant_rows(const float* h32, int P, int I, const int32_t* expert_offsets,
                                int E, uint8_t* hq, float* h_scale, bool find_amax, hipStream_t s);

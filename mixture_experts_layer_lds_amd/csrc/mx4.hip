@@ -1,0 +1,179 @@
+// MXFP4 quantisation of rows, its inverse, and the one-time weight pre-pack
+// (SGLang tuning guide, block shapes: gfx95 devices keep MX's [1, 32]
+// blocks; the format and its rounding are in mx4.h).
+//
+// Quantisation: four lanes a block, eight values each, so that a wave reads
+// 64 consecutive runs of eight values and writes 256 consecutive bytes of
+// codes; the block's largest magnitude crosses the four lanes in two
+// exchanges.  Every value is read once and nothing is kept, so the kernel is
+// bound by its reads and writes.
+#include "decode_route.h"
+#include "mx4.h"
+#include "rows.h"
+
+namespace moe {
+
+constexpr int kMx4Threads = 256;
+
+// Eight values -> the lane's four code bytes and the block's scale code.
+__device__ __forceinline__ uint32_t mx4_quant8(const float (&v)[8], uint32_t& code) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; i++) m = max(m, abs_bits(v[i]));
+  m = max(m, (uint32_t)__shfl_xor((int)m, 1, 64));
+  m = max(m, (uint32_t)__shfl_xor((int)m, 2, 64));
+  code = mx4_scale_code(m);
+  return mx4_encode8(v, code);
+}
+
+// rows x cols values (row_stride elements apart) -> codes [rows][cols/2] and
+// scale codes [rows][cols/32], row-major.  nvec = rows * cols / 8.
+template <typename R>
+__global__ void __launch_bounds__(kMx4Threads)
+mx4_quantize_kernel(const typename R::elem* __restrict__ x, size_t nvec, uint32_t vec_per_row, size_t row_stride,
+                    uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  const bool flat = row_stride == (size_t)vec_per_row * 8;
+  for (size_t i = (size_t)blockIdx.x * kMx4Threads + threadIdx.x; i < nvec; i += (size_t)gridDim.x * kMx4Threads) {
+    size_t at = i * 8;
+    if (!flat) {
+      const size_t row = i / vec_per_row;
+      at = row * row_stride + (i - row * vec_per_row) * 8;
+    }
+    float v[8];
+    R::load8(x + at, v);
+    uint32_t code;
+    codes[i] = mx4_quant8(v, code);
+    if ((threadIdx.x & 3) == 0) scales[i / 4] = (uint8_t)code;
+  }
+}
+
+// codes and scale codes -> values, eight a thread.
+template <typename R>
+__global__ void __launch_bounds__(kMx4Threads)
+mx4_dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales, size_t nvec,
+                      typename R::elem* __restrict__ out) {
+  for (size_t i = (size_t)blockIdx.x * kMx4Threads + threadIdx.x; i < nvec; i += (size_t)gridDim.x * kMx4Threads) {
+    const uint32_t c = codes[i], s = scales[i / 4];
+    const float sc = mx4_scale_value(s);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      const uint32_t n = (c >> (4 * j)) & 15u, m = n & 7u;
+      // magnitudes 0, 1/2, 1, 3/2, 2, 3, 4, 6 as floats, from the code's exponent and mantissa bits
+      const float mag = m < 2 ? 0.5f * (float)m : __uint_as_float(((126u + (m >> 1)) << 23) | ((m & 1u) << 22));
+      const float a = s == 255u ? __uint_as_float(0x7fc00000u) : mag * sc;
+      v[j] = n & 8u ? -a : a;
+    }
+    R::store8(out + i * 8, v);
+  }
+}
+
+// x [T][H] bf16 -> codes [T][H/2] row-major, scale codes [T][H/128/G][4][G]
+// (a lane of the product takes the G codes of its 32-value column in one
+// load).  ROUTE (at most 64 pairs): workgroup 0 also does the routing build.
+template <bool ROUTE>
+__global__ void __launch_bounds__(kMx4Threads)
+mx4_quant_x_kernel(const uint16_t* __restrict__ x, uint32_t nvec, uint32_t vec_per_row, int G,
+                   uint32_t* __restrict__ xq, uint8_t* __restrict__ sx, moe_host::DecodeRouteOut route, int P) {
+  if constexpr (ROUTE) {
+    if (blockIdx.x == 0) {
+      const int lane = threadIdx.x & 63;
+      const DecodeRoute rt = decode_route(route.ids, P, route.E, route.block_m, lane);
+      decode_route_write(rt, route, P, threadIdx.x, kMx4Threads, lane, threadIdx.x >> 6);
+    }
+  }
+  const uint32_t i = blockIdx.x * kMx4Threads + threadIdx.x;
+  if (i >= nvec) return;   // whole waves of four-lane blocks: nvec % 16 == 0
+  float v[8];
+  RowBf16::load8(x + (size_t)i * 8, v);
+  uint32_t code;
+  xq[i] = mx4_quant8(v, code);
+  if ((threadIdx.x & 3) == 0) {
+    const uint32_t row = i / vec_per_row, b = (i - row * vec_per_row) / 4;   // block of the row
+    const uint32_t unit = b / 4, kb = b % 4, grp = unit / G, u = unit % G;
+    sx[(size_t)row * (vec_per_row / 4) + grp * 4 * G + kb * G + u] = (uint8_t)code;
+  }
+}
+
+// Row-major codes and scale codes -> blocks of 16 rows x G units (mx4.h).
+// Block b of an expert holds rows 32 (b / 2) + 8 g + 4 (b % 2) + i in its
+// row 4 g + i: the product then leaves a lane four consecutive output
+// columns, and with the neighbouring block eight.  One thread a 16-byte
+// piece of codes.
+__global__ void __launch_bounds__(256)
+mx4_pack_kernel(const u32x4* __restrict__ codes, const uint8_t* __restrict__ scales, size_t pieces, int units,
+                int G, char* __restrict__ packed) {
+  for (size_t p = (size_t)blockIdx.x * 256 + threadIdx.x; p < pieces; p += (size_t)gridDim.x * 256) {
+    const int lane = (int)(p % 64);
+    const size_t chunk = p / 64;
+    const int unit = (int)(chunk % units);
+    const size_t blk = chunk / units;   // over all experts
+    const int m = lane & 15, kb = lane >> 4;
+    const size_t row = 32 * (blk / 2) + 8 * (m >> 2) + 4 * (blk % 2) + (m & 3);
+    char* base = packed + (blk * units + unit / G * G) * kMx4Unit;
+    const int u = unit % G;
+    *reinterpret_cast<u32x4*>(base + u * 1024 + 16 * lane) = codes[(row * units + unit) * 4 + kb];
+    base[G * 1024 + lane * G + u] = (char)scales[(row * units + unit) * 4 + kb];
+  }
+}
+
+}  // namespace moe
+
+namespace moe_host {
+
+// Workgroups of a grid-stride pass over n items: eight per compute unit of
+// the largest part (256), fewer when there is less to do.
+static unsigned pass_grid(size_t n) {
+  const size_t b = (n + 255) / 256;
+  return (unsigned)(b < 4096 ? b : 4096);
+}
+
+hipError_t launch_mx4_quantize(const void* x, int row_type, size_t rows, int cols, size_t row_stride, uint8_t* codes,
+                               uint8_t* scales, hipStream_t s) {
+  const size_t nvec = rows * (size_t)(cols / 8);
+  return moe::with_row_type(row_type, [&](auto r) {
+    using R = decltype(r);
+    hipLaunchKernelGGL((moe::mx4_quantize_kernel<R>), dim3(pass_grid(nvec)), dim3(moe::kMx4Threads), 0, s,
+                       static_cast<const typename R::elem*>(x), nvec, (uint32_t)(cols / 8), row_stride,
+                       reinterpret_cast<uint32_t*>(codes), scales);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, size_t rows, int cols, int row_type,
+                                 void* out, hipStream_t s) {
+  const size_t nvec = rows * (size_t)(cols / 8);
+  return moe::with_row_type(row_type, [&](auto r) {
+    using R = decltype(r);
+    hipLaunchKernelGGL((moe::mx4_dequantize_kernel<R>), dim3(pass_grid(nvec)), dim3(moe::kMx4Threads), 0, s,
+                       reinterpret_cast<const uint32_t*>(codes), scales, nvec, static_cast<typename R::elem*>(out));
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_mx4_quant_x(const uint16_t* x, int T, int H, uint8_t* xq, uint8_t* sx, hipStream_t s,
+                              const DecodeRouteOut* route, int P) {
+  if (route && (P > moe::kDecodeRoutePairs || !route->ids)) return hipErrorInvalidValue;
+  const uint32_t nvec = (uint32_t)T * (uint32_t)(H / 8);   // T * H <= 2^32
+  const dim3 grid((nvec + moe::kMx4Threads - 1) / moe::kMx4Threads);
+  const DecodeRouteOut ro = route ? *route : DecodeRouteOut{};
+  uint32_t* q = reinterpret_cast<uint32_t*>(xq);
+  if (route)
+    hipLaunchKernelGGL(moe::mx4_quant_x_kernel<true>, grid, dim3(moe::kMx4Threads), 0, s, x, nvec, (uint32_t)(H / 8),
+                       moe::mx4_group(H), q, sx, ro, P);
+  else
+    hipLaunchKernelGGL(moe::mx4_quant_x_kernel<false>, grid, dim3(moe::kMx4Threads), 0, s, x, nvec, (uint32_t)(H / 8),
+                       moe::mx4_group(H), q, sx, ro, P);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx4_pack(const uint8_t* codes, const uint8_t* scales, int E, int rows, int cols, void* packed,
+                           hipStream_t s) {
+  const size_t pieces = (size_t)E * rows * (cols / 32);
+  hipLaunchKernelGGL(moe::mx4_pack_kernel, dim3(pass_grid(pieces)), dim3(256), 0, s,
+                     reinterpret_cast<const moe::u32x4*>(codes), scales, pieces, cols / 128, moe::mx4_group(cols),
+                     static_cast<char*>(packed));
+  return hipGetLastError();
+}
+
+}  // namespace moe_host

@@ -1,0 +1,290 @@
+// Token rows to expert order and back, and their gradients (HPC-Ops x SGLang
+// blog, section "MoE", routing & index build: the route index names, for
+// every token-expert pair, its row in the expert-sorted order).
+//
+// Pair p = t * k + j stands at sorted row r = pair_pos[p] when its id is
+// valid (r < expert_offsets[E]):
+//   to experts   rows[r] = w[p] tokens[t]
+//   to tokens    tokens[t] = sum_j w[p] rows[r]
+// Each is the other's gradient with respect to the rows; the gradient of
+// the weights is dw[p] = <rows[r], tokens[t]>, with dw[p] = 0 for a dropped
+// pair.  All of them are bound by the rows' bytes, so every kernel reads
+// each row once: a thread holds eight columns of its token in registers and
+// goes through the token's k pairs.  Sums run in fp32 in ascending j and are
+// rounded once; rows behind the last valid one are not written.
+//
+// A position outside [0, valid) counts as dropped, so a routing buffer that
+// does not belong to these sizes cannot lead a row access out of bounds.
+#include "rows.h"
+
+namespace moe {
+
+constexpr int kMoveThreads = 256;
+
+// The k pairs of token t: sorted row (-1: dropped) and weight.
+template <int KM>
+__device__ __forceinline__ void pair_rows(const moe_host::RowMoveArgs& g, int t, int (&row)[KM], float (&w)[KM]) {
+  const int valid = min(g.expert_offsets[g.E], g.T * g.k);
+#pragma unroll
+  for (int j = 0; j < KM; j++) {
+    const int p = t * g.k + (j < g.k ? j : g.k - 1);
+    const int r = g.pair_pos[p];
+    w[j] = g.w ? g.w[p] : 1.0f;
+    row[j] = j < g.k && (unsigned)r < (unsigned)valid ? r : -1;
+  }
+}
+
+template <typename R, int KM>
+__global__ void __launch_bounds__(kMoveThreads)
+rows_to_experts_kernel(moe_host::RowMoveArgs g) {
+  typedef typename R::elem elem;
+  const int t = blockIdx.x;
+  const int c = (blockIdx.y * kMoveThreads + threadIdx.x) * 8;
+  if (c >= g.H) return;
+  float v[8];
+  R::load8(static_cast<const elem*>(g.tokens) + (size_t)t * g.H + c, v);
+  int row[KM];
+  float w[KM];
+  pair_rows<KM>(g, t, row, w);
+  elem* out = static_cast<elem*>(g.out);
+#pragma unroll
+  for (int j = 0; j < KM; j++) {
+    if (row[j] < 0) continue;
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) o[i] = w[j] * v[i];
+    R::store8(out + (size_t)row[j] * g.H + c, o);
+  }
+}
+
+template <typename R, int KM>
+__global__ void __launch_bounds__(kMoveThreads)
+rows_to_tokens_kernel(moe_host::RowMoveArgs g) {
+  typedef typename R::elem elem;
+  const int t = blockIdx.x;
+  const int c = (blockIdx.y * kMoveThreads + threadIdx.x) * 8;
+  if (c >= g.H) return;
+  int row[KM];
+  float w[KM];
+  pair_rows<KM>(g, t, row, w);
+  const elem* rows = static_cast<const elem*>(g.rows);
+  float v[KM][8];
+#pragma unroll
+  for (int j = 0; j < KM; j++) {
+    if (row[j] >= 0) R::load8(rows + (size_t)row[j] * g.H + c, v[j]);
+  }
+  float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int j = 0; j < KM; j++) {
+    if (row[j] < 0) continue;
+#pragma unroll
+    for (int i = 0; i < 8; i++) acc[i] += w[j] * v[j][i];
+  }
+  R::store8(static_cast<elem*>(g.out) + (size_t)t * g.H + c, acc);
+}
+
+// The gradients with the weights': WPT waves a token.  TO_TOKENS (the
+// gradient of dispatch): out[t] = sum_j w rows[r]; else (of combine)
+// out[r] = w tokens[t].  Both: dw[p] = <rows[r], tokens[t]>, a lane's columns
+// in ascending order, then over the lanes and waves.
+template <typename R, int KM, int WPT, bool TO_TOKENS>
+__global__ void __launch_bounds__(WPT < 4 ? kMoveThreads : WPT * 64)
+rows_grad_kernel(moe_host::RowMoveArgs g) {
+  typedef typename R::elem elem;
+  constexpr int TPB = WPT < 4 ? 4 / WPT : 1;   // tokens a workgroup
+  __shared__ float part[WPT][KM];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int t = blockIdx.x * TPB + wave / WPT;
+  if (t >= g.T) return;   // whole waves; with WPT > 1 whole workgroups
+  int row[KM];
+  float w[KM], dot[KM];
+  pair_rows<KM>(g, t, row, w);
+#pragma unroll
+  for (int j = 0; j < KM; j++) dot[j] = 0.0f;
+  const elem* rows = static_cast<const elem*>(g.rows);
+  elem* out = static_cast<elem*>(g.out);
+  for (int c = ((wave % WPT) * 64 + lane) * 8; c < g.H; c += WPT * 512) {
+    float x[8], acc[8];
+    R::load8(static_cast<const elem*>(g.tokens) + (size_t)t * g.H + c, x);
+#pragma unroll
+    for (int i = 0; i < 8; i++) acc[i] = 0.0f;
+    float v[KM][8];
+#pragma unroll
+    for (int j = 0; j < KM; j++) {
+      if (row[j] >= 0) R::load8(rows + (size_t)row[j] * g.H + c, v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < KM; j++) {
+      if (row[j] < 0) continue;
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        dot[j] += v[j][i] * x[i];
+        if constexpr (TO_TOKENS) acc[i] += w[j] * v[j][i];
+        else v[j][i] = w[j] * x[i];
+      }
+      if constexpr (!TO_TOKENS) R::store8(out + (size_t)row[j] * g.H + c, v[j]);
+    }
+    if constexpr (TO_TOKENS) R::store8(out + (size_t)t * g.H + c, acc);
+  }
+#pragma unroll
+  for (int j = 0; j < KM; j++)
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) dot[j] += __shfl_xor(dot[j], o, 64);
+  if constexpr (WPT > 1) {
+    if (lane == 0) {
+#pragma unroll
+      for (int j = 0; j < KM; j++) part[wave][j] = dot[j];
+    }
+    __syncthreads();
+    if (threadIdx.x < g.k) {
+      float s = 0.0f;
+#pragma unroll
+      for (int q = 0; q < WPT; q++) s += part[q][threadIdx.x];
+      g.dw[(size_t)t * g.k + threadIdx.x] = s;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < KM; j++)
+      if (lane == 0 && j < g.k) g.dw[(size_t)t * g.k + j] = dot[j];
+  }
+}
+
+// d(logits) of the router's softmax top-k (router.hip) from d(topk_w), a wave
+// a token.  With p the softmax over the E scores and s = sum_j w_j dw_j over
+// the token's k chosen experts:
+//   renormalised   dl[e] = w_j (dw_j - s) for the chosen e = e_j, else 0
+//   otherwise      dl[e] = [e = e_j] w_j dw_j - p[e] s
+// The n_shared columns behind the k have constant weights and pass no
+// gradient.  The scores and their gradient are read and written once.
+template <bool RENORM>
+__global__ void __launch_bounds__(256)
+router_topk_grad_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids,
+                        const float* __restrict__ w, const float* __restrict__ dw, int T, int E, int k, int ncol,
+                        float* __restrict__ dl) {
+  const int lane = threadIdx.x & 63;
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= T) return;
+  // lane j < k holds the j-th chosen expert
+  const size_t at = (size_t)t * ncol + (lane < k ? lane : 0);
+  const int id = ids[at];
+  const float wj = lane < k ? w[at] : 0.0f, dj = lane < k ? dw[at] : 0.0f;
+  constexpr int NE = 4;   // E <= 256: experts a lane
+  float l[NE];
+  if constexpr (!RENORM) {
+#pragma unroll
+    for (int q = 0; q < NE; q++) {
+      const int e = q * 64 + lane;
+      l[q] = e < E ? logits[(size_t)t * E + e] : 0.0f;
+    }
+  }
+  float s = lane < k ? wj * dj : 0.0f;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+  s = __shfl(s, 0, 64);   // k <= 16: the first 16 lanes' sum
+  const float up = RENORM ? wj * (dj - s) : wj * dj;
+  float g[NE];
+#pragma unroll
+  for (int q = 0; q < NE; q++) g[q] = 0.0f;
+  if constexpr (!RENORM) {
+    // softmax over the E scores; a NaN score counts as -infinity, as in the choice
+    float m = -__builtin_inff();
+#pragma unroll
+    for (int q = 0; q < NE; q++) {
+      l[q] = q * 64 + lane < E && l[q] == l[q] ? l[q] : -__builtin_inff();
+      m = __builtin_fmaxf(m, l[q]);
+    }
+    m = wave_max(m);
+    float z = 0.0f;
+#pragma unroll
+    for (int q = 0; q < NE; q++) {
+      l[q] = l[q] == -__builtin_inff() ? 0.0f : expf(l[q] - m);
+      z += l[q];
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) z += __shfl_xor(z, o, 64);
+    const float c = s / z;
+#pragma unroll
+    for (int q = 0; q < NE; q++) g[q] = l[q] == 0.0f ? 0.0f : -l[q] * c;
+  }
+  for (int j = 0; j < k; j++) {
+    const int e = __builtin_amdgcn_readlane(id, j);
+    const float u = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(up), j));
+#pragma unroll
+    for (int q = 0; q < NE; q++) g[q] += e == q * 64 + lane ? u : 0.0f;
+  }
+#pragma unroll
+  for (int q = 0; q < NE; q++) {
+    const int e = q * 64 + lane;
+    if (e < E) dl[(size_t)t * E + e] = g[q];
+  }
+}
+
+template <typename F>
+static hipError_t with_pairs(int k, F&& f) {
+  if (k <= 2) return f(std::integral_constant<int, 2>{});
+  if (k <= 4) return f(std::integral_constant<int, 4>{});
+  if (k <= 8) return f(std::integral_constant<int, 8>{});
+  return f(std::integral_constant<int, 16>{});
+}
+
+}  // namespace moe
+
+namespace moe_host {
+
+hipError_t launch_rows_to_experts(const RowMoveArgs& a, int row_type, hipStream_t s) {
+  const dim3 grid(a.T, (a.H / 8 + moe::kMoveThreads - 1) / moe::kMoveThreads);
+  return moe::with_row_type(row_type, [&](auto r) {
+    return moe::with_pairs(a.k, [&](auto km) {
+      hipLaunchKernelGGL((moe::rows_to_experts_kernel<decltype(r), decltype(km)::value>), grid,
+                         dim3(moe::kMoveThreads), 0, s, a);
+      return hipGetLastError();
+    });
+  });
+}
+
+hipError_t launch_rows_to_tokens(const RowMoveArgs& a, int row_type, hipStream_t s) {
+  const dim3 grid(a.T, (a.H / 8 + moe::kMoveThreads - 1) / moe::kMoveThreads);
+  return moe::with_row_type(row_type, [&](auto r) {
+    return moe::with_pairs(a.k, [&](auto km) {
+      hipLaunchKernelGGL((moe::rows_to_tokens_kernel<decltype(r), decltype(km)::value>), grid,
+                         dim3(moe::kMoveThreads), 0, s, a);
+      return hipGetLastError();
+    });
+  });
+}
+
+hipError_t launch_rows_grad(const RowMoveArgs& a, bool to_tokens, int row_type, hipStream_t s) {
+  return moe::with_row_type(row_type, [&](auto r) {
+    return moe::with_pairs(a.k, [&](auto km) {
+      using R = decltype(r);
+      constexpr int KM = decltype(km)::value;
+      if (a.H > 512) {   // four waves a token; narrower rows fill a wave at most
+        if (to_tokens)
+          hipLaunchKernelGGL((moe::rows_grad_kernel<R, KM, 4, true>), dim3(a.T), dim3(256), 0, s, a);
+        else
+          hipLaunchKernelGGL((moe::rows_grad_kernel<R, KM, 4, false>), dim3(a.T), dim3(256), 0, s, a);
+      } else {
+        const dim3 grid((a.T + 3) / 4);
+        if (to_tokens)
+          hipLaunchKernelGGL((moe::rows_grad_kernel<R, KM, 1, true>), grid, dim3(256), 0, s, a);
+        else
+          hipLaunchKernelGGL((moe::rows_grad_kernel<R, KM, 1, false>), grid, dim3(256), 0, s, a);
+      }
+      return hipGetLastError();
+    });
+  });
+}
+
+hipError_t launch_router_topk_grad(const float* logits, const int32_t* ids, const float* w, const float* dw, int T,
+                                   int E, int k, bool renorm, int n_shared, float* dl, hipStream_t s) {
+  const dim3 grid((T + 3) / 4);
+  if (renorm)
+    hipLaunchKernelGGL(moe::router_topk_grad_kernel<true>, grid, dim3(256), 0, s, logits, ids, w, dw, T, E, k,
+                       k + n_shared, dl);
+  else
+    hipLaunchKernelGGL(moe::router_topk_grad_kernel<false>, grid, dim3(256), 0, s, logits, ids, w, dw, T, E, k,
+                       k + n_shared, dl);
+  return hipGetLastError();
+}
+
+}  // namespace moe_host

@@ -1,0 +1,167 @@
+"""Host-side refusals of the MXFP4 and expert-order row entry points (no GPU,
+nothing is launched)."""
+import ctypes
+
+import pytest
+import torch
+
+NULL = None
+FAKE, ODD = ctypes.c_void_p(4096), ctypes.c_void_p(4100)   # never dereferenced: every call fails its checks
+
+
+@pytest.fixture(scope="module")
+def m():
+    import mixture_experts_layer_lds_amd as mod
+    return mod
+
+
+def test_layouts(m):
+    # decode: x codes, h blocks of max_tasks 16-row tiles, no down rows at one token
+    for T, k, E, H, I in ((1, 8, 256, 7168, 2048), (16, 8, 256, 7168, 2048), (4096, 8, 256, 7168, 2048), (300, 2, 4, 384, 640)):
+        R, W = m.moe_routing_layout(T, k, E, H, I, "mxfp4"), m.moe_workspace_layout(T, k, E, H, I, "mxfp4")
+        none = 2 ** 64 - 1
+        assert W["xq"] == 0 and W["x_scale"] >= T * H // 2 and W["h"] >= W["x_scale"] + T * H // 32
+        assert W["g"] == W["h_scale"] == W["x_scale_rows"] == none
+        end = W["h"] + R["max_tasks"] * R["block_m"] * I * 17 // 32
+        if T == 1:
+            assert W["y"] == none and end <= W["total_bytes"]
+        else:
+            assert W["y"] >= end and W["y"] + 2 * T * k * H <= W["total_bytes"]
+        assert all(W[n] == none or W[n] % 256 == 0 for n in ("xq", "x_scale", "h", "y"))
+        assert R["max_tasks"] == T * k // R["block_m"] + min(E, T * k)
+    for bad in ((4, 2, 8, 64, 128), (4, 2, 8, 128, 192), (8193, 8, 8, 128, 128)):
+        with pytest.raises(m.MoeError) as e:
+            m.moe_workspace_layout(*bad, "mxfp4")
+        assert e.value.status == -2
+
+
+def test_quantize_refusals(m):
+    q, d = m._lib.moe_quantize_mxfp4, m._lib.moe_dequantize_mxfp4
+    assert q(FAKE, 3, 4, 64, 64, FAKE, FAKE, NULL) == -1      # no such row type
+    assert q(FAKE, -1, 4, 64, 64, FAKE, FAKE, NULL) == -1
+    assert q(FAKE, 0, -1, 64, 64, FAKE, FAKE, NULL) == -1
+    assert q(FAKE, 0, 4, 0, 64, FAKE, FAKE, NULL) == -1
+    assert q(FAKE, 0, 4, 64, 32, FAKE, FAKE, NULL) == -1      # rows would overlap
+    assert q(FAKE, 0, 4, 48, 64, FAKE, FAKE, NULL) == -2
+    assert q(FAKE, 0, 4, 64, 68, FAKE, FAKE, NULL) == -2      # rows not 16-byte aligned
+    assert q(FAKE, 0, 0, 64, 64, NULL, NULL, NULL) == 0
+    for args in ((NULL, FAKE, FAKE), (FAKE, NULL, FAKE), (FAKE, FAKE, NULL), (ODD, FAKE, FAKE)):
+        assert q(args[0], 0, 4, 64, 64, args[1], args[2], NULL) == -1
+    assert q(FAKE, 0, 4, 64, 64, ctypes.c_void_p(4098), FAKE, NULL) == -1
+    assert d(FAKE, FAKE, 4, 48, 0, FAKE, NULL) == -2 and d(FAKE, FAKE, 4, 64, 5, FAKE, NULL) == -1
+    assert d(FAKE, FAKE, 4, 64, 0, ODD, NULL) == -1 and d(NULL, FAKE, 4, 64, 0, FAKE, NULL) == -1
+    assert d(NULL, NULL, 0, 64, 0, NULL, NULL) == 0
+
+
+def test_pack_and_forward_refusals(m):
+    lib = m._lib
+    desc = m.PackedWeightsDesc()
+    D = ctypes.byref(desc)
+    big = ctypes.c_void_p(1 << 30)
+    pack = lib.moe_pack_weights_mxfp4
+    assert pack(FAKE, FAKE, 8, 256, 128, big, NULL, NULL) == -1
+    assert pack(FAKE, FAKE, 8, 48, 128, big, D, NULL) == -2 and pack(FAKE, FAKE, 8, 64, 192, big, D, NULL) == -2
+    assert pack(FAKE, FAKE, 0, 64, 128, big, D, NULL) == -1
+    assert pack(NULL, FAKE, 8, 64, 128, big, D, NULL) == -1 and pack(FAKE, NULL, 8, 64, 128, big, D, NULL) == -1
+    assert pack(FAKE, FAKE, 8, 64, 128, NULL, D, NULL) == -1 and pack(ODD, FAKE, 8, 64, 128, big, D, NULL) == -1
+    assert pack(FAKE, big, 8, 64, 128, FAKE, D, NULL) == -1                                   # codes overlap
+    assert pack(big, ctypes.c_void_p(4096 + 64), 8, 64, 128, FAKE, D, NULL) == -1             # scales overlap
+    assert desc.data is None and desc.check == 0
+    # the generic pack has no scales to pack
+    assert lib.moe_pack_weights(FAKE, 8, 64, 128, m.MOE_DTYPE_MXFP4, big, D, NULL) == -1
+
+    E, H, I, T, k = 8, 128, 128, 4, 2
+
+    def describe(rows, cols, dtype):
+        d = m.PackedWeightsDesc()
+        assert lib.moe_describe_packed_weights(FAKE, E, rows, cols, m.DTYPES[dtype], ctypes.byref(d)) == 0
+        return ctypes.byref(d)
+
+    w1, w2, f1 = describe(2 * I, H, "mxfp4"), describe(H, I, "mxfp4"), describe(2 * I, H, "fp8")
+    n, W = m.moe_routing_layout(T, k, E, H, I, "mxfp4")["total_bytes"], m.moe_workspace_layout(T, k, E, H, I, "mxfp4")["total_bytes"]
+    fwd, rfw, bld = lib.moe_forward_mxfp4, lib.moe_route_forward_mxfp4, lib.moe_build_routing_mxfp4
+    good = [FAKE, FAKE, FAKE, w1, w2, T, k, E, H, I, FAKE, W, FAKE, NULL]
+    for at, value, code in ((0, NULL, -1), (1, NULL, -1), (2, NULL, -1), (3, NULL, -1), (3, f1, -1), (3, w2, -1), (4, w1, -1),
+                            (10, NULL, -1), (10, ODD, -1), (11, W - 1, -3), (12, NULL, -1), (12, ODD, -1), (8, 192, -2), (9, 64, -2),
+                            (6, 17, -1), (5, -1, -1), (7, 0, -1)):
+        a = list(good)
+        a[at] = value
+        assert fwd(*a) == code, (at, value)
+        b = [FAKE, a[0], a[1], a[2], n, *a[3:]]
+        assert rfw(*b) == code, (at, value)
+    assert fwd(*[NULL] * 5, 0, k, E, H, I, NULL, 0, NULL, NULL) == 0
+    assert rfw(*[FAKE, FAKE, FAKE, FAKE, n - 1], *good[3:]) == -3 and rfw(NULL, FAKE, FAKE, FAKE, n, *good[3:]) == -1
+    assert bld(FAKE, T, k, E, H, I, FAKE, n - 1, NULL) == -3 and bld(FAKE, T, k, E, 192, I, FAKE, n, NULL) == -2
+    # MXFP4 weights do not pass for another dtype's
+    assert lib.moe_forward_mxfp8(FAKE, FAKE, FAKE, w1, FAKE, w2, FAKE, T, k, E, H, I, FAKE, 1 << 30, FAKE, NULL) == -1
+
+
+def test_row_operator_refusals(m):
+    lib = m._lib
+    T, k, E, H = 4, 2, 8, 64
+    n = m.moe_routing_layout(T, k, E, 128, 128, "bf16")["tasks"]
+    for name in ("moe_dispatch", "moe_combine"):
+        f = getattr(lib, name)
+        good = [FAKE, 0, FAKE, FAKE, n, T, k, E, H, FAKE, NULL]
+        for at, value, code in ((0, NULL, -1), (0, ODD, -1), (1, 3, -1), (1, -1, -1), (2, ctypes.c_void_p(4098), -1), (3, NULL, -1), (3, ODD, -1),
+                                (4, n - 1, -3), (5, -1, -1), (5, 40000, -2), (6, 0, -1), (6, 17, -1), (7, 0, -1), (7, 512, -1), (8, 0, -1),
+                                (8, 12, -2), (8, 65544, -2), (9, NULL, -1), (9, ODD, -1)):
+            a = list(good)
+            a[at] = value
+            assert f(*a) == code, (name, at, value)
+        assert f(NULL, 0, NULL, NULL, 0, 0, k, E, H, NULL, NULL) == 0
+    for name in ("moe_dispatch_grad", "moe_combine_grad"):
+        f = getattr(lib, name)
+        good = [FAKE, FAKE, 0, FAKE, FAKE, n, T, k, E, H, FAKE, FAKE, NULL]
+        for at, value, code in ((0, NULL, -1), (1, NULL, -1), (1, ODD, -1), (2, 7, -1), (3, NULL, -1), (4, NULL, -1), (5, n - 1, -3),
+                                (9, 12, -2), (10, NULL, -1), (11, ctypes.c_void_p(4097), -1)):
+            a = list(good)
+            a[at] = value
+            assert f(*a) == code, (name, at, value)
+        # without the weights' gradient the second operand is not needed, the rest still is
+        assert f(FAKE, NULL, 0, NULL, FAKE, n, T, k, E, H, NULL, NULL, NULL) == -1
+    g = lib.moe_router_topk_grad
+    good = [FAKE, FAKE, FAKE, FAKE, T, E, k, 1, 0, FAKE, NULL]
+    for at, value, code in ((1, NULL, -1), (2, NULL, -1), (3, NULL, -1), (4, -1, -1), (5, 0, -1), (5, 257, -2), (6, 0, -1), (6, 9, -1),
+                            (7, 2, -1), (8, -1, -1), (8, 15, -2), (9, NULL, -1), (9, ctypes.c_void_p(4097), -1)):
+        a = list(good)
+        a[at] = value
+        assert g(*a) == code, (at, value)
+    assert g(NULL, FAKE, FAKE, FAKE, T, E, k, 0, 0, FAKE, NULL) == -1      # the full softmax needs the scores
+    assert g(NULL, NULL, NULL, NULL, 0, E, k, 1, 0, NULL, NULL) == 0
+
+
+def test_binding_refuses_wrong_tensors(m):
+    """Shapes, types, strides and devices are refused before the library is called."""
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    r = torch.zeros(4096, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="current GPU"):
+        m.moe_quantize_mxfp4(x)
+    with pytest.raises(ValueError, match="current GPU"):
+        m.moe_dispatch(x, r, 2, 8)
+    with pytest.raises(ValueError, match="32 values"):
+        m.moe_quantize_mxfp4(x[:, :48])
+    with pytest.raises(ValueError, match="contiguous rows"):
+        m.moe_quantize_mxfp4(torch.zeros(64, 64).t()[:, :32])
+    with pytest.raises(ValueError, match="contiguous rows"):
+        m.moe_quantize_mxfp4(torch.zeros(1, 64).expand(4, 64))
+    with pytest.raises(ValueError, match="rows"):
+        m.moe_quantize_mxfp4(x.double())
+    with pytest.raises(ValueError, match="codes"):
+        m.moe_dequantize_mxfp4(torch.zeros(4, 24, dtype=torch.uint8), r)
+    with pytest.raises(ValueError, match="scales"):
+        m.moe_pack_weights_mxfp4(torch.zeros(1, 32, 64, dtype=torch.uint8), torch.zeros(1, 32, 5, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="y: expected"):
+        m.moe_combine(torch.zeros(7, 64), r, 2, 8)
+    with pytest.raises(ValueError, match="topk_w"):
+        m.moe_dispatch(x, r, 2, 8, topk_w=torch.zeros(4, 3))
+    with pytest.raises(ValueError, match="topk_w"):
+        m.moe_dispatch_grad(torch.zeros(8, 64), r, 2, 8, x=torch.zeros(4, 64))
+    with pytest.raises(ValueError, match="dtopk_w needs"):
+        m.moe_combine_grad(torch.zeros(4, 64), r, 2, 8, topk_w=torch.zeros(4, 2), dtopk_w=torch.zeros(4, 2))
+    with pytest.raises(ValueError, match="x: expected"):
+        m.moe_dispatch_grad(torch.zeros(8, 64), r, 2, 8, x=torch.zeros(5, 64), topk_w=torch.zeros(4, 2))
+    with pytest.raises(ValueError, match="dtopk_w"):
+        m.moe_router_topk_grad(torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2), torch.zeros(4, 3))
+    with pytest.raises(ValueError, match="packed MXFP4"):
+        m.moe_describe_packed_weights(torch.zeros(1, 32, 64, dtype=torch.uint8), "mxfp4")
