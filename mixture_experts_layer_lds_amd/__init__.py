@@ -727,16 +727,29 @@ def moe_forward_int8(x, topk_w, routing, w1, w1_scale, w2, w2_scale, workspace, 
     return out
 
 
-def _check_device(**tensors):
-    """Every given tensor is on the current GPU (a kernel cannot take host
-    memory, and a launch goes to the current device's streams)."""
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if isinstance(t, PackedWeight):
-            t = t.tensor
-        if not t.is_cuda or t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name}: expected a tensor on the current GPU, got one on {t.device}")
+def _check_device(*tensors):
+    """Every given tensor (None: left out) is on the current GPU: a kernel
+    cannot take host memory, and a launch goes to the current device's streams."""
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"expected tensors on the current GPU, got one of shape {tuple(t.shape)} on {t.device}")
+    return dev
+
+
+def _here(dev, stream):
+    """The hipStream_t of `stream`, or of device dev's current stream."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _is(name, t, dtype, shape):
+    """_check_tensor for the short calls: no conversions where all is well."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _check_tensor(name, t, dtype, shape)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _empty(shape, dtype, device, stream):
@@ -770,11 +783,11 @@ def moe_quantize_mxfp4(x, codes=None, scales=None, stream=None):
         codes = _empty((*x.shape[:-1], cols // 2), torch.uint8, x.device, stream)
     if scales is None:
         scales = _empty((*x.shape[:-1], cols // 32), torch.uint8, x.device, stream)
-    _check_tensor("codes", codes, torch.uint8, (*x.shape[:-1], cols // 2))
-    _check_tensor("scales", scales, torch.uint8, (*x.shape[:-1], cols // 32))
-    _check_device(x=x, codes=codes, scales=scales)
+    _is("codes", codes, torch.uint8, (*x.shape[:-1], cols // 2))
+    _is("scales", scales, torch.uint8, (*x.shape[:-1], cols // 32))
+    dev = _check_device(x, codes, scales)
     _check("moe_quantize_mxfp4", _lib.moe_quantize_mxfp4(
-        _ptr(x), kind, x.numel() // cols, cols, stride, _ptr(codes), _ptr(scales), _stream(stream)))
+        x.data_ptr(), kind, x.numel() // cols, cols, stride, codes.data_ptr(), scales.data_ptr(), _here(dev, stream)))
     return codes, scales
 
 
@@ -787,12 +800,12 @@ def moe_dequantize_mxfp4(codes, scales, dtype=torch.bfloat16, out=None, stream=N
     if out is None:
         out = _empty((*lead, cols), dtype, codes.device, stream)
     kind = _row_type("out", out)
-    _check_tensor("codes", codes, torch.uint8, (*lead, cols // 2))
-    _check_tensor("scales", scales, torch.uint8, (*lead, cols // 32))
-    _check_tensor("out", out, out.dtype, (*lead, cols))
-    _check_device(codes=codes, scales=scales, out=out)
+    _is("codes", codes, torch.uint8, (*lead, cols // 2))
+    _is("scales", scales, torch.uint8, (*lead, cols // 32))
+    _is("out", out, out.dtype, (*lead, cols))
+    dev = _check_device(codes, scales, out)
     _check("moe_dequantize_mxfp4", _lib.moe_dequantize_mxfp4(
-        _ptr(codes), _ptr(scales), out.numel() // cols, cols, kind, _ptr(out), _stream(stream)))
+        codes.data_ptr(), scales.data_ptr(), out.numel() // cols, cols, kind, out.data_ptr(), _here(dev, stream)))
     return out
 
 
@@ -807,7 +820,7 @@ def moe_pack_weights_mxfp4(codes, scales, out=None, stream=None):
     if out is None:
         out = _empty((E, rows, cols // 2 + cols // 32), torch.uint8, codes.device, stream)
     _check_tensor("out", out, torch.uint8, (E, rows, cols // 2 + cols // 32))
-    _check_device(codes=codes, scales=scales, out=out)
+    _check_device(codes, scales, out)
     desc = PackedWeightsDesc()
     _check("moe_pack_weights_mxfp4", _lib.moe_pack_weights_mxfp4(
         _ptr(codes), _ptr(scales), E, rows, cols, _ptr(out), ctypes.byref(desc), _stream(stream)))
@@ -818,39 +831,39 @@ def moe_build_routing_mxfp4(topk_ids, E, H, I, routing, stream=None):
     _build_routing(_lib.moe_build_routing_mxfp4, "moe_build_routing_mxfp4", topk_ids, E, H, I, routing, stream)
 
 
-def _mxfp4_sizes(x, topk_w, w1, w2, workspace, out):
-    """(T, k, E, H, I) of an MXFP4 forward call, its tensors checked."""
+def _mxfp4_sizes(x, topk_w, w1, w2, routing, workspace, out, topk_ids=None):
+    """(T, k, E, H, I), the weights' descriptors and the device of an MXFP4
+    forward call, its tensors checked."""
     T, H = x.shape
     k = topk_w.shape[1]
     E, I2 = w1.shape[:2]
     I = I2 // 2
-    _check_tensor("x", x, torch.bfloat16, (T, H))
-    _check_tensor("topk_w", topk_w, torch.float32, (T, k))
-    _check_tensor("w1", w1, torch.uint8, (E, 2 * I, H // 2 + H // 32))
-    _check_tensor("w2", w2, torch.uint8, (E, H, I // 2 + I // 32))
-    _check_tensor("out", out, torch.bfloat16, (T, H))
-    _check_device(x=x, topk_w=topk_w, w1=w1, w2=w2, workspace=workspace, out=out)
-    return T, k, E, H, I
+    d1, d2 = _desc("w1", w1), _desc("w2", w2)
+    _is("x", x, torch.bfloat16, (T, H))
+    _is("topk_w", topk_w, torch.float32, (T, k))
+    _is("w1", w1.tensor, torch.uint8, (E, 2 * I, H // 2 + H // 32))
+    _is("w2", w2.tensor, torch.uint8, (E, H, I // 2 + I // 32))
+    _is("out", out, torch.bfloat16, (T, H))
+    dev = _check_device(x, topk_w, w1.tensor, w2.tensor, routing, workspace, out, topk_ids)
+    return (T, k, E, H, I), (d1, d2), dev
 
 
 def moe_forward_mxfp4(x, topk_w, routing, w1, w2, workspace, out, stream=None):
-    T, k, E, H, I = _mxfp4_sizes(x, topk_w, w1, w2, workspace, out)
-    _check_device(routing=routing)
+    sizes, desc, dev = _mxfp4_sizes(x, topk_w, w1, w2, routing, workspace, out)
     _check("moe_forward_mxfp4", _lib.moe_forward_mxfp4(
-        _ptr(x), _ptr(topk_w), _ptr(routing), _desc("w1", w1), _desc("w2", w2), T, k, E, H, I,
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out), _stream(stream)))
+        x.data_ptr(), topk_w.data_ptr(), routing.data_ptr(), *desc, *sizes, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), out.data_ptr(), _here(dev, stream)))
     return out
 
 
 def moe_route_forward_mxfp4(topk_ids, x, topk_w, routing, w1, w2, workspace, out, stream=None):
     """moe_build_routing_mxfp4 + moe_forward_mxfp4 in one call."""
-    T, k, E, H, I = _mxfp4_sizes(x, topk_w, w1, w2, workspace, out)
-    _check_tensor("topk_ids", topk_ids, torch.int32, (T, k))
-    _check_device(topk_ids=topk_ids, routing=routing)
+    sizes, desc, dev = _mxfp4_sizes(x, topk_w, w1, w2, routing, workspace, out, topk_ids)
+    _is("topk_ids", topk_ids, torch.int32, sizes[:2])
     _check("moe_route_forward_mxfp4", _lib.moe_route_forward_mxfp4(
-        _ptr(topk_ids), _ptr(x), _ptr(topk_w), _ptr(routing), routing.numel() * routing.element_size(),
-        _desc("w1", w1), _desc("w2", w2), T, k, E, H, I, _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(out), _stream(stream)))
+        topk_ids.data_ptr(), x.data_ptr(), topk_w.data_ptr(), routing.data_ptr(),
+        routing.numel() * routing.element_size(), *desc, *sizes, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), out.data_ptr(), _here(dev, stream)))
     return out
 
 
@@ -867,13 +880,13 @@ def _move(name, fn, src, src_name, sorted_src, routing, k, E, topk_w, out, out_n
     shape = (T, H) if sorted_src else (T * k, H)
     if out is None:
         out = _empty(shape, src.dtype, src.device, stream)
-    _check_tensor(src_name, src, src.dtype, src.shape)
-    _check_tensor(out_name, out, src.dtype, shape)
+    _is(src_name, src, src.dtype, src.shape)
+    _is(out_name, out, src.dtype, shape)
     if topk_w is not None:
-        _check_tensor("topk_w", topk_w, torch.float32, (T, k))
-    _check_device(**{src_name: src, out_name: out}, topk_w=topk_w, routing=routing)
-    _check(name, fn(_ptr(src), kind, _ptr(topk_w), _ptr(routing), routing.numel() * routing.element_size(), T, k, E, H,
-                    _ptr(out), _stream(stream)))
+        _is("topk_w", topk_w, torch.float32, (T, k))
+    dev = _check_device(src, out, topk_w, routing)
+    _check(name, fn(src.data_ptr(), kind, _at(topk_w), routing.data_ptr(), routing.numel() * routing.element_size(),
+                    T, k, E, H, out.data_ptr(), _here(dev, stream)))
     return out
 
 
@@ -902,16 +915,16 @@ def _move_grad(name, fn, grad, grad_name, sorted_grad, other, other_name, routin
         out = _empty(shape, grad.dtype, grad.device, stream)
     if other is not None and dw is None:
         dw = _empty((T, k), torch.float32, grad.device, stream)
-    _check_tensor(grad_name, grad, grad.dtype, grad.shape)
-    _check_tensor(out_name, out, grad.dtype, shape)
+    _is(grad_name, grad, grad.dtype, grad.shape)
+    _is(out_name, out, grad.dtype, shape)
     if topk_w is not None:
-        _check_tensor("topk_w", topk_w, torch.float32, (T, k))
+        _is("topk_w", topk_w, torch.float32, (T, k))
     if other is not None:
-        _check_tensor(other_name, other, grad.dtype, shape)
-        _check_tensor("dtopk_w", dw, torch.float32, (T, k))
-    _check_device(**{grad_name: grad, out_name: out, other_name: other}, topk_w=topk_w, dtopk_w=dw, routing=routing)
-    _check(name, fn(_ptr(grad), _ptr(other), kind, _ptr(topk_w), _ptr(routing),
-                    routing.numel() * routing.element_size(), T, k, E, H, _ptr(out), _ptr(dw), _stream(stream)))
+        _is(other_name, other, grad.dtype, shape)
+        _is("dtopk_w", dw, torch.float32, (T, k))
+    dev = _check_device(grad, out, other, topk_w, dw, routing)
+    _check(name, fn(grad.data_ptr(), _at(other), kind, _at(topk_w), routing.data_ptr(),
+                    routing.numel() * routing.element_size(), T, k, E, H, out.data_ptr(), _at(dw), _here(dev, stream)))
     return out if dw is None else (out, dw)
 
 
@@ -939,15 +952,15 @@ def moe_router_topk_grad(logits, topk_ids, topk_w, dtopk_w, renormalize=True, n_
     ncol = topk_ids.shape[1]
     if dlogits is None:
         dlogits = _empty((T, E), torch.float32, logits.device, stream)
-    _check_tensor("logits", logits, torch.float32, (T, E))
-    _check_tensor("topk_ids", topk_ids, torch.int32, (T, ncol))
-    _check_tensor("topk_w", topk_w, torch.float32, (T, ncol))
-    _check_tensor("dtopk_w", dtopk_w, torch.float32, (T, ncol))
-    _check_tensor("dlogits", dlogits, torch.float32, (T, E))
-    _check_device(logits=logits, topk_ids=topk_ids, topk_w=topk_w, dtopk_w=dtopk_w, dlogits=dlogits)
+    _is("logits", logits, torch.float32, (T, E))
+    _is("topk_ids", topk_ids, torch.int32, (T, ncol))
+    _is("topk_w", topk_w, torch.float32, (T, ncol))
+    _is("dtopk_w", dtopk_w, torch.float32, (T, ncol))
+    _is("dlogits", dlogits, torch.float32, (T, E))
+    dev = _check_device(logits, topk_ids, topk_w, dtopk_w, dlogits)
     _check("moe_router_topk_grad", _lib.moe_router_topk_grad(
-        _ptr(logits), _ptr(topk_ids), _ptr(topk_w), _ptr(dtopk_w), T, E, ncol - n_shared, int(bool(renormalize)),
-        n_shared, _ptr(dlogits), _stream(stream)))
+        logits.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(), dtopk_w.data_ptr(), T, E, ncol - n_shared,
+        1 if renormalize else 0, n_shared, dlogits.data_ptr(), _here(dev, stream)))
     return dlogits
 
 

@@ -214,7 +214,7 @@ void plan_mx4(int T, int k, int E, int H, int I, Plan* p) {
   const long P = (long)T * k, active = std::min(P, (long)E);
   const long avg = active > 0 ? (P + active - 1) / active : 1;
   p->tiling = avg <= 16 ? kStreaming : kStrips;
-  p->mb = avg <= 8 ? 1 : (avg <= 16 ? 2 : (avg <= 40 ? 4 : (avg <= 96 ? 8 : 12)));
+  p->mb = avg <= 8 ? 1 : (avg <= 16 ? 2 : (avg <= 40 ? 4 : (avg <= 72 ? 6 : (avg <= 96 ? 8 : (avg <= 128 ? 10 : 12)))));
   p->block_m = 16 * p->mb;
   p->max_tasks = (int)(P / p->block_m + active);
   if (p->tiling == kStrips) return;
@@ -937,6 +937,7 @@ int forward_mx4(const void* x, const float* topk_w, const void* routing, const v
   }
   moe_host::Mx4Args a{};
   a.sorted_pairs = R.sorted_pairs;
+  a.expert_offsets = R.expert_offsets;
   a.header = R.header;
   a.tasks = R.tasks;
   a.topk = k;

@@ -434,6 +434,7 @@ struct Mx4Args {
   const uint8_t* a_sc;          // gate-up: their scale codes [T][K/128/G][4][G]
   const void* b;                // packed weights, w_rows rows per expert
   const int32_t* sorted_pairs;
+  const int32_t* expert_offsets;
   const int32_t* header;
   const moe_task_t* tasks;
   void* c;                      // gate-up: SiLU(gate) * up as blocks of 16 rows x G units, mb blocks a task;
@@ -449,7 +450,7 @@ struct Mx4Args {
 hipError_t launch_mx4_stream(const Mx4Args& a, bool gateup, int mb, int waves, int grid, hipStream_t s);
 // One token: down GEMM and top-k weighted sum, out (bf16 [H]) in a.c.
 hipError_t launch_mx4_down_reduce(const Mx4Args& a, hipStream_t s);
-// mb in {4, 8, 12}
+// mb in {4, 6, 8, 10, 12}
 hipError_t launch_mx4_strip(const Mx4Args& a, bool gateup, int mb, int grid, hipStream_t s);
 
 // Rows between token and expert order (rows.hip).

@@ -2,11 +2,12 @@
 // (SGLang tuning guide, block shapes: gfx95 devices keep MX's [1, 32]
 // blocks; the format and its rounding are in mx4.h).
 //
-// Quantisation: four lanes a block, eight values each, so that a wave reads
-// 64 consecutive runs of eight values and writes 256 consecutive bytes of
-// codes; the block's largest magnitude crosses the four lanes in two
-// exchanges.  Every value is read once and nothing is kept, so the kernel is
-// bound by its reads and writes.
+// Both passes go over 16 bytes of row values a lane at a time (eight 16-bit or
+// four 32-bit values), so that a wave's loads and stores of rows are whole
+// 1 KiB runs, and a 32-value block lies on four or eight neighbouring lanes,
+// which exchange its largest magnitude in two or three steps.  Every value is
+// read once and nothing is kept: the passes are bound by their bytes.  Large
+// ones take four runs a wave, all loads ahead of the first use.
 #include "decode_route.h"
 #include "mx4.h"
 #include "rows.h"
@@ -26,45 +27,79 @@ __device__ __forceinline__ uint32_t mx4_quant8(const float (&v)[8], uint32_t& co
   return mx4_encode8(v, code);
 }
 
-// rows x cols values (row_stride elements apart) -> codes [rows][cols/2] and
-// scale codes [rows][cols/32], row-major.  nvec = rows * cols / 8.
-template <typename R>
+// The vector (16 bytes of row values) that lane and step u of this thread
+// take: a wave's UN runs are consecutive.
+template <int UN>
+__device__ __forceinline__ size_t mx4_vector(int u) {
+  return (((size_t)blockIdx.x * (kMx4Threads / 64) + (threadIdx.x >> 6)) * UN + u) * 64 + (threadIdx.x & 63);
+}
+
+// rows x cols values -> codes [rows][cols/2] and scale codes [rows][cols/32],
+// row-major.  FLAT: rows follow one another; else row_stride elements apart.
+template <typename R, int UN, bool FLAT>
 __global__ void __launch_bounds__(kMx4Threads)
 mx4_quantize_kernel(const typename R::elem* __restrict__ x, size_t nvec, uint32_t vec_per_row, size_t row_stride,
-                    uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {
-  const bool flat = row_stride == (size_t)vec_per_row * 8;
-  for (size_t i = (size_t)blockIdx.x * kMx4Threads + threadIdx.x; i < nvec; i += (size_t)gridDim.x * kMx4Threads) {
-    size_t at = i * 8;
-    if (!flat) {
+                    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  constexpr int N = R::kVec, LB = 32 / N;   // values a lane, lanes a block
+  u32x4 raw[UN];
+#pragma unroll
+  for (int u = 0; u < UN; u++) {
+    size_t i = mx4_vector<UN>(u);
+    i = i < nvec ? i : 0;
+    size_t at = i * N;
+    if constexpr (!FLAT) {
       const size_t row = i / vec_per_row;
-      at = row * row_stride + (i - row * vec_per_row) * 8;
+      at = row * row_stride + (i - row * vec_per_row) * N;
     }
-    float v[8];
-    R::load8(x + at, v);
-    uint32_t code;
-    codes[i] = mx4_quant8(v, code);
-    if ((threadIdx.x & 3) == 0) scales[i / 4] = (uint8_t)code;
+    raw[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(x + at));
+  }
+#pragma unroll
+  for (int u = 0; u < UN; u++) {
+    const size_t i = mx4_vector<UN>(u);
+    if (i >= nvec) continue;   // whole blocks: nvec is a multiple of LB
+    float v[N];
+    R::unpack(raw[u], v);
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < N; j++) m = max(m, abs_bits(v[j]));
+#pragma unroll
+    for (int o = 1; o < LB; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
+    const uint32_t code = mx4_scale_code(m);
+    if constexpr (N == 8) reinterpret_cast<uint32_t*>(codes)[i] = mx4_encode8(v, code);
+    else reinterpret_cast<uint16_t*>(codes)[i] = (uint16_t)mx4_encode4(f32x4{v[0], v[1], v[2], v[3]}, code);
+    if (threadIdx.x % LB == 0) scales[i / LB] = (uint8_t)code;
   }
 }
 
-// codes and scale codes -> values, eight a thread.
-template <typename R>
+// codes and scale codes -> values.
+template <typename R, int UN>
 __global__ void __launch_bounds__(kMx4Threads)
-mx4_dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales, size_t nvec,
+mx4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, size_t nvec,
                       typename R::elem* __restrict__ out) {
-  for (size_t i = (size_t)blockIdx.x * kMx4Threads + threadIdx.x; i < nvec; i += (size_t)gridDim.x * kMx4Threads) {
-    const uint32_t c = codes[i], s = scales[i / 4];
-    const float sc = mx4_scale_value(s);
-    float v[8];
+  constexpr int N = R::kVec, LB = 32 / N;
+  uint32_t c[UN], sc[UN];
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-      const uint32_t n = (c >> (4 * j)) & 15u, m = n & 7u;
+  for (int u = 0; u < UN; u++) {
+    size_t i = mx4_vector<UN>(u);
+    i = i < nvec ? i : 0;
+    if constexpr (N == 8) c[u] = reinterpret_cast<const uint32_t*>(codes)[i];
+    else c[u] = reinterpret_cast<const uint16_t*>(codes)[i];
+    sc[u] = scales[i / LB];
+  }
+#pragma unroll
+  for (int u = 0; u < UN; u++) {
+    const size_t i = mx4_vector<UN>(u);
+    if (i >= nvec) continue;
+    const float scale = sc[u] == 255u ? __uint_as_float(0x7fc00000u) : mx4_scale_value(sc[u]);
+    float v[N];
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+      const uint32_t n = (c[u] >> (4 * j)) & 15u, m = n & 7u;
       // magnitudes 0, 1/2, 1, 3/2, 2, 3, 4, 6 as floats, from the code's exponent and mantissa bits
       const float mag = m < 2 ? 0.5f * (float)m : __uint_as_float(((126u + (m >> 1)) << 23) | ((m & 1u) << 22));
-      const float a = s == 255u ? __uint_as_float(0x7fc00000u) : mag * sc;
-      v[j] = n & 8u ? -a : a;
+      v[j] = __uint_as_float(__float_as_uint(mag) | ((n & 8u) << 28)) * scale;
     }
-    R::store8(out + i * 8, v);
+    __builtin_nontemporal_store(R::pack(v), reinterpret_cast<u32x4*>(out + i * N));
   }
 }
 
@@ -85,7 +120,7 @@ mx4_quant_x_kernel(const uint16_t* __restrict__ x, uint32_t nvec, uint32_t vec_p
   const uint32_t i = blockIdx.x * kMx4Threads + threadIdx.x;
   if (i >= nvec) return;   // whole waves of four-lane blocks: nvec % 16 == 0
   float v[8];
-  RowBf16::load8(x + (size_t)i * 8, v);
+  row_load<RowBf16>(x + (size_t)i * 8, v);
   uint32_t code;
   xq[i] = mx4_quant8(v, code);
   if ((threadIdx.x & 3) == 0) {
@@ -128,26 +163,45 @@ static unsigned pass_grid(size_t n) {
   return (unsigned)(b < 4096 ? b : 4096);
 }
 
+// f(UN) with the workgroups of a pass over nvec vectors: four runs a wave from
+// 4 MiB of them on (fewer would leave compute units idle).
+template <typename F>
+static hipError_t mx4_pass(size_t nvec, F&& f) {
+  const size_t per = moe::kMx4Threads;
+  if (nvec >= (size_t)1 << 18) return f(std::integral_constant<int, 4>{}, dim3((unsigned)((nvec + 4 * per - 1) / (4 * per))));
+  return f(std::integral_constant<int, 1>{}, dim3((unsigned)((nvec + per - 1) / per)));
+}
+
 hipError_t launch_mx4_quantize(const void* x, int row_type, size_t rows, int cols, size_t row_stride, uint8_t* codes,
                                uint8_t* scales, hipStream_t s) {
-  const size_t nvec = rows * (size_t)(cols / 8);
   return moe::with_row_type(row_type, [&](auto r) {
     using R = decltype(r);
-    hipLaunchKernelGGL((moe::mx4_quantize_kernel<R>), dim3(pass_grid(nvec)), dim3(moe::kMx4Threads), 0, s,
-                       static_cast<const typename R::elem*>(x), nvec, (uint32_t)(cols / 8), row_stride,
-                       reinterpret_cast<uint32_t*>(codes), scales);
-    return hipGetLastError();
+    const uint32_t per_row = cols / R::kVec;
+    const size_t nvec = rows * (size_t)per_row;
+    const typename R::elem* p = static_cast<const typename R::elem*>(x);
+    return mx4_pass(nvec, [&](auto un, dim3 grid) {
+      constexpr int UN = decltype(un)::value;
+      if (row_stride == (size_t)cols)
+        hipLaunchKernelGGL((moe::mx4_quantize_kernel<R, UN, true>), grid, dim3(moe::kMx4Threads), 0, s, p, nvec,
+                           per_row, row_stride, codes, scales);
+      else
+        hipLaunchKernelGGL((moe::mx4_quantize_kernel<R, UN, false>), grid, dim3(moe::kMx4Threads), 0, s, p, nvec,
+                           per_row, row_stride, codes, scales);
+      return hipGetLastError();
+    });
   });
 }
 
 hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, size_t rows, int cols, int row_type,
                                  void* out, hipStream_t s) {
-  const size_t nvec = rows * (size_t)(cols / 8);
   return moe::with_row_type(row_type, [&](auto r) {
     using R = decltype(r);
-    hipLaunchKernelGGL((moe::mx4_dequantize_kernel<R>), dim3(pass_grid(nvec)), dim3(moe::kMx4Threads), 0, s,
-                       reinterpret_cast<const uint32_t*>(codes), scales, nvec, static_cast<typename R::elem*>(out));
-    return hipGetLastError();
+    const size_t nvec = rows * (size_t)(cols / R::kVec);
+    return mx4_pass(nvec, [&](auto un, dim3 grid) {
+      hipLaunchKernelGGL((moe::mx4_dequantize_kernel<R, decltype(un)::value>), grid, dim3(moe::kMx4Threads), 0, s,
+                         codes, scales, nvec, static_cast<typename R::elem*>(out));
+      return hipGetLastError();
+    });
   });
 }
 

@@ -182,7 +182,7 @@ mx4_stream_kernel(moe_host::Mx4Args g) {
         uint32_t mx = 0;
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-          h[i] = silu_f32(tot[i >> 2][i & 3]) * tot[2 + (i >> 2)][i & 3];
+          h[i] = mx4_silu(tot[i >> 2][i & 3]) * tot[2 + (i >> 2)][i & 3];
           mx = max(mx, abs_bits(h[i]));
         }
         mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16, 64));

@@ -11,27 +11,51 @@
 //    gate-up, half of 32 gate rows and the matching half of 32 up rows; down,
 //    32 output columns.
 //  * A stage is GS groups of G units of K.  Its token rows and their scale
-//    codes go to one of two LDS slots by direct global->LDS copies spread over
-//    the waves, while the other slot is multiplied.
+//    codes go to one of two LDS slots by direct buffer->LDS copies spread over
+//    the waves, while the other slot is multiplied.  (Buffer copies, not
+//    global ones: with those the compiler loses count of the vector-memory
+//    queue and waits for all of it at the first fragment of every stage.)
 //  * The wave's weights of a unit are loaded into the registers that the
-//    multiplication of the same unit of the stage before has just left, so a
-//    whole stage (8 KiB a wave at four units, 64 KiB a CU) stays in flight at
-//    the cost of one stage of registers, and the copies and loads run straight
-//    across work items.
+//    multiplication of the same unit has just left, D stages on: 8 KiB a wave
+//    and stage at four units, 64 KiB a CU, run straight across work items.
+//    Two stages instead of one: DeepSeek-V3-shaped gate-up, T = 4096, 920 ->
+//    868 us; Mixtral-shaped T = 512 136 -> 126 us.
+//  * Row blocks past the tile are copied and read but not multiplied.
 //  * Gate-up epilogue: 32 columns of h are one MXFP4 block a row, held by two
 //    neighbouring waves; they exchange the rows' largest magnitudes through
 //    LDS and write codes and scale codes in the blocks that the down GEMM
 //    copies as contiguous chunks.  Down writes bf16 rows, 16 bytes a lane.
 //
-// Every wave issues the same number of vector-memory operations a stage
-// (copies past the tile's chunks repeat an earlier one, bytes and place), so
-// the wait at the head of a stage is an exact count.
+// A wave's copies of a stage come before its weight loads of the same stage,
+// whose number is fixed, so the wait at the head of a stage is an exact count.
+//
+// Measured (us, TB/s of weights with their scale codes): DeepSeek-V3-shaped
+// gate-up / down at T = 1024 609 (6.6) / 369 (5.4), at 4096 868 (4.6) / 486
+// (4.1).  Per CU a stage moves 70 KiB of weights and 17 to 52 KiB of token
+// rows, about 30 GB/s in all at every tile height, with the MFMA busy 29% of
+// the time at T = 4096 and the L1 stalled on pending data for 57%: what bounds
+// it is the CU's path to memory, which the token rows share with the weights.
 #include "lds_dma.h"
 #include "mx4_epilogue.h"
 
 namespace moe {
 
 constexpr int kMx4Waves = 8;
+// Row blocks x units of a stage up to which the registers hold two stages of
+// weights (above, the accumulators leave room for one).
+constexpr int kMx4TwoAhead = 40;
+
+// Direct buffer->LDS copies (a lane's N bytes at base + off + soff, to its
+// place after dst).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const char* base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, 0xffffffffu, 0x00027000);
+}
+__device__ __forceinline__ void buf_dma16(__amdgpu_buffer_rsrc_t r, uint32_t off, int soff, char* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 16, off, soff, 0, 0);
+}
+__device__ __forceinline__ void buf_dma4(__amdgpu_buffer_rsrc_t r, uint32_t off, int soff, char* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 4, off, soff, 0, 0);
+}
 
 template <int MB, int G, int GS>
 struct Mx4Stage {
@@ -41,93 +65,136 @@ struct Mx4Stage {
   static constexpr int NW = 2 * U + 2 * GS;                          // weight loads of a wave
   static constexpr int kTokens = MB * U * 1024;
   static constexpr int kSlot = kTokens + MB * GS * 256;
-  static constexpr int kLds = 2 * kSlot + kMx4Waves * MB * 16 * 4;
+  static constexpr int kRows = MB * 16;
+  static constexpr int kPairs = (kRows + 63) / 64 * 64;              // whole copies
 };
+
+// Item `item` of the grid's order: a task tile (task ti, rows row_begin ..
+// + rows of `expert`) and a strip nt of its expert's weights.  An expert's
+// tiles take a strip one after another, so that its weights, once in L2,
+// serve them all; the strips of one tile stand side by side where an expert
+// has one tile, and meet its token rows in L2.
+struct Mx4Place {
+  int ti, nt, expert, row_begin, rows;
+};
+
+template <int MB>
+__device__ __forceinline__ Mx4Place mx4_place(const moe_host::Mx4Args& g, int item, int n_strips) {
+  Mx4Place p;
+  p.ti = item / n_strips;
+  p.nt = item - p.ti * n_strips;
+  const moe_task_t t = load_task_scalar(g.tasks + p.ti);
+  p.expert = t.expert;
+  p.row_begin = t.row_begin;
+  p.rows = t.rows;
+  const int begin = load1_scalar(g.expert_offsets + t.expert), end = load1_scalar(g.expert_offsets + t.expert + 1);
+  const int tiles = (end - begin + 16 * MB - 1) / (16 * MB);
+  if (tiles > 1) {
+    const int first = p.ti - (t.row_begin - begin) / (16 * MB), local = item - first * n_strips;
+    const int j = local % tiles;
+    p.nt = local / tiles;
+    p.ti = first + j;
+    p.row_begin = begin + 16 * MB * j;
+    p.rows = min(16 * MB, end - p.row_begin);
+  }
+  return p;
+}
 
 template <int MB, int G, int GS>
 struct Mx4Item {
   using St = Mx4Stage<MB, G, GS>;
-  int ti, row_begin, rows;
-  int blk0;                        // gate-up: first of the 32-column pair's blocks; down: the wave's first block
-  bool store;                      // the wave's columns exist (down: H may end inside a strip)
+  Mx4Place at;
   const char* abase;               // of the offsets a[] (and, down, s[]): uniform
   uint32_t a[St::NA], s[St::NS];   // this lane's byte offsets
-  const char* b[2];                // the wave's weight blocks: uniform
 };
 
+// The item's token sources.  pairs: the pair index of each of the tile's rows
+// (LDS; gate-up only); inv_topk: 2^20 / topk rounded up (pair * inv_topk >> 20
+// is pair / topk: pair < 2^16, topk <= 16).
 template <int MB, int G, int GS, bool GATEUP>
-__device__ __forceinline__ Mx4Item<MB, G, GS> mx4_item(const moe_host::Mx4Args& g, int item, int n_strips, int wave,
-                                                       int lane) {
+__device__ __forceinline__ Mx4Item<MB, G, GS> mx4_item(const moe_host::Mx4Args& g, const Mx4Place& at, const int* pairs,
+                                                       uint32_t inv_topk, int wave, int lane) {
   using St = Mx4Stage<MB, G, GS>;
   Mx4Item<MB, G, GS> it;
-  const int units = g.K / 128;
-  const uint32_t block_bytes = (uint32_t)units * kMx4Unit;
-  it.ti = item / n_strips;
-  const int nt = item - it.ti * n_strips;   // the strips of one tile side by side: they meet its token rows in L2
-  const moe_task_t task = load_task_scalar(g.tasks + it.ti);
-  it.row_begin = task.row_begin;
-  it.rows = task.rows;
+  const uint32_t block_bytes = (uint32_t)(g.K / 128) * kMx4Unit;
+  it.at = at;
   // x codes take at most 2^31 bytes (T H / 2), a task's blocks of h far less:
   // 32-bit offsets from a uniform base
-  it.abase = static_cast<const char*>(g.a) + (GATEUP ? 0 : (size_t)it.ti * MB * block_bytes);
-  // row blocks past the tile, and rows past it inside the last block, re-read
-  // the tile's first row (gate-up) or block: valid, never stored
+  it.abase = static_cast<const char*>(g.a) + (GATEUP ? 0 : (size_t)at.ti * MB * block_bytes);
+  // rows past the tile re-read its last row (gate-up; a whole block of them
+  // one line) or its first block (down): valid addresses, never stored
 #pragma unroll
   for (int i = 0; i < St::NA; i++) {
     const int c = (wave + kMx4Waves * i) % (MB * St::U);   // chunk: row block c / U, unit c % U
     const int rb = c / St::U, u = c % St::U;
-    const bool in = rb * 16 < task.rows;
     if constexpr (GATEUP) {
-      const int crow = tok_copy_row(lane);
-      const i32x16_t sp = load16_scalar(g.sorted_pairs + task.row_begin + (in ? rb * 16 : 0));
-      const int p = in && rb * 16 + crow < task.rows ? pick16(sp, crow) : sp[0];
-      it.a[i] = (uint32_t)(p / g.topk) * (uint32_t)(g.K / 2) + u * 64 + 16 * tok_copy_piece(lane);
+      const uint32_t tok = (uint32_t)pairs[rb * 16 + tok_copy_row(lane)] * inv_topk >> 20;
+      it.a[i] = tok * (uint32_t)(g.K / 2) + u * 64 + 16 * tok_copy_piece(lane);
     } else {
-      it.a[i] = (in ? rb : 0) * block_bytes + u / G * (G * kMx4Unit) + u % G * 1024 + 16 * lane;
+      it.a[i] = (rb * 16 < at.rows ? rb : 0) * block_bytes + u / G * (G * kMx4Unit) + u % G * 1024 + 16 * lane;
     }
   }
 #pragma unroll
   for (int i = 0; i < St::NS; i++) {
     const int c = (wave + kMx4Waves * i) % (MB * GS);      // row block c / GS, group c % GS
     const int rb = c / GS, j = c % GS;
-    const bool in = rb * 16 < task.rows;
     if constexpr (GATEUP) {
-      const int lrow = lane & 15;
-      const i32x16_t sp = load16_scalar(g.sorted_pairs + task.row_begin + (in ? rb * 16 : 0));
-      const int p = in && rb * 16 + lrow < task.rows ? spread16(sp, lane) : sp[0];
-      it.s[i] = (uint32_t)(p / g.topk) * (uint32_t)(g.K / 32) + 4 * G * j + (((lane >> 4) * G) & ~3);
+      const uint32_t tok = (uint32_t)pairs[rb * 16 + (lane & 15)] * inv_topk >> 20;
+      it.s[i] = tok * (uint32_t)(g.K / 32) + 4 * G * j + (((lane >> 4) * G) & ~3);
     } else {
-      it.s[i] = (in ? rb : 0) * block_bytes + j * (G * kMx4Unit) + G * 1024 + ((lane * G) & ~3);
+      it.s[i] = (rb * 16 < at.rows ? rb : 0) * block_bytes + j * (G * kMx4Unit) + G * 1024 + ((lane * G) & ~3);
     }
   }
-  int b0, b1;
-  if constexpr (GATEUP) {
-    it.blk0 = 8 * nt + (wave & ~1);   // 128 h columns a strip, 32 a pair of waves
-    b0 = it.blk0 + (wave & 1);
-    b1 = b0 + g.N_out / 16;
-    it.store = true;
-  } else {
-    it.blk0 = 16 * nt + 2 * wave;
-    it.store = it.blk0 < g.N_out / 16;
-    b0 = it.store ? it.blk0 : 0;
-    b1 = b0 + 1;
-  }
-  const char* B = static_cast<const char*>(g.b) + (size_t)task.expert * (g.w_rows / 16) * block_bytes;
-  it.b[0] = B + (size_t)b0 * block_bytes;
-  it.b[1] = B + (size_t)b1 * block_bytes;
   return it;
 }
 
-template <int MB, int G, int GS, bool GATEUP>
+// The wave's two 16-row weight blocks in strip nt.
+struct Mx4Blocks {
+  int out;      // gate-up: first block of the 32 columns of h that a pair of waves forms; down: the first block
+  bool store;   // they exist (down: H may end inside a strip; else block 0 is read and nothing stored)
+  const char *b0, *b1;
+};
+
+template <bool GATEUP>
+__device__ __forceinline__ Mx4Blocks mx4_blocks(const moe_host::Mx4Args& g, const Mx4Place& at, int wave) {
+  Mx4Blocks r;
+  const size_t block_bytes = (size_t)(g.K / 128) * kMx4Unit;
+  int b0, b1;
+  if constexpr (GATEUP) {
+    r.out = 8 * at.nt + (wave & ~1);   // 128 columns of h a strip, 32 a pair of waves
+    r.store = true;
+    b0 = r.out + (wave & 1);
+    b1 = b0 + g.N_out / 16;
+  } else {
+    r.out = 16 * at.nt + 2 * wave;
+    r.store = r.out < g.N_out / 16;
+    b0 = r.store ? r.out : 0;
+    b1 = b0 + 1;
+  }
+  const char* B = static_cast<const char*>(g.b) + (size_t)at.expert * (g.w_rows / 16) * block_bytes;
+  r.b0 = B + (size_t)b0 * block_bytes;
+  r.b1 = B + (size_t)b1 * block_bytes;
+  return r;
+}
+
+template <int MB, int G, int GS, int D, bool GATEUP>
 __global__ void __launch_bounds__(kMx4Waves * 64, 1)
 mx4_strip_kernel(moe_host::Mx4Args g) {
   using St = Mx4Stage<MB, G, GS>;
   using It = Mx4Item<MB, G, GS>;
   constexpr int U = St::U;
-  static_assert(MB % 4 == 0, "row blocks are read four at a time");
-  static_assert(St::NW < 64, "vmcnt range");
-  extern __shared__ __attribute__((aligned(1024))) char lds[];
-  uint32_t* amax = reinterpret_cast<uint32_t*>(lds + 2 * St::kSlot);   // [wave][16 MB rows]
+  constexpr int CH = 2, NC = MB / CH;   // row blocks multiplied at a time, and how many times
+  static_assert(MB % CH == 0, "whole chunks of row blocks");
+  static_assert(D == 1 || D == 2, "weights one or two stages ahead (a stage of either slot has its own)");
+  static_assert(St::NA + St::NS + St::NW < 64, "vmcnt range");
+  // The two slots are two variables, and a stage is compiled for each: the
+  // compiler then knows that a fragment read from one does not have to wait
+  // for copies into the other (with one array it waits, at the head of every
+  // stage, for the copies that the stage has just issued).
+  __shared__ __attribute__((aligned(1024))) char slot0[St::kSlot];
+  __shared__ __attribute__((aligned(1024))) char slot1[St::kSlot];
+  __shared__ uint32_t amax[kMx4Waves * St::kRows];
+  __shared__ int pairs[3 * St::kPairs];   // the pair indices of three items
   const int lane = threadIdx.x & 63;
   const int lrow = lane & 15, lgrp = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -156,51 +223,98 @@ mx4_strip_kernel(moe_host::Mx4Args g) {
   // expert has several tiles the later ones find them in L2 (ordinary loads).
   auto body = [&](auto nt_tag) {
     constexpr bool NT_B = decltype(nt_tag)::value;
-    It cur = mx4_item<MB, G, GS, GATEUP>(g, vid, n_strips, wave, lane);
-    It nxt = cur;   // past the last item its own first stage again: valid, never used
-    if (n_items > 1) nxt = mx4_item<MB, G, GS, GATEUP>(g, vid + gs, n_strips, wave, lane);
+    // The sources of an item are formed one item ahead of its first stage,
+    // from pair indices that were copied to LDS an item earlier still (three
+    // places, so that no wave overwrites what another still reads).  Past the
+    // last item: the last one again, its first stage loaded and never used.
+    const uint32_t inv_topk = ((1u << 20) + g.topk - 1) / g.topk;
+    auto place = [&](int i) __attribute__((always_inline)) { return mx4_place<MB>(g, vid + min(i, n_items - 1) * gs, n_strips); };
+    auto copy_pairs = [&](const Mx4Place& p, int i) __attribute__((always_inline)) {
+      if constexpr (GATEUP) {
+        const auto r = rows_rsrc(reinterpret_cast<const char*>(g.sorted_pairs + p.row_begin));
+#pragma unroll
+        for (int r0 = 0; r0 < St::kRows; r0 += 64)   // every wave all of them: no branch round a copy
+          buf_dma4(r, 4 * min(r0 + lane, p.rows - 1), 0, reinterpret_cast<char*>(pairs + i % 3 * St::kPairs + r0));
+      }
+    };
+    auto sources = [&](const Mx4Place& p, int i) __attribute__((always_inline)) {
+      return mx4_item<MB, G, GS, GATEUP>(g, p, pairs + i % 3 * St::kPairs, inv_topk, wave, lane);
+    };
+    const Mx4Place place0 = place(0), place1 = place(1);
+    Mx4Place ahead = place(2);   // the item whose pairs are on their way
+    copy_pairs(place0, 0);
+    copy_pairs(place1, 1);
+    copy_pairs(ahead, 2);
+    wait_vm<0>();
+    barrier_nofence();
+    It cur = sources(place0, 0), nxt = sources(place1, 1);
 
     auto issue_tokens = [&](bool in_cur, int kt, char* slot) __attribute__((always_inline)) {
-      const size_t at = GATEUP ? (size_t)kt * (U * 64) : (size_t)kt * (U * kMx4Unit);
-      const char* as = (in_cur ? cur.abase : nxt.abase) + at;
-      const char* ss = GATEUP ? reinterpret_cast<const char*>(g.a_sc) + (size_t)kt * (4 * U) : as;
+      const int at = kt * (GATEUP ? U * 64 : U * kMx4Unit);
+      const auto ra = rows_rsrc(in_cur ? cur.abase : nxt.abase);
+      const auto rs = GATEUP ? rows_rsrc(reinterpret_cast<const char*>(g.a_sc)) : ra;
 #pragma unroll
       for (int i = 0; i < St::NA; i++)
-        dma16(as + (in_cur ? cur.a[i] : nxt.a[i]), slot + ((wave + kMx4Waves * i) % (MB * U)) * 1024);
+        buf_dma16(ra, in_cur ? cur.a[i] : nxt.a[i], at, slot + ((wave + kMx4Waves * i) % (MB * U)) * 1024);
 #pragma unroll
       for (int i = 0; i < St::NS; i++)
-        dma4(ss + (in_cur ? cur.s[i] : nxt.s[i]), slot + St::kTokens + ((wave + kMx4Waves * i) % (MB * GS)) * 256);
+        buf_dma4(rs, in_cur ? cur.s[i] : nxt.s[i], GATEUP ? kt * (4 * U) : at,
+                 slot + St::kTokens + ((wave + kMx4Waves * i) % (MB * GS)) * 256);
     };
-    u32x4 w[U][2];
-    uint32_t sw[GS][2];
-    auto load_unit = [&](const char* b0, const char* b1, int u) __attribute__((always_inline)) {
+
+    // Weights run D stages ahead of the multiplication, over the items by
+    // themselves: stage wk of item wi is the next to be loaded.
+    Mx4Blocks wb = mx4_blocks<GATEUP>(g, place0, wave);
+    int wk = 0, wi = 0;
+    auto next_weights = [&]() __attribute__((always_inline)) {
+      if (++wk == nk) {
+        wk = 0;
+        if (++wi < n_items) wb = mx4_blocks<GATEUP>(g, place(wi), wave);
+      }
+    };
+    u32x4 w[D][U][2];
+    uint32_t sw[GS][2], swn[D][GS][2];   // scale codes of this stage, and those on their way
+    auto load_unit = [&](u32x4 (&to)[2], const char* b0, const char* b1, int u) __attribute__((always_inline)) {
       const int at = u / G * (G * kMx4Unit) + u % G * 1024;
       const u32x4* p0 = reinterpret_cast<const u32x4*>(b0 + at + wlane);
       const u32x4* p1 = reinterpret_cast<const u32x4*>(b1 + at + wlane);
-      w[u][0] = NT_B ? __builtin_nontemporal_load(p0) : *p0;
-      w[u][1] = NT_B ? __builtin_nontemporal_load(p1) : *p1;
-      if (u % G == G - 1) {   // the group's scale codes with its last unit
-        const uint32_t* q0 = reinterpret_cast<const uint32_t*>(b0 + u / G * (G * kMx4Unit) + slane);
-        const uint32_t* q1 = reinterpret_cast<const uint32_t*>(b1 + u / G * (G * kMx4Unit) + slane);
-        sw[u / G][0] = NT_B ? __builtin_nontemporal_load(q0) : *q0;
-        sw[u / G][1] = NT_B ? __builtin_nontemporal_load(q1) : *q1;
+      to[0] = NT_B ? __builtin_nontemporal_load(p0) : *p0;
+      to[1] = NT_B ? __builtin_nontemporal_load(p1) : *p1;
+    };
+    auto load_scales = [&](uint32_t (&to)[GS][2], const char* b0, const char* b1) __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < GS; j++) {
+        const uint32_t* q0 = reinterpret_cast<const uint32_t*>(b0 + j * (G * kMx4Unit) + slane);
+        const uint32_t* q1 = reinterpret_cast<const uint32_t*>(b1 + j * (G * kMx4Unit) + slane);
+        to[j][0] = NT_B ? __builtin_nontemporal_load(q0) : *q0;
+        to[j][1] = NT_B ? __builtin_nontemporal_load(q1) : *q1;
       }
     };
     // The empty asm statements keep the copies ahead of the weights in issue
     // order, which the vmcnt count relies on.
-    issue_tokens(true, 0, lds);
+    issue_tokens(true, 0, slot0);
     __asm__ volatile("" ::: "memory");
 #pragma unroll
-    for (int u = 0; u < U; u++) load_unit(cur.b[0], cur.b[1], u);
-    __asm__ volatile("" ::: "memory");
+    for (int d = 0; d < D; d++) {
+      const size_t at = (size_t)wk * (U * kMx4Unit);
+      load_scales(swn[d], wb.b0 + at, wb.b1 + at);
+#pragma unroll
+      for (int u = 0; u < U; u++) load_unit(w[d][u], wb.b0 + at, wb.b1 + at, u);
+      __asm__ volatile("" ::: "memory");
+      next_weights();
+    }
 
-    int par = 0;   // LDS slot of the stage
-    for (int ii = 0; ii < n_items; ii++) {
-      f32x4 acc[MB][2];
+    f32x4 acc[MB][2];
+    auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
       for (int m = 0; m < MB; m++) acc[m][0] = acc[m][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    };
+    clear();
+    int ii = 0;
 
-      for (int kt = 0; kt < nk; kt++, par ^= 1) {
+    // One stage (kt of the item) from slot sb, the next one's copies into `next`; w_, swn_: the
+    // stage's weights, replaced by those of D stages on.
+    auto stage = [&](int kt, const char* sb, char* next, u32x4 (&w_)[U][2], uint32_t (&swn_)[GS][2]) __attribute__((always_inline)) {
         // the stage's copies have landed in this wave (only its weights were
         // issued after them), then in every wave
         __asm__ volatile("" ::: "memory");
@@ -208,25 +322,30 @@ mx4_strip_kernel(moe_host::Mx4Args g) {
         barrier_nofence();
         // the next stage into the slot that every wave had read before the barrier
         const bool in_cur = kt + 1 < nk;
-        const int kn = in_cur ? kt + 1 : 0;
-        issue_tokens(in_cur, kn, lds + (par ^ 1) * St::kSlot);
+        issue_tokens(in_cur, in_cur ? kt + 1 : 0, next);
         __asm__ volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
-        const char* b0 = (in_cur ? cur.b[0] : nxt.b[0]) + (size_t)kn * (U * kMx4Unit);
-        const char* b1 = (in_cur ? cur.b[1] : nxt.b[1]) + (size_t)kn * (U * kMx4Unit);
-        const char* sb = lds + par * St::kSlot;
-        const uint32_t* sc = reinterpret_cast<const uint32_t*>(sb + St::kTokens);
-        // four row blocks at a time, their fragments read while the previous
-        // four are multiplied; the scheduling barriers keep the compiler from
-        // reading more of them ahead than there are registers for
-        u32x4 t[2][4];
-        uint32_t st[MB];
-        auto read4 = [&](u32x4 (&to)[4], int step) __attribute__((always_inline)) {
+        const char* b0 = wb.b0 + (size_t)wk * (U * kMx4Unit);
+        const char* b1 = wb.b1 + (size_t)wk * (U * kMx4Unit);
 #pragma unroll
-          for (int i = 0; i < 4; i++)
-            to[i] = *reinterpret_cast<const u32x4*>(sb + ((step % (MB / 4) * 4 + i) * U + step / (MB / 4)) * 1024 + aoff);
+        for (int j = 0; j < GS; j++)
+#pragma unroll
+          for (int q = 0; q < 2; q++) sw[j][q] = swn_[j][q] >> bsh;
+        load_scales(swn_, b0, b1);
+        const uint32_t* sc = reinterpret_cast<const uint32_t*>(sb + St::kTokens);
+        // CH row blocks at a time, their fragments read while the previous
+        // ones are multiplied; the scheduling barriers keep the compiler from
+        // reading more of them ahead than there are registers for.  Blocks past
+        // the tile are read but not multiplied.
+        const int chunks = (cur.at.rows + 16 * CH - 1) / (16 * CH);
+        u32x4 t[2][CH];
+        uint32_t st[MB];
+        auto read = [&](u32x4 (&to)[CH], int step) __attribute__((always_inline)) {
+#pragma unroll
+          for (int i = 0; i < CH; i++)
+            to[i] = *reinterpret_cast<const u32x4*>(sb + ((step % NC * CH + i) * U + step / NC) * 1024 + aoff);
         };
-        read4(t[0], 0);
+        read(t[0], 0);
 #pragma unroll
         for (int j = 0; j < GS; j++) {
 #pragma unroll
@@ -234,33 +353,45 @@ mx4_strip_kernel(moe_host::Mx4Args g) {
           mx4_units<G>([&](auto uu) {
             constexpr int V = decltype(uu)::value;
             const int un = j * G + V;
+            // (uses outside the branch below, so that the waits for the loads stand
+            // here and count exactly; under a branch the compiler waits for
+            // everything in flight)
+            __asm__ volatile("" : "+v"(w_[un][0]), "+v"(w_[un][1]));
 #pragma unroll
-            for (int mc = 0; mc < MB / 4; mc++) {
-              const int step = un * (MB / 4) + mc;
-              if (step + 1 < U * (MB / 4)) read4(t[(step + 1) & 1], step + 1);
+            for (int mc = 0; mc < NC; mc++) {
+              const int step = un * NC + mc;
+              if (step + 1 < U * NC) read(t[(step + 1) & 1], step + 1);
               __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-              for (int i = 0; i < 4; i++) {
-                mfma_mx4<V>(acc[4 * mc + i][0], w[un][0], t[step & 1][i], sw[j][0] >> bsh, st[4 * mc + i]);
-                mfma_mx4<V>(acc[4 * mc + i][1], w[un][1], t[step & 1][i], sw[j][1] >> bsh, st[4 * mc + i]);
+              for (int i = 0; i < CH; i++) __asm__ volatile("" : "+v"(t[step & 1][i]));
+              if (mc < chunks) {
+#pragma unroll
+                for (int i = 0; i < CH; i++) {
+                  mfma_mx4<V>(acc[CH * mc + i][0], w_[un][0], t[step & 1][i], sw[j][0], st[CH * mc + i]);
+                  mfma_mx4<V>(acc[CH * mc + i][1], w_[un][1], t[step & 1][i], sw[j][1], st[CH * mc + i]);
+                }
               }
               __builtin_amdgcn_sched_barrier(0);
             }
-            load_unit(b0, b1, un);   // of the next stage
+            load_unit(w_[un], b0, b1, un);
             __builtin_amdgcn_sched_barrier(0);
           });
         }
-      }
-
+        next_weights();
+      };
+    // The item's results, and the next item's turn.
+    auto finish = [&]() __attribute__((always_inline)) {
+      const Mx4Blocks blk = mx4_blocks<GATEUP>(g, cur.at, wave);
       if constexpr (GATEUP) {
         // h = SiLU(gate) * up in place of the gate sums; the row's largest
         // magnitude over this wave's 16 columns to LDS
 #pragma unroll
         for (int m = 0; m < MB; m++) {
+          if (16 * m >= cur.at.rows) break;
           uint32_t mx = 0;
 #pragma unroll
           for (int i = 0; i < 4; i++) {
-            acc[m][0][i] = silu_f32(acc[m][0][i]) * acc[m][1][i];
+            acc[m][0][i] = mx4_silu(acc[m][0][i]) * acc[m][1][i];
             mx = max(mx, abs_bits(acc[m][0][i]));
           }
           mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16, 64));
@@ -270,31 +401,56 @@ mx4_strip_kernel(moe_host::Mx4Args g) {
         __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the writes are in LDS
         barrier_nofence();
         // (the next write of `amax` comes after the barriers of the next item's stages)
+        const Mx4Out o = mx4_out(g.c, (size_t)cur.at.ti * MB, blk.out / 2, units2, G2);
+        // whole blocks, also of rows past the tile's last one: their places are
+        // this task's and never read
 #pragma unroll
         for (int m = 0; m < MB; m++) {
+          if (16 * m >= cur.at.rows) break;
           const uint32_t mx = max(amax[(wave * MB + m) * 16 + lrow], amax[((wave ^ 1) * MB + m) * 16 + lrow]);
           const uint32_t code = mx4_scale_code(mx);
-          const uint32_t w4 = mx4_encode4(acc[m][0], code);
-          if (16 * m + lrow < cur.rows) {
-            const Mx4Out o = mx4_out(g.c, (size_t)cur.ti * MB + m, cur.blk0 / 2, units2, G2);
-            *reinterpret_cast<uint16_t*>(o.codes + 16 * lrow + 4 * lgrp + 2 * (wave & 1)) = (uint16_t)w4;
-            if (lgrp == 0 && (wave & 1) == 0) o.scale[lrow * o.G] = (char)code;
-          }
+          const uint32_t at = m * (uint32_t)units2 * kMx4Unit;
+          *reinterpret_cast<uint16_t*>(o.codes + at + 16 * lrow + 4 * lgrp + 2 * (wave & 1)) =
+              (uint16_t)mx4_encode4(acc[m][0], code);
+          o.scale[at + lrow * o.G] = (char)code;   // (the same byte from every lane and wave of the row)
         }
       } else {
+        // rows past the tile are out of the buffer's bounds and dropped
+        const auto y = __builtin_amdgcn_make_buffer_rsrc(static_cast<uint16_t*>(g.c) + (size_t)cur.at.row_begin * g.N_out, 0,
+                                                         blk.store ? cur.at.rows * g.N_out * 2 : 0, 0x00027000);
 #pragma unroll
         for (int m = 0; m < MB; m++) {
-          if (16 * m + lrow < cur.rows && cur.store) {
-            u32x4 v;
+          if (16 * m >= cur.at.rows) break;
+          u32x4 v;
 #pragma unroll
-            for (int i = 0; i < 4; i++) v[i] = bf16_pair(acc[m][i >> 1][2 * (i & 1)], acc[m][i >> 1][2 * (i & 1) + 1]);
-            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(g.c) + (size_t)(cur.row_begin + 16 * m + lrow) * g.N_out +
-                                      16 * cur.blk0 + 8 * lgrp) = v;
-          }
+          for (int i = 0; i < 4; i++) v[i] = bf16_pair(acc[m][i >> 1][2 * (i & 1)], acc[m][i >> 1][2 * (i & 1) + 1]);
+          __builtin_amdgcn_raw_buffer_store_b128(v, y, ((16 * m + lrow) * g.N_out + 16 * blk.out + 8 * lgrp) * 2, 0, 0);
         }
       }
+      clear();
       cur = nxt;
-      if (ii + 2 < n_items) nxt = mx4_item<MB, G, GS, GATEUP>(g, vid + (ii + 2) * gs, n_strips, wave, lane);
+      // the pair copies of the finish before this one are older than a whole
+      // stage's operations
+      wait_vm<St::NA + St::NS + St::NW>();
+      nxt = sources(ahead, ii + 2);
+      ahead = place(ii + 3);
+      copy_pairs(ahead, ii + 3);
+      ii++;
+    };
+    // stages in turn, the slots with them, straight across items
+    for (int kt = 0;;) {
+      stage(kt, slot0, slot1, w[0], swn[0]);
+      if (++kt == nk) {
+        finish();
+        kt = 0;
+        if (ii == n_items) break;
+      }
+      stage(kt, slot1, slot0, w[D - 1], swn[D - 1]);
+      if (++kt == nk) {
+        finish();
+        kt = 0;
+        if (ii == n_items) break;
+      }
     }
     // the trailing re-loads still write this workgroup's LDS: let them land
     wait_vm<0>();
@@ -305,13 +461,8 @@ mx4_strip_kernel(moe_host::Mx4Args g) {
 
 template <int MB, int G, int GS, bool GATEUP>
 static hipError_t launch_mx4_strip_t(const moe_host::Mx4Args& a, int grid, hipStream_t s) {
-  constexpr int lds_bytes = Mx4Stage<MB, G, GS>::kLds;
-  static_assert(lds_bytes <= 160 * 1024, "LDS of a CU");
-  // (an attribute of the function on the current device; set before every launch)
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&mx4_strip_kernel<MB, G, GS, GATEUP>),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, lds_bytes);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((mx4_strip_kernel<MB, G, GS, GATEUP>), dim3(grid), dim3(kMx4Waves * 64), lds_bytes, s, a);
+  hipLaunchKernelGGL((mx4_strip_kernel<MB, G, GS, MB * G * GS <= kMx4TwoAhead ? 2 : 1, GATEUP>), dim3(grid),
+                     dim3(kMx4Waves * 64), 0, s, a);
   return hipGetLastError();
 }
 
@@ -338,7 +489,7 @@ hipError_t launch_mx4_strip(const Mx4Args& a, bool gateup, int mb, int grid, hip
   if (a.K % 128 || a.N_out % 128 || a.w_rows != (gateup ? 2 : 1) * a.N_out) return hipErrorInvalidValue;
 #define MOE_MX4_CASE(M) \
   if (mb == M) return gateup ? moe::launch_mx4_strip_g<M, true>(a, grid, s) : moe::launch_mx4_strip_g<M, false>(a, grid, s);
-  MOE_MX4_CASE(4) MOE_MX4_CASE(8) MOE_MX4_CASE(12)
+  MOE_MX4_CASE(4) MOE_MX4_CASE(6) MOE_MX4_CASE(8) MOE_MX4_CASE(10) MOE_MX4_CASE(12)
 #undef MOE_MX4_CASE
   return hipErrorInvalidValue;
 }

@@ -9,8 +9,8 @@
 // Each is the other's gradient with respect to the rows; the gradient of
 // the weights is dw[p] = <rows[r], tokens[t]>, with dw[p] = 0 for a dropped
 // pair.  All of them are bound by the rows' bytes, so every kernel reads
-// each row once: a thread holds eight columns of its token in registers and
-// goes through the token's k pairs.  Sums run in fp32 in ascending j and are
+// each row once: a thread holds 16 bytes of its token in registers and goes
+// through the token's k pairs.  Sums run in fp32 in ascending j and are
 // rounded once; rows behind the last valid one are not written.
 //
 // A position outside [0, valid) counts as dropped, so a routing buffer that
@@ -38,22 +38,23 @@ template <typename R, int KM>
 __global__ void __launch_bounds__(kMoveThreads)
 rows_to_experts_kernel(moe_host::RowMoveArgs g) {
   typedef typename R::elem elem;
+  constexpr int N = R::kVec;
   const int t = blockIdx.x;
-  const int c = (blockIdx.y * kMoveThreads + threadIdx.x) * 8;
+  const int c = (blockIdx.y * kMoveThreads + threadIdx.x) * N;
   if (c >= g.H) return;
-  float v[8];
-  R::load8(static_cast<const elem*>(g.tokens) + (size_t)t * g.H + c, v);
+  float v[N];
+  row_load<R>(static_cast<const elem*>(g.tokens) + (size_t)t * g.H + c, v);
   int row[KM];
   float w[KM];
   pair_rows<KM>(g, t, row, w);
-  elem* out = static_cast<elem*>(g.out);
+  elem* out = static_cast<elem*>(g.out) + c;
 #pragma unroll
   for (int j = 0; j < KM; j++) {
     if (row[j] < 0) continue;
-    float o[8];
+    float o[N];
 #pragma unroll
-    for (int i = 0; i < 8; i++) o[i] = w[j] * v[i];
-    R::store8(out + (size_t)row[j] * g.H + c, o);
+    for (int i = 0; i < N; i++) o[i] = w[j] * v[i];
+    __builtin_nontemporal_store(R::pack(o), reinterpret_cast<u32x4*>(out + (size_t)row[j] * g.H));
   }
 }
 
@@ -61,26 +62,31 @@ template <typename R, int KM>
 __global__ void __launch_bounds__(kMoveThreads)
 rows_to_tokens_kernel(moe_host::RowMoveArgs g) {
   typedef typename R::elem elem;
+  constexpr int N = R::kVec;
   const int t = blockIdx.x;
-  const int c = (blockIdx.y * kMoveThreads + threadIdx.x) * 8;
+  const int c = (blockIdx.y * kMoveThreads + threadIdx.x) * N;
   if (c >= g.H) return;
   int row[KM];
   float w[KM];
   pair_rows<KM>(g, t, row, w);
-  const elem* rows = static_cast<const elem*>(g.rows);
-  float v[KM][8];
+  const elem* rows = static_cast<const elem*>(g.rows) + c;
+  // every row's load ahead of the first use; a dropped pair's is of row 0 and
+  // takes no part (a load under a condition would wait for the ones before it)
+  u32x4 raw[KM];
+#pragma unroll
+  for (int j = 0; j < KM; j++)
+    raw[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(rows + (size_t)max(row[j], 0) * g.H));
+  float acc[N];
+#pragma unroll
+  for (int i = 0; i < N; i++) acc[i] = 0.0f;
 #pragma unroll
   for (int j = 0; j < KM; j++) {
-    if (row[j] >= 0) R::load8(rows + (size_t)row[j] * g.H + c, v[j]);
-  }
-  float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    float v[N];
+    R::unpack(raw[j], v);
 #pragma unroll
-  for (int j = 0; j < KM; j++) {
-    if (row[j] < 0) continue;
-#pragma unroll
-    for (int i = 0; i < 8; i++) acc[i] += w[j] * v[j][i];
+    for (int i = 0; i < N; i++) acc[i] = row[j] < 0 ? acc[i] : acc[i] + w[j] * v[i];
   }
-  R::store8(static_cast<elem*>(g.out) + (size_t)t * g.H + c, acc);
+  row_store<R>(static_cast<elem*>(g.out) + (size_t)t * g.H + c, acc);
 }
 
 // The gradients with the weights': WPT waves a token.  TO_TOKENS (the
@@ -91,6 +97,7 @@ template <typename R, int KM, int WPT, bool TO_TOKENS>
 __global__ void __launch_bounds__(WPT < 4 ? kMoveThreads : WPT * 64)
 rows_grad_kernel(moe_host::RowMoveArgs g) {
   typedef typename R::elem elem;
+  constexpr int N = R::kVec;
   constexpr int TPB = WPT < 4 ? 4 / WPT : 1;   // tokens a workgroup
   __shared__ float part[WPT][KM];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -103,28 +110,30 @@ rows_grad_kernel(moe_host::RowMoveArgs g) {
   for (int j = 0; j < KM; j++) dot[j] = 0.0f;
   const elem* rows = static_cast<const elem*>(g.rows);
   elem* out = static_cast<elem*>(g.out);
-  for (int c = ((wave % WPT) * 64 + lane) * 8; c < g.H; c += WPT * 512) {
-    float x[8], acc[8];
-    R::load8(static_cast<const elem*>(g.tokens) + (size_t)t * g.H + c, x);
+  for (int c = ((wave % WPT) * 64 + lane) * N; c < g.H; c += WPT * 64 * N) {
+    u32x4 raw[KM];
 #pragma unroll
-    for (int i = 0; i < 8; i++) acc[i] = 0.0f;
-    float v[KM][8];
+    for (int j = 0; j < KM; j++)
+      raw[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(rows + (size_t)max(row[j], 0) * g.H + c));
+    float x[N], acc[N];
+    row_load<R>(static_cast<const elem*>(g.tokens) + (size_t)t * g.H + c, x);
 #pragma unroll
-    for (int j = 0; j < KM; j++) {
-      if (row[j] >= 0) R::load8(rows + (size_t)row[j] * g.H + c, v[j]);
-    }
+    for (int i = 0; i < N; i++) acc[i] = 0.0f;
 #pragma unroll
     for (int j = 0; j < KM; j++) {
       if (row[j] < 0) continue;
+      float v[N];
+      R::unpack(raw[j], v);
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
-        dot[j] += v[j][i] * x[i];
-        if constexpr (TO_TOKENS) acc[i] += w[j] * v[j][i];
-        else v[j][i] = w[j] * x[i];
+      for (int i = 0; i < N; i++) {
+        dot[j] += v[i] * x[i];
+        if constexpr (TO_TOKENS) acc[i] += w[j] * v[i];
+        else v[i] = w[j] * x[i];
       }
-      if constexpr (!TO_TOKENS) R::store8(out + (size_t)row[j] * g.H + c, v[j]);
+      if constexpr (!TO_TOKENS)
+        __builtin_nontemporal_store(R::pack(v), reinterpret_cast<u32x4*>(out + (size_t)row[j] * g.H + c));
     }
-    if constexpr (TO_TOKENS) R::store8(out + (size_t)t * g.H + c, acc);
+    if constexpr (TO_TOKENS) row_store<R>(out + (size_t)t * g.H + c, acc);
   }
 #pragma unroll
   for (int j = 0; j < KM; j++)
@@ -232,8 +241,8 @@ static hipError_t with_pairs(int k, F&& f) {
 namespace moe_host {
 
 hipError_t launch_rows_to_experts(const RowMoveArgs& a, int row_type, hipStream_t s) {
-  const dim3 grid(a.T, (a.H / 8 + moe::kMoveThreads - 1) / moe::kMoveThreads);
   return moe::with_row_type(row_type, [&](auto r) {
+    const dim3 grid(a.T, (a.H / decltype(r)::kVec + moe::kMoveThreads - 1) / moe::kMoveThreads);
     return moe::with_pairs(a.k, [&](auto km) {
       hipLaunchKernelGGL((moe::rows_to_experts_kernel<decltype(r), decltype(km)::value>), grid,
                          dim3(moe::kMoveThreads), 0, s, a);
@@ -243,8 +252,8 @@ hipError_t launch_rows_to_experts(const RowMoveArgs& a, int row_type, hipStream_
 }
 
 hipError_t launch_rows_to_tokens(const RowMoveArgs& a, int row_type, hipStream_t s) {
-  const dim3 grid(a.T, (a.H / 8 + moe::kMoveThreads - 1) / moe::kMoveThreads);
   return moe::with_row_type(row_type, [&](auto r) {
+    const dim3 grid(a.T, (a.H / decltype(r)::kVec + moe::kMoveThreads - 1) / moe::kMoveThreads);
     return moe::with_pairs(a.k, [&](auto km) {
       hipLaunchKernelGGL((moe::rows_to_tokens_kernel<decltype(r), decltype(km)::value>), grid,
                          dim3(moe::kMoveThreads), 0, s, a);
@@ -258,7 +267,7 @@ hipError_t launch_rows_grad(const RowMoveArgs& a, bool to_tokens, int row_type, 
     return moe::with_pairs(a.k, [&](auto km) {
       using R = decltype(r);
       constexpr int KM = decltype(km)::value;
-      if (a.H > 512) {   // four waves a token; narrower rows fill a wave at most
+      if (a.H > 64 * R::kVec) {   // four waves a token; narrower rows fill a wave at most
         if (to_tokens)
           hipLaunchKernelGGL((moe::rows_grad_kernel<R, KM, 4, true>), dim3(a.T), dim3(256), 0, s, a);
         else

@@ -182,7 +182,7 @@ def run_layer(lib, T, k, E, H, I, seed, p_drop=0.0, ids=None, x=None, W=None):
 
 
 # E, H, I, k, T, p_drop, tile rows.  Register streaming on 16- and 32-row
-# tiles, strips on 64, 128 and 192; reductions in groups of 4, 2 and 1 units
+# tiles, strips on 64, 96, 128, 160 and 192; reductions in groups of 4, 2 and 1 units
 # and every stage length of the strips (units 4, 6, 2, 5, 3, 1); H not a
 # multiple of 256.
 SHAPES = [
@@ -198,9 +198,12 @@ SHAPES = [
     (8, 768, 512, 2, 130, 0.1, 64),
     (4, 640, 256, 2, 60, 0.0, 64),
     (4, 256, 640, 2, 150, 0.0, 128),
-    (5, 384, 896, 3, 120, 0.2, 128),
+    (5, 384, 896, 3, 120, 0.2, 96),
     (4, 896, 384, 2, 160, 0.0, 128),
     (2, 1536, 768, 2, 90, 0.0, 128),
+    (4, 512, 512, 2, 130, 0.0, 96),
+    (4, 768, 640, 2, 220, 0.1, 160),
+    (3, 1280, 768, 3, 110, 0.0, 160),
     (4, 512, 512, 2, 300, 0.0, 192),
     (3, 768, 640, 2, 310, 0.1, 192),
     (2, 384, 1280, 1, 400, 0.0, 192),
