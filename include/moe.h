@@ -492,8 +492,7 @@ int moe_pack_weights_mxfp4(const uint8_t *codes, const uint8_t *scales, int E, i
  * intermediate makes the values of its block NaN, and with them the outputs
  * that they enter.  H and I must be multiples of 128.
  * moe_route_forward_mxfp4: both in one call, with the same results; at most
- * 64 pairs on the register-streaming plan are routed inside the x
- * quantisation. */
+ * 4096 pairs are routed inside the x quantisation's launch. */
 int moe_build_routing_mxfp4(const int32_t *topk_ids, int T, int k, int E, int H, int I,
                             void *routing, size_t routing_bytes, void *stream);
 int moe_forward_mxfp4(const void *x, const float *topk_w, const void *routing,

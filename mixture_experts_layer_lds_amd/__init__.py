@@ -752,12 +752,12 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _empty(shape, dtype, device, stream):
-    """An output allocated for use on `stream` (None: the current stream)."""
+def _empty(like, shape, dtype, stream):
+    """An output beside `like`, allocated for use on `stream` (None: the current stream)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _row_type(name, t):
@@ -780,9 +780,9 @@ def moe_quantize_mxfp4(x, codes=None, scales=None, stream=None):
             raise ValueError(f"x: expected contiguous rows, got strides {x.stride()}")
         stride = x.stride(0)
     if codes is None:
-        codes = _empty((*x.shape[:-1], cols // 2), torch.uint8, x.device, stream)
+        codes = _empty(x, (*x.shape[:-1], cols // 2), torch.uint8, stream)
     if scales is None:
-        scales = _empty((*x.shape[:-1], cols // 32), torch.uint8, x.device, stream)
+        scales = _empty(x, (*x.shape[:-1], cols // 32), torch.uint8, stream)
     _is("codes", codes, torch.uint8, (*x.shape[:-1], cols // 2))
     _is("scales", scales, torch.uint8, (*x.shape[:-1], cols // 32))
     dev = _check_device(x, codes, scales)
@@ -798,7 +798,7 @@ def moe_dequantize_mxfp4(codes, scales, dtype=torch.bfloat16, out=None, stream=N
         raise ValueError(f"codes: expected rows of a multiple of 16 bytes, got {tuple(codes.shape)}")
     lead, cols = codes.shape[:-1], 2 * codes.shape[-1]
     if out is None:
-        out = _empty((*lead, cols), dtype, codes.device, stream)
+        out = _empty(codes, (*lead, cols), dtype, stream)
     kind = _row_type("out", out)
     _is("codes", codes, torch.uint8, (*lead, cols // 2))
     _is("scales", scales, torch.uint8, (*lead, cols // 32))
@@ -818,7 +818,7 @@ def moe_pack_weights_mxfp4(codes, scales, out=None, stream=None):
     _check_tensor("codes", codes, torch.uint8, (E, rows, cols // 2))
     _check_tensor("scales", scales, torch.uint8, (E, rows, cols // 32))
     if out is None:
-        out = _empty((E, rows, cols // 2 + cols // 32), torch.uint8, codes.device, stream)
+        out = _empty(codes, (E, rows, cols // 2 + cols // 32), torch.uint8, stream)
     _check_tensor("out", out, torch.uint8, (E, rows, cols // 2 + cols // 32))
     _check_device(codes, scales, out)
     desc = PackedWeightsDesc()
@@ -879,7 +879,7 @@ def _move(name, fn, src, src_name, sorted_src, routing, k, E, topk_w, out, out_n
     T, H = _rows(src_name, src, k, sorted_src)
     shape = (T, H) if sorted_src else (T * k, H)
     if out is None:
-        out = _empty(shape, src.dtype, src.device, stream)
+        out = _empty(src, shape, src.dtype, stream)
     _is(src_name, src, src.dtype, src.shape)
     _is(out_name, out, src.dtype, shape)
     if topk_w is not None:
@@ -912,9 +912,9 @@ def _move_grad(name, fn, grad, grad_name, sorted_grad, other, other_name, routin
     T, H = _rows(grad_name, grad, k, sorted_grad)
     shape = (T, H) if sorted_grad else (T * k, H)
     if out is None:
-        out = _empty(shape, grad.dtype, grad.device, stream)
+        out = _empty(grad, shape, grad.dtype, stream)
     if other is not None and dw is None:
-        dw = _empty((T, k), torch.float32, grad.device, stream)
+        dw = _empty(grad, (T, k), torch.float32, stream)
     _is(grad_name, grad, grad.dtype, grad.shape)
     _is(out_name, out, grad.dtype, shape)
     if topk_w is not None:
@@ -951,7 +951,7 @@ def moe_router_topk_grad(logits, topk_ids, topk_w, dtopk_w, renormalize=True, n_
     T, E = logits.shape
     ncol = topk_ids.shape[1]
     if dlogits is None:
-        dlogits = _empty((T, E), torch.float32, logits.device, stream)
+        dlogits = _empty(logits, (T, E), torch.float32, stream)
     _is("logits", logits, torch.float32, (T, E))
     _is("topk_ids", topk_ids, torch.int32, (T, ncol))
     _is("topk_w", topk_w, torch.float32, (T, ncol))

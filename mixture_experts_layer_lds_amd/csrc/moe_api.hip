@@ -207,18 +207,34 @@ int pick_mx4_waves(int groups, long items) {
   return best;
 }
 
-// MXFP4: register streaming on 16- or 32-row tiles up to 16 mean rows per
-// expert, strips above, tiles of about twice the mean rows (as the one-byte
-// dtypes) so that the usual spread of a routing still fits one tile.
+// MXFP4: register streaming on 16-row tiles up to 8 mean rows per expert and
+// strips above 16, of tiles a quarter or more above the mean, so that the usual
+// spread of a routing still fits one tile (rows past a tile's last are not
+// multiplied).  Between, strips where both products have three items a CU or
+// more, streaming on 32-row tiles below, whose split reductions spread better.
+// Graph replay, us, streaming against strips: DeepSeek-V3-shaped T = 512 1023 /
+// 989, Qwen3-30B-A3B-shaped T = 256 73 / 60 (768 and 1024 items);
+// Mixtral-8x7B-shaped T = 64 140 / 148 (896 and 128), Qwen2-57B-shaped slice
+// T = 100 68 / 78 (320 and 896).
 void plan_mx4(int T, int k, int E, int H, int I, Plan* p) {
   const long P = (long)T * k, active = std::min(P, (long)E);
   const long avg = active > 0 ? (P + active - 1) / active : 1;
-  p->tiling = avg <= 16 ? kStreaming : kStrips;
-  p->mb = avg <= 8 ? 1 : (avg <= 16 ? 2 : (avg <= 40 ? 4 : (avg <= 72 ? 6 : (avg <= 96 ? 8 : (avg <= 128 ? 10 : 12)))));
+  const long strips = (H + kStripCols - 1) / kStripCols;   // of the down product; the gate-up has I / 128
+  const bool wide = active * std::min((long)I / 128, strips) >= 3 * kPlanCUs;
+  p->tiling = avg <= 8 || (avg <= 16 && !wide) ? kStreaming : kStrips;
+  p->mb = p->tiling == kStreaming ? (avg <= 8 ? 1 : 2)
+                                  : (avg <= 40 ? 4 : (avg <= 72 ? 6 : (avg <= 96 ? 8 : (avg <= 128 ? 10 : 12))));
   p->block_m = 16 * p->mb;
   p->max_tasks = (int)(P / p->block_m + active);
-  if (p->tiling == kStrips) return;
   auto tasks = [&](long experts) { return std::max((P + p->block_m - 1) / p->block_m, experts); };
+  if (p->tiling == kStrips) {
+    // K slices of the down reduction while its items leave CUs without one
+    // (Mixtral-8x7B-shaped T = 80, 128 items: 161 -> 149 us, T = 200 174 -> 159)
+    const long items = tasks(std::min(active, expected_active(T, k, E))) * strips;
+    const int nk = moe_host::mx4_strip_stages(p->mb, I);
+    while (items * p->split2 * 5 < kPlanCUs * 4 && nk % (2 * p->split2) == 0 && p->split2 < 8) p->split2 *= 2;
+    return;
+  }
   p->sw1 = pick_mx4_waves(H / 128 / moe::mx4_group(H), tasks(active) * (I / 32));
   p->sw2 = pick_mx4_waves(I / 128 / moe::mx4_group(I), tasks(std::min(active, expected_active(T, k, E))) * (H / 64));
   p->dr_waves = T == 1 ? 8 : 0;
@@ -569,9 +585,11 @@ void workspace_layout(int dtype, int T, int k, int H, int I, const Plan& p,
     W->x_scale = take((size_t)T * H / 32);
     W->x_scale_rows = W->g = W->h_scale = kNone;
     W->h = take((size_t)p.max_tasks * p.mb * (I / 128) * moe::kMx4Unit);
-    W->y = p.dr_waves ? kNone : take(2 * P * H);   // one token: the down launch adds the top-k rows itself
+    // one token: the down launch adds the top-k rows itself
+    W->y = p.dr_waves ? kNone : (p.split2 == 1 ? take(2 * P * H) : take(4 * (size_t)p.split2 * P * H));
     W->total_bytes = off;
-    W->split_k1 = W->split_k2 = 1;
+    W->split_k1 = 1;
+    W->split_k2 = p.split2;
     W->tiling = p.tiling;
     return;
   }
@@ -943,6 +961,8 @@ int forward_mx4(const void* x, const float* topk_w, const void* routing, const v
   a.topk = k;
   a.max_tasks = p.max_tasks;
   a.topk_w = topk_w;
+  a.P = P;
+  a.split = 1;
   {
     StageScope st(s, 1);
     a.a = xq;
@@ -966,6 +986,7 @@ int forward_mx4(const void* x, const float* topk_w, const void* routing, const v
     a.K = I;
     a.N_out = H;
     a.w_rows = H;
+    a.split = p.split2;
     if (p.tiling == kStrips) e = moe_host::launch_mx4_strip(a, false, p.mb, cus, s);
     else if (p.dr_waves) e = moe_host::launch_mx4_down_reduce(a, s);
     else e = moe_host::launch_mx4_stream(a, false, p.mb, p.sw2,
@@ -974,8 +995,8 @@ int forward_mx4(const void* x, const float* topk_w, const void* routing, const v
   }
   if (!p.dr_waves) {
     StageScope st(s, 4);
-    e = moe_host::launch_reduce(ws + W.y, true, 1, P, topk_w, R.pair_pos, R.expert_offsets, nullptr, E, T, k, H,
-                                static_cast<uint16_t*>(out), s);
+    e = moe_host::launch_reduce(ws + W.y, p.split2 == 1, p.split2, P, topk_w, R.pair_pos, R.expert_offsets, nullptr, E,
+                                T, k, H, static_cast<uint16_t*>(out), s);
     if (e != hipSuccess) return MOE_ERR_HIP;
   }
   return MOE_OK;
@@ -1703,7 +1724,10 @@ int route_forward(int dtype, const int32_t* ids, const void* x, const float* top
   // two weight blocks per item (bf16 also the half-width items)
   const bool bf16_act = dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_INT4_W4A16 || dtype == MOE_DTYPE_INT8_W8A16;
   const bool first_takes_it = !bf16_act || (p.mb == 1 && (p.nb == 2 || (dtype == MOE_DTYPE_BF16 && p.half1)));
-  if ((long)T * k <= moe::kDecodeRoutePairs && p.tiling == kStreaming && first_takes_it) {
+  const bool folded = dtype == MOE_DTYPE_MXFP4   // its x quantisation takes larger batches and any plan too
+                          ? (long)T * k <= moe_host::mx4_route_pairs()
+                          : (long)T * k <= moe::kDecodeRoutePairs && p.tiling == kStreaming && first_takes_it;
+  if (folded) {
     char* b = static_cast<char*>(routing);
     moe_host::DecodeRouteOut f;
     f.ids = ids;

@@ -416,8 +416,9 @@ hipError_t launch_tile_copy(int pattern, const void* buf, int row_bytes, int rep
 
 // MXFP4 (mx4.hip; the format and the packed layout are in mx4.h): rows of
 // moe_row_type_t to codes and scale codes and back; bf16 token rows as the
-// layer reads them (with route, at most 64 pairs, the launch also does the
-// routing build); row-major weights to packed blocks.
+// layer reads them (with route, at most mx4_route_pairs() pairs, the launch
+// also does the routing build); row-major weights to packed blocks.
+int mx4_route_pairs();
 hipError_t launch_mx4_quantize(const void* x, int row_type, size_t rows, int cols, size_t row_stride, uint8_t* codes,
                                uint8_t* scales, hipStream_t s);
 hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, size_t rows, int cols, int row_type,
@@ -445,12 +446,15 @@ struct Mx4Args {
   int topk;
   int max_tasks;
   const float* topk_w;          // one token, down: the routing weights
+  int split;                    // strips, down: K slices; with more than one, c is fp32 [split][P][N_out]
+  int P;                        // sorted rows
 };
 // (mb, waves) = 16-row blocks per tile (1 or 2), waves per workgroup (1, 2, 4, 8)
 hipError_t launch_mx4_stream(const Mx4Args& a, bool gateup, int mb, int waves, int grid, hipStream_t s);
 // One token: down GEMM and top-k weighted sum, out (bf16 [H]) in a.c.
 hipError_t launch_mx4_down_reduce(const Mx4Args& a, hipStream_t s);
-// mb in {4, 6, 8, 10, 12}
+// mb in {4, 6, 8, 10, 12}; a.split divides mx4_strip_stages
+int mx4_strip_stages(int mb, int K);   // stages of a strip's reduction over K
 hipError_t launch_mx4_strip(const Mx4Args& a, bool gateup, int mb, int grid, hipStream_t s);
 
 // Rows between token and expert order (rows.hip).

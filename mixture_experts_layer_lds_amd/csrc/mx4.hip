@@ -9,6 +9,7 @@
 // read once and nothing is kept: the passes are bound by their bytes.  Large
 // ones take four runs a wave, all loads ahead of the first use.
 #include "decode_route.h"
+#include "route_group.h"
 #include "mx4.h"
 #include "rows.h"
 
@@ -105,7 +106,21 @@ mx4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restri
 
 // x [T][H] bf16 -> codes [T][H/2] row-major, scale codes [T][H/128/G][4][G]
 // (a lane of the product takes the G codes of its 32-value column in one
-// load).  ROUTE (at most 64 pairs): workgroup 0 also does the routing build.
+// load); vector i, eight values.
+__device__ __forceinline__ void mx4_quant_x(const uint16_t* __restrict__ x, uint32_t i, uint32_t vec_per_row, int G,
+                                            uint32_t* __restrict__ xq, uint8_t* __restrict__ sx) {
+  float v[8];
+  row_load<RowBf16>(x + (size_t)i * 8, v);
+  uint32_t code;
+  xq[i] = mx4_quant8(v, code);
+  if ((threadIdx.x & 3) == 0) {
+    const uint32_t row = i / vec_per_row, b = (i - row * vec_per_row) / 4;   // block of the row
+    const uint32_t unit = b / 4, kb = b % 4, grp = unit / G, u = unit % G;
+    sx[(size_t)row * (vec_per_row / 4) + grp * 4 * G + kb * G + u] = (uint8_t)code;
+  }
+}
+
+// ROUTE (at most 64 pairs): workgroup 0 also does the routing build.
 template <bool ROUTE>
 __global__ void __launch_bounds__(kMx4Threads)
 mx4_quant_x_kernel(const uint16_t* __restrict__ x, uint32_t nvec, uint32_t vec_per_row, int G,
@@ -118,16 +133,23 @@ mx4_quant_x_kernel(const uint16_t* __restrict__ x, uint32_t nvec, uint32_t vec_p
     }
   }
   const uint32_t i = blockIdx.x * kMx4Threads + threadIdx.x;
-  if (i >= nvec) return;   // whole waves of four-lane blocks: nvec % 16 == 0
-  float v[8];
-  row_load<RowBf16>(x + (size_t)i * 8, v);
-  uint32_t code;
-  xq[i] = mx4_quant8(v, code);
-  if ((threadIdx.x & 3) == 0) {
-    const uint32_t row = i / vec_per_row, b = (i - row * vec_per_row) / 4;   // block of the row
-    const uint32_t unit = b / 4, kb = b % 4, grp = unit / G, u = unit % G;
-    sx[(size_t)row * (vec_per_row / 4) + grp * 4 * G + kb * G + u] = (uint8_t)code;
+  if (i < nvec) mx4_quant_x(x, i, vec_per_row, G, xq, sx);   // whole blocks: nvec % 16 == 0
+}
+
+// Up to kOneGroupPairs pairs: workgroup 0 does the routing build, the others
+// the codes, which do not depend on it.  One launch instead of two: the build
+// takes about 5 us whatever the batch, the codes 4 (Qwen3-30B-A3B-shaped layer,
+// T = 64: 46.0 -> 44.4 us, DeepSeek-V3-shaped 816 -> 814).
+__global__ void __launch_bounds__(kRouteThreads)
+mx4_route_quant_kernel(const uint16_t* __restrict__ x, uint32_t nvec, uint32_t vec_per_row, int G,
+                       uint32_t* __restrict__ xq, uint8_t* __restrict__ sx, moe_host::DecodeRouteOut o, int P) {
+  if (blockIdx.x == 0) {
+    route_one_group(o.ids, P, o.E, o.block_m, o.max_tasks, o.header, o.expert_offsets, o.sorted_pairs, o.pair_pos,
+                    o.tasks);
+    return;
   }
+  const uint32_t i = (blockIdx.x - 1) * kRouteThreads + threadIdx.x;
+  if (i < nvec) mx4_quant_x(x, i, vec_per_row, G, xq, sx);
 }
 
 // Row-major codes and scale codes -> blocks of 16 rows x G units (mx4.h).
@@ -205,14 +227,19 @@ hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, si
   });
 }
 
+int mx4_route_pairs() { return moe::kOneGroupPairs; }
+
 hipError_t launch_mx4_quant_x(const uint16_t* x, int T, int H, uint8_t* xq, uint8_t* sx, hipStream_t s,
                               const DecodeRouteOut* route, int P) {
-  if (route && (P > moe::kDecodeRoutePairs || !route->ids)) return hipErrorInvalidValue;
+  if (route && (P > moe::kOneGroupPairs || !route->ids)) return hipErrorInvalidValue;
   const uint32_t nvec = (uint32_t)T * (uint32_t)(H / 8);   // T * H <= 2^32
   const dim3 grid((nvec + moe::kMx4Threads - 1) / moe::kMx4Threads);
   const DecodeRouteOut ro = route ? *route : DecodeRouteOut{};
   uint32_t* q = reinterpret_cast<uint32_t*>(xq);
-  if (route)
+  if (route && P > moe::kDecodeRoutePairs)
+    hipLaunchKernelGGL(moe::mx4_route_quant_kernel, dim3(1 + (nvec + moe::kRouteThreads - 1) / moe::kRouteThreads),
+                       dim3(moe::kRouteThreads), 0, s, x, nvec, (uint32_t)(H / 8), moe::mx4_group(H), q, sx, ro, P);
+  else if (route)
     hipLaunchKernelGGL(moe::mx4_quant_x_kernel<true>, grid, dim3(moe::kMx4Threads), 0, s, x, nvec, (uint32_t)(H / 8),
                        moe::mx4_group(H), q, sx, ro, P);
   else

@@ -77,6 +77,26 @@ mx4_stream_kernel(moe_host::Mx4Args g) {
       const int blk = GATEUP ? (q & 1) + 2 * cg + (q >> 1) * (g.N_out / 16) : 4 * cg + q;
       bp[q] = B + (size_t)task.expert * expert_bytes + (size_t)blk * block_bytes;
     }
+    struct Stage {
+      u32x4 w[G][kMx4NB], t[G][MB];
+      uint32_t sw[kMx4NB], st[MB];
+    };
+    auto load_weights = [&](Stage& f, int grp) __attribute__((always_inline)) {
+      const size_t at = (size_t)grp * (G * kMx4Unit);
+#pragma unroll
+      for (int q = 0; q < kMx4NB; q++)
+        f.sw[q] = __builtin_nontemporal_load(
+            reinterpret_cast<const uint32_t*>(mx4_piece<G>(bp[q] + at + G * 1024, lane)));
+#pragma unroll
+      for (int u = 0; u < G; u++)
+#pragma unroll
+        for (int q = 0; q < kMx4NB; q++)
+          f.w[u][q] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(bp[q] + at + u * 1024 + 16 * lane));
+    };
+    // the first group's weights before the (dependent) look-up of the token rows
+    const int n = ngrp > wave ? (ngrp - wave + W - 1) / W : 0;
+    Stage s0, s1;
+    if (n > 0) load_weights(s0, wave);
     // token rows: rows past the tile re-read its first row (a valid address
     // whose products land only in columns that are never stored)
     const char *ap[MB], *asp[MB];
@@ -97,36 +117,28 @@ mx4_stream_kernel(moe_host::Mx4Args g) {
     const int ash = GATEUP ? 8 * ((lgrp * G) & 3) : mx4_piece_shift<G>(lane);
     const int bsh = mx4_piece_shift<G>(lane);
 
+    auto load_tokens = [&](Stage& f, int grp) __attribute__((always_inline)) {
+      const size_t at = (size_t)grp * (G * kMx4Unit);
+#pragma unroll
+      for (int b = 0; b < MB; b++)
+        f.st[b] = *reinterpret_cast<const uint32_t*>(asp[b] + (GATEUP ? (size_t)grp * (4 * G) : at));
+#pragma unroll
+      for (int u = 0; u < G; u++)
+#pragma unroll
+        for (int b = 0; b < MB; b++)
+          f.t[u][b] = *reinterpret_cast<const u32x4*>(
+              ap[b] + (GATEUP ? (size_t)(grp * G + u) * 64 : at + u * 1024));
+    };
+    auto load = [&](Stage& f, int grp) __attribute__((always_inline)) {
+      load_tokens(f, grp);
+      load_weights(f, grp);
+    };
     f32x4 acc[MB][kMx4NB];
 #pragma unroll
     for (int m = 0; m < MB; m++)
 #pragma unroll
       for (int q = 0; q < kMx4NB; q++) acc[m][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    struct Stage {
-      u32x4 w[G][kMx4NB], t[G][MB];
-      uint32_t sw[kMx4NB], st[MB];
-    };
-    auto load = [&](Stage& f, int grp) __attribute__((always_inline)) {
-      const size_t at = (size_t)grp * (G * kMx4Unit);
-#pragma unroll
-      for (int q = 0; q < kMx4NB; q++)
-        f.sw[q] = __builtin_nontemporal_load(
-            reinterpret_cast<const uint32_t*>(mx4_piece<G>(bp[q] + at + G * 1024, lane)));
-#pragma unroll
-      for (int b = 0; b < MB; b++)
-        f.st[b] = *reinterpret_cast<const uint32_t*>(asp[b] + (GATEUP ? (size_t)grp * (4 * G) : at));
-#pragma unroll
-      for (int u = 0; u < G; u++) {
-#pragma unroll
-        for (int b = 0; b < MB; b++)
-          f.t[u][b] = *reinterpret_cast<const u32x4*>(
-              ap[b] + (GATEUP ? (size_t)(grp * G + u) * 64 : at + u * 1024));
-#pragma unroll
-        for (int q = 0; q < kMx4NB; q++)
-          f.w[u][q] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(bp[q] + at + u * 1024 + 16 * lane));
-      }
-    };
     auto compute = [&](const Stage& f) __attribute__((always_inline)) {
       mx4_units<G>([&](auto u) {
         constexpr int U = decltype(u)::value;
@@ -140,10 +152,8 @@ mx4_stream_kernel(moe_host::Mx4Args g) {
     // Groups wave, wave + W, ...: no load sits under a condition inside the
     // loop, so each multiply waits for exactly its own group while the next
     // one is in flight.
-    const int n = ngrp > wave ? (ngrp - wave + W - 1) / W : 0;
     if (n > 0) {
-      Stage s0, s1;
-      load(s0, wave);
+      load_tokens(s0, wave);
       int i = 0;
       for (; i + 2 < n; i += 2) {
         load(s1, wave + (i + 1) * W);

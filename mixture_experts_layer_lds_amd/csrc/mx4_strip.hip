@@ -41,9 +41,9 @@
 namespace moe {
 
 constexpr int kMx4Waves = 8;
-// Row blocks x units of a stage up to which the registers hold two stages of
-// weights (above, the accumulators leave room for one).
-constexpr int kMx4TwoAhead = 40;
+// Whether the registers hold two stages of weights beside the accumulators of
+// MB row blocks (a stage of one group of four units takes the fewest others).
+constexpr int mx4_stages_ahead(int MB, int G, int GS) { return MB * G * GS <= (G == 4 ? 40 : 32) ? 2 : 1; }
 
 // Direct buffer->LDS copies (a lane's N bytes at base + off + soff, to its
 // place after dst).
@@ -74,13 +74,19 @@ struct Mx4Stage {
 // tiles take a strip one after another, so that its weights, once in L2,
 // serve them all; the strips of one tile stand side by side where an expert
 // has one tile, and meet its token rows in L2.
+// With `split` K slices an item is one slice of them, stages k0 on, the
+// slices of a strip side by side.
 struct Mx4Place {
   int ti, nt, expert, row_begin, rows;
+  int slice, k0;
 };
 
 template <int MB>
-__device__ __forceinline__ Mx4Place mx4_place(const moe_host::Mx4Args& g, int item, int n_strips) {
+__device__ __forceinline__ Mx4Place mx4_place(const moe_host::Mx4Args& g, int item, int n_strips, int nk) {
   Mx4Place p;
+  p.slice = item % g.split;
+  p.k0 = p.slice * nk;
+  item /= g.split;
   p.ti = item / n_strips;
   p.nt = item - p.ti * n_strips;
   const moe_task_t t = load_task_scalar(g.tasks + p.ti);
@@ -151,6 +157,7 @@ __device__ __forceinline__ Mx4Item<MB, G, GS> mx4_item(const moe_host::Mx4Args& 
 // The wave's two 16-row weight blocks in strip nt.
 struct Mx4Blocks {
   int out;      // gate-up: first block of the 32 columns of h that a pair of waves forms; down: the first block
+  int k0;       // the item's first stage
   bool store;   // they exist (down: H may end inside a strip; else block 0 is read and nothing stored)
   const char *b0, *b1;
 };
@@ -158,6 +165,7 @@ struct Mx4Blocks {
 template <bool GATEUP>
 __device__ __forceinline__ Mx4Blocks mx4_blocks(const moe_host::Mx4Args& g, const Mx4Place& at, int wave) {
   Mx4Blocks r;
+  r.k0 = at.k0;
   const size_t block_bytes = (size_t)(g.K / 128) * kMx4Unit;
   int b0, b1;
   if constexpr (GATEUP) {
@@ -201,8 +209,8 @@ mx4_strip_kernel(moe_host::Mx4Args g) {
 
   const int num_tasks = min(g.header[kHdrNumTasks], g.max_tasks);
   const int n_strips = GATEUP ? g.N_out / 128 : (g.N_out + 255) / 256;
-  const int total = num_tasks * n_strips;
-  const int nk = g.K / 128 / U;   // stages per item
+  const int total = num_tasks * n_strips * g.split;   // < 2^31: see the launch
+  const int nk = g.K / 128 / U / g.split;             // stages per item
   const int units2 = g.N_out / 128, G2 = units2 % 4 == 0 ? 4 : (units2 % 2 == 0 ? 2 : 1);
 
   // XCD-aware numbering: each XCD takes a contiguous run of items, so the
@@ -228,7 +236,7 @@ mx4_strip_kernel(moe_host::Mx4Args g) {
     // places, so that no wave overwrites what another still reads).  Past the
     // last item: the last one again, its first stage loaded and never used.
     const uint32_t inv_topk = ((1u << 20) + g.topk - 1) / g.topk;
-    auto place = [&](int i) __attribute__((always_inline)) { return mx4_place<MB>(g, vid + min(i, n_items - 1) * gs, n_strips); };
+    auto place = [&](int i) __attribute__((always_inline)) { return mx4_place<MB>(g, vid + min(i, n_items - 1) * gs, n_strips, nk); };
     auto copy_pairs = [&](const Mx4Place& p, int i) __attribute__((always_inline)) {
       if constexpr (GATEUP) {
         const auto r = rows_rsrc(reinterpret_cast<const char*>(g.sorted_pairs + p.row_begin));
@@ -250,6 +258,7 @@ mx4_strip_kernel(moe_host::Mx4Args g) {
     It cur = sources(place0, 0), nxt = sources(place1, 1);
 
     auto issue_tokens = [&](bool in_cur, int kt, char* slot) __attribute__((always_inline)) {
+      kt += in_cur ? cur.at.k0 : nxt.at.k0;
       const int at = kt * (GATEUP ? U * 64 : U * kMx4Unit);
       const auto ra = rows_rsrc(in_cur ? cur.abase : nxt.abase);
       const auto rs = GATEUP ? rows_rsrc(reinterpret_cast<const char*>(g.a_sc)) : ra;
@@ -296,7 +305,7 @@ mx4_strip_kernel(moe_host::Mx4Args g) {
     __asm__ volatile("" ::: "memory");
 #pragma unroll
     for (int d = 0; d < D; d++) {
-      const size_t at = (size_t)wk * (U * kMx4Unit);
+      const size_t at = (size_t)(wb.k0 + wk) * (U * kMx4Unit);
       load_scales(swn[d], wb.b0 + at, wb.b1 + at);
 #pragma unroll
       for (int u = 0; u < U; u++) load_unit(w[d][u], wb.b0 + at, wb.b1 + at, u);
@@ -325,8 +334,8 @@ mx4_strip_kernel(moe_host::Mx4Args g) {
         issue_tokens(in_cur, in_cur ? kt + 1 : 0, next);
         __asm__ volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
-        const char* b0 = wb.b0 + (size_t)wk * (U * kMx4Unit);
-        const char* b1 = wb.b1 + (size_t)wk * (U * kMx4Unit);
+        const char* b0 = wb.b0 + (size_t)(wb.k0 + wk) * (U * kMx4Unit);
+        const char* b1 = wb.b1 + (size_t)(wb.k0 + wk) * (U * kMx4Unit);
 #pragma unroll
         for (int j = 0; j < GS; j++)
 #pragma unroll
@@ -416,15 +425,23 @@ mx4_strip_kernel(moe_host::Mx4Args g) {
         }
       } else {
         // rows past the tile are out of the buffer's bounds and dropped
-        const auto y = __builtin_amdgcn_make_buffer_rsrc(static_cast<uint16_t*>(g.c) + (size_t)cur.at.row_begin * g.N_out, 0,
-                                                         blk.store ? cur.at.rows * g.N_out * 2 : 0, 0x00027000);
+        const int esz = g.split > 1 ? 4 : 2;
+        const auto y = __builtin_amdgcn_make_buffer_rsrc(
+            static_cast<char*>(g.c) + ((size_t)cur.at.slice * g.P + cur.at.row_begin) * g.N_out * esz, 0,
+            blk.store ? cur.at.rows * g.N_out * esz : 0, 0x00027000);
 #pragma unroll
         for (int m = 0; m < MB; m++) {
           if (16 * m >= cur.at.rows) break;
-          u32x4 v;
+          const int at = ((16 * m + lrow) * g.N_out + 16 * blk.out + 8 * lgrp) * esz;
+          if (g.split > 1) {   // fp32 sums of this slice
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[m][0]), y, at, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[m][1]), y, at + 16, 0, 0);
+          } else {
+            u32x4 v;
 #pragma unroll
-          for (int i = 0; i < 4; i++) v[i] = bf16_pair(acc[m][i >> 1][2 * (i & 1)], acc[m][i >> 1][2 * (i & 1) + 1]);
-          __builtin_amdgcn_raw_buffer_store_b128(v, y, ((16 * m + lrow) * g.N_out + 16 * blk.out + 8 * lgrp) * 2, 0, 0);
+            for (int i = 0; i < 4; i++) v[i] = bf16_pair(acc[m][i >> 1][2 * (i & 1)], acc[m][i >> 1][2 * (i & 1) + 1]);
+            __builtin_amdgcn_raw_buffer_store_b128(v, y, at, 0, 0);
+          }
         }
       }
       clear();
@@ -461,23 +478,34 @@ mx4_strip_kernel(moe_host::Mx4Args g) {
 
 template <int MB, int G, int GS, bool GATEUP>
 static hipError_t launch_mx4_strip_t(const moe_host::Mx4Args& a, int grid, hipStream_t s) {
-  hipLaunchKernelGGL((mx4_strip_kernel<MB, G, GS, MB * G * GS <= kMx4TwoAhead ? 2 : 1, GATEUP>), dim3(grid),
+  hipLaunchKernelGGL((mx4_strip_kernel<MB, G, GS, mx4_stages_ahead(MB, G, GS), GATEUP>), dim3(grid),
                      dim3(kMx4Waves * 64), 0, s, a);
   return hipGetLastError();
 }
 
-// Stages of four to six units where the reduction divides into them: shorter
-// ones leave too little in flight.
+// Groups a stage: four to six units where the reduction divides into them
+// (shorter stages leave too little in flight).  160- and 192-row tiles: two slots
+// of six units do not fit the LDS or five spill registers.
+static int mx4_stage_groups(int mb, int K) {
+  const int units = K / 128;
+  if (units % 4 == 0) return 1;
+  if (units % 2 == 0) return mb <= 8 && units % 6 == 0 ? 3 : 1;
+  if (mb <= 8 && units % 5 == 0) return 5;
+  return units % 3 == 0 ? 3 : 1;
+}
+
+static int mx4_strip_stages(int mb, int K) { return K / 128 / mx4_group(K) / mx4_stage_groups(mb, K); }
+
 template <int MB, bool GATEUP>
 static hipError_t launch_mx4_strip_g(const moe_host::Mx4Args& a, int grid, hipStream_t s) {
-  const int units = a.K / 128;
-  if (units % 4 == 0) return launch_mx4_strip_t<MB, 4, 1, GATEUP>(a, grid, s);
-  if constexpr (MB <= 8) {   // 192 rows: two slots of six units do not fit, five spill registers
-    if (units % 6 == 0) return launch_mx4_strip_t<MB, 2, 3, GATEUP>(a, grid, s);
-    if (units % 10 == 5) return launch_mx4_strip_t<MB, 1, 5, GATEUP>(a, grid, s);
+  const int G = mx4_group(a.K), GS = mx4_stage_groups(MB, a.K);
+  if (G == 4) return launch_mx4_strip_t<MB, 4, 1, GATEUP>(a, grid, s);
+  if constexpr (MB <= 8) {
+    if (G == 2 && GS == 3) return launch_mx4_strip_t<MB, 2, 3, GATEUP>(a, grid, s);
+    if (GS == 5) return launch_mx4_strip_t<MB, 1, 5, GATEUP>(a, grid, s);
   }
-  if (units % 2 == 0) return launch_mx4_strip_t<MB, 2, 1, GATEUP>(a, grid, s);
-  if (units % 3 == 0) return launch_mx4_strip_t<MB, 1, 3, GATEUP>(a, grid, s);
+  if (G == 2) return launch_mx4_strip_t<MB, 2, 1, GATEUP>(a, grid, s);
+  if (GS == 3) return launch_mx4_strip_t<MB, 1, 3, GATEUP>(a, grid, s);
   return launch_mx4_strip_t<MB, 1, 1, GATEUP>(a, grid, s);
 }
 
@@ -485,8 +513,11 @@ static hipError_t launch_mx4_strip_g(const moe_host::Mx4Args& a, int grid, hipSt
 
 namespace moe_host {
 
+int mx4_strip_stages(int mb, int K) { return moe::mx4_strip_stages(mb, K); }
+
 hipError_t launch_mx4_strip(const Mx4Args& a, bool gateup, int mb, int grid, hipStream_t s) {
   if (a.K % 128 || a.N_out % 128 || a.w_rows != (gateup ? 2 : 1) * a.N_out) return hipErrorInvalidValue;
+  if (a.split < 1 || (gateup && a.split > 1) || moe::mx4_strip_stages(mb, a.K) % a.split) return hipErrorInvalidValue;
 #define MOE_MX4_CASE(M) \
   if (mb == M) return gateup ? moe::launch_mx4_strip_g<M, true>(a, grid, s) : moe::launch_mx4_strip_g<M, false>(a, grid, s);
   MOE_MX4_CASE(4) MOE_MX4_CASE(6) MOE_MX4_CASE(8) MOE_MX4_CASE(10) MOE_MX4_CASE(12)

@@ -99,18 +99,18 @@ rows_grad_kernel(moe_host::RowMoveArgs g) {
   typedef typename R::elem elem;
   constexpr int N = R::kVec;
   constexpr int TPB = WPT < 4 ? 4 / WPT : 1;   // tokens a workgroup
-  __shared__ float part[WPT][KM];
+  __shared__ float part[WPT * TPB][KM];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int t = blockIdx.x * TPB + wave / WPT;
-  if (t >= g.T) return;   // whole waves; with WPT > 1 whole workgroups
+  const int t = blockIdx.x * TPB + wave / WPT;   // waves past the last token have no columns
+  const int H = t < g.T ? g.H : 0;
   int row[KM];
   float w[KM], dot[KM];
-  pair_rows<KM>(g, t, row, w);
+  pair_rows<KM>(g, min(t, g.T - 1), row, w);
 #pragma unroll
   for (int j = 0; j < KM; j++) dot[j] = 0.0f;
   const elem* rows = static_cast<const elem*>(g.rows);
   elem* out = static_cast<elem*>(g.out);
-  for (int c = ((wave % WPT) * 64 + lane) * N; c < g.H; c += WPT * 64 * N) {
+  for (int c = ((wave % WPT) * 64 + lane) * N; c < H; c += WPT * 64 * N) {
     u32x4 raw[KM];
 #pragma unroll
     for (int j = 0; j < KM; j++)
@@ -145,16 +145,17 @@ rows_grad_kernel(moe_host::RowMoveArgs g) {
       for (int j = 0; j < KM; j++) part[wave][j] = dot[j];
     }
     __syncthreads();
-    if (threadIdx.x < g.k) {
+    const int j = (wave % WPT) * 64 + lane;   // of the token's threads
+    if (t < g.T && j < g.k) {
       float s = 0.0f;
 #pragma unroll
-      for (int q = 0; q < WPT; q++) s += part[q][threadIdx.x];
-      g.dw[(size_t)t * g.k + threadIdx.x] = s;
+      for (int q = 0; q < WPT; q++) s += part[wave / WPT * WPT + q][j];
+      g.dw[(size_t)t * g.k + j] = s;
     }
   } else {
 #pragma unroll
     for (int j = 0; j < KM; j++)
-      if (lane == 0 && j < g.k) g.dw[(size_t)t * g.k + j] = dot[j];
+      if (lane == 0 && t < g.T && j < g.k) g.dw[(size_t)t * g.k + j] = dot[j];
   }
 }
 
@@ -267,18 +268,19 @@ hipError_t launch_rows_grad(const RowMoveArgs& a, bool to_tokens, int row_type, 
     return moe::with_pairs(a.k, [&](auto km) {
       using R = decltype(r);
       constexpr int KM = decltype(km)::value;
-      if (a.H > 64 * R::kVec) {   // four waves a token; narrower rows fill a wave at most
-        if (to_tokens)
-          hipLaunchKernelGGL((moe::rows_grad_kernel<R, KM, 4, true>), dim3(a.T), dim3(256), 0, s, a);
-        else
-          hipLaunchKernelGGL((moe::rows_grad_kernel<R, KM, 4, false>), dim3(a.T), dim3(256), 0, s, a);
-      } else {
-        const dim3 grid((a.T + 3) / 4);
-        if (to_tokens)
-          hipLaunchKernelGGL((moe::rows_grad_kernel<R, KM, 1, true>), grid, dim3(256), 0, s, a);
-        else
-          hipLaunchKernelGGL((moe::rows_grad_kernel<R, KM, 1, false>), grid, dim3(256), 0, s, a);
-      }
+      // waves a token by its 1 KiB runs: one, two or four up to as many, four
+      // for longer rows, and sixteen where few tokens leave compute units idle
+      const int runs = (a.H / R::kVec + 63) / 64;
+      auto launch = [&](auto wpt) {
+        constexpr int W = decltype(wpt)::value, tpb = W < 4 ? 4 / W : 1;
+        const dim3 grid((a.T + tpb - 1) / tpb), block(W < 4 ? moe::kMoveThreads : W * 64);
+        if (to_tokens) hipLaunchKernelGGL((moe::rows_grad_kernel<R, KM, W, true>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((moe::rows_grad_kernel<R, KM, W, false>), grid, block, 0, s, a);
+      };
+      if (runs <= 1) launch(std::integral_constant<int, 1>{});
+      else if (runs <= 2) launch(std::integral_constant<int, 2>{});
+      else if (runs >= 8 && a.T <= 512) launch(std::integral_constant<int, 16>{});
+      else launch(std::integral_constant<int, 4>{});
       return hipGetLastError();
     });
   });

@@ -184,7 +184,7 @@ def run_layer(lib, T, k, E, H, I, seed, p_drop=0.0, ids=None, x=None, W=None):
 # E, H, I, k, T, p_drop, tile rows.  Register streaming on 16- and 32-row
 # tiles, strips on 64, 96, 128, 160 and 192; reductions in groups of 4, 2 and 1 units
 # and every stage length of the strips (units 4, 6, 2, 5, 3, 1); H not a
-# multiple of 256.
+# multiple of 256; down reductions in 2, 4 and 8 slices.
 SHAPES = [
     (8, 512, 512, 2, 5, 0.0, 16),
     (16, 256, 384, 4, 33, 0.1, 32),
@@ -204,6 +204,10 @@ SHAPES = [
     (4, 512, 512, 2, 130, 0.0, 96),
     (4, 768, 640, 2, 220, 0.1, 160),
     (3, 1280, 768, 3, 110, 0.0, 160),
+    (4, 512, 2048, 2, 130, 0.0, 96),
+    (8, 384, 1024, 2, 100, 0.1, 64),
+    (2, 256, 2048, 1, 300, 0.0, 192),
+    (192, 1024, 640, 2, 1200, 0.0, 64),
     (4, 512, 512, 2, 300, 0.0, 192),
     (3, 768, 640, 2, 310, 0.1, 192),
     (2, 384, 1280, 1, 400, 0.0, 192),
