@@ -231,7 +231,7 @@ void plan_mx4(int T, int k, int E, int H, int I, Plan* p) {
     // K slices of the down reduction while its items leave CUs without one
     // (Mixtral-8x7B-shaped T = 80, 128 items: 161 -> 149 us, T = 200 174 -> 159)
     const long items = tasks(std::min(active, expected_active(T, k, E))) * strips;
-    const int nk = moe_host::mx4_strip_stages(p->mb, I);
+    const int nk = moe_host::mx4_down_stages(p->mb, I);
     while (items * p->split2 * 5 < kPlanCUs * 4 && nk % (2 * p->split2) == 0 && p->split2 < 8) p->split2 *= 2;
     return;
   }
@@ -995,8 +995,22 @@ int forward_mx4(const void* x, const float* topk_w, const void* routing, const v
   }
   if (!p.dr_waves) {
     StageScope st(s, 4);
-    e = moe_host::launch_reduce(ws + W.y, p.split2 == 1, p.split2, P, topk_w, R.pair_pos, R.expert_offsets, nullptr, E,
-                                T, k, H, static_cast<uint16_t*>(out), s);
+    if (p.split2 == 1) {   // bf16 rows: the weighted sum of moe_combine
+      moe_host::RowMoveArgs m{};
+      m.rows = ws + W.y;
+      m.w = topk_w;
+      m.pair_pos = R.pair_pos;
+      m.expert_offsets = R.expert_offsets;
+      m.out = out;
+      m.T = T;
+      m.k = k;
+      m.E = E;
+      m.H = H;
+      e = moe_host::launch_rows_to_tokens(m, MOE_ROW_BF16, s);
+    } else {
+      e = moe_host::launch_reduce(ws + W.y, false, p.split2, P, topk_w, R.pair_pos, R.expert_offsets, nullptr, E, T, k,
+                                  H, static_cast<uint16_t*>(out), s);
+    }
     if (e != hipSuccess) return MOE_ERR_HIP;
   }
   return MOE_OK;

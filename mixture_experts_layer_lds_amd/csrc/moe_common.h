@@ -453,8 +453,8 @@ struct Mx4Args {
 hipError_t launch_mx4_stream(const Mx4Args& a, bool gateup, int mb, int waves, int grid, hipStream_t s);
 // One token: down GEMM and top-k weighted sum, out (bf16 [H]) in a.c.
 hipError_t launch_mx4_down_reduce(const Mx4Args& a, hipStream_t s);
-// mb in {4, 6, 8, 10, 12}; a.split divides mx4_strip_stages
-int mx4_strip_stages(int mb, int K);   // stages of a strip's reduction over K
+// mb in {4, 6, 8, 10, 12}; a.split divides mx4_down_stages
+int mx4_down_stages(int mb, int K);   // stages of a down strip's reduction over K
 hipError_t launch_mx4_strip(const Mx4Args& a, bool gateup, int mb, int grid, hipStream_t s);
 
 // Rows between token and expert order (rows.hip).

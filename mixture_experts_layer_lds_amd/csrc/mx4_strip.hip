@@ -484,23 +484,26 @@ static hipError_t launch_mx4_strip_t(const moe_host::Mx4Args& a, int grid, hipSt
 }
 
 // Groups a stage: four to six units where the reduction divides into them
-// (shorter stages leave too little in flight).  160- and 192-row tiles: two slots
-// of six units do not fit the LDS or five spill registers.
-static int mx4_stage_groups(int mb, int K) {
+// (shorter stages leave too little in flight; Qwen2-57B-shaped slice, T = 1024,
+// down over five units on 160-row tiles, one stage instead of five: 39.0 -> 36.3
+// us).  Taller tiles have no registers for the longer stages, the gate-up, whose
+// sources and epilogue take more, from 160 rows on, the down from 192.
+static int mx4_stage_groups(int mb, int K, bool gateup) {
   const int units = K / 128;
+  const bool room = mb <= (gateup ? 8 : 10);
   if (units % 4 == 0) return 1;
-  if (units % 2 == 0) return mb <= 8 && units % 6 == 0 ? 3 : 1;
-  if (mb <= 8 && units % 5 == 0) return 5;
+  if (units % 2 == 0) return room && units % 6 == 0 ? 3 : 1;
+  if (room && units % 5 == 0) return 5;
   return units % 3 == 0 ? 3 : 1;
 }
 
-static int mx4_strip_stages(int mb, int K) { return K / 128 / mx4_group(K) / mx4_stage_groups(mb, K); }
+static int mx4_strip_stages(int mb, int K, bool gateup) { return K / 128 / mx4_group(K) / mx4_stage_groups(mb, K, gateup); }
 
 template <int MB, bool GATEUP>
 static hipError_t launch_mx4_strip_g(const moe_host::Mx4Args& a, int grid, hipStream_t s) {
-  const int G = mx4_group(a.K), GS = mx4_stage_groups(MB, a.K);
+  const int G = mx4_group(a.K), GS = mx4_stage_groups(MB, a.K, GATEUP);
   if (G == 4) return launch_mx4_strip_t<MB, 4, 1, GATEUP>(a, grid, s);
-  if constexpr (MB <= 8) {
+  if constexpr (MB <= (GATEUP ? 8 : 10)) {
     if (G == 2 && GS == 3) return launch_mx4_strip_t<MB, 2, 3, GATEUP>(a, grid, s);
     if (GS == 5) return launch_mx4_strip_t<MB, 1, 5, GATEUP>(a, grid, s);
   }
@@ -513,11 +516,11 @@ static hipError_t launch_mx4_strip_g(const moe_host::Mx4Args& a, int grid, hipSt
 
 namespace moe_host {
 
-int mx4_strip_stages(int mb, int K) { return moe::mx4_strip_stages(mb, K); }
+int mx4_down_stages(int mb, int K) { return moe::mx4_strip_stages(mb, K, false); }
 
 hipError_t launch_mx4_strip(const Mx4Args& a, bool gateup, int mb, int grid, hipStream_t s) {
   if (a.K % 128 || a.N_out % 128 || a.w_rows != (gateup ? 2 : 1) * a.N_out) return hipErrorInvalidValue;
-  if (a.split < 1 || (gateup && a.split > 1) || moe::mx4_strip_stages(mb, a.K) % a.split) return hipErrorInvalidValue;
+  if (a.split < 1 || (gateup && a.split > 1) || moe::mx4_strip_stages(mb, a.K, gateup) % a.split) return hipErrorInvalidValue;
 #define MOE_MX4_CASE(M) \
   if (mb == M) return gateup ? moe::launch_mx4_strip_g<M, true>(a, grid, s) : moe::launch_mx4_strip_g<M, false>(a, grid, s);
   MOE_MX4_CASE(4) MOE_MX4_CASE(6) MOE_MX4_CASE(8) MOE_MX4_CASE(10) MOE_MX4_CASE(12)
