@@ -221,8 +221,9 @@ void plan_mx4(int T, int k, int E, int H, int I, Plan* p) {
   const long avg = active > 0 ? (P + active - 1) / active : 1;
   const long strips = (H + kStripCols - 1) / kStripCols;   // of the down product; the gate-up has I / 128
   const bool wide = active * std::min((long)I / 128, strips) >= 3 * kPlanCUs;
-  p->tiling = avg <= 8 || (avg <= 16 && !wide) ? kStreaming : kStrips;
-  p->mb = p->tiling == kStreaming ? (avg <= 8 ? 1 : 2)
+  const bool few = avg <= 8 || T == 1;   // (one token: at most 16 rows, and the down launch takes 16-row tiles)
+  p->tiling = few || (avg <= 16 && !wide) ? kStreaming : kStrips;
+  p->mb = p->tiling == kStreaming ? (few ? 1 : 2)
                                   : (avg <= 40 ? 4 : (avg <= 72 ? 6 : (avg <= 96 ? 8 : (avg <= 128 ? 10 : 12))));
   p->block_m = 16 * p->mb;
   p->max_tasks = (int)(P / p->block_m + active);

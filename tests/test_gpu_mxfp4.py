@@ -223,11 +223,11 @@ def test_layer_parity(lib, E, H, I, k, T, p_drop, bm):
     check_layer(lib, x, ids, w, W, out, routing, ws, (T, k, E, H, I), f"E={E} T={T}")
 
 
-@pytest.mark.parametrize("k,E,H,I", [(1, 4, 256, 256), (8, 64, 512, 512), (16, 40, 384, 768), (5, 5, 640, 640)])
+@pytest.mark.parametrize("k,E,H,I", [(1, 4, 256, 256), (16, 1, 256, 384), (8, 64, 512, 512), (16, 40, 384, 768), (5, 5, 640, 640)])
 def test_one_token(lib, k, E, H, I):
     # the down launch adds the token's rows; one pair dropped, and two pairs of one expert
     ids = random_ids(1, k, E, seed=k)
-    if k > 4:
+    if k > 4:   # (one expert: sixteen rows of it, one dropped)
         ids[0, 1] = -1
         ids[0, 3] = ids[0, 2]
     x, ids, w, W, _, out, routing, ws = run_layer(lib, 1, k, E, H, I, 50 + k, ids=ids)
