@@ -194,7 +194,15 @@ long expected_active(int T, int k, int E) {
 
 // Waves per workgroup of the MXFP4 streaming kernel: the count that minimises
 // (items per workgroup slot) x (groups per wave + 1, the first loads' latency).
+// From two and a half items a slot, four waves where they idle for at most an
+// eighth of their steps: an item then ends sooner, so the last ones leave less of the
+// device without work (gate-up / down in us, one wave against four:
+// DeepSeek-V3-shaped T = 64 522 -> 517 / 281 -> 269, T = 8 down 84 -> 77,
+// Mixtral-8x7B T = 4 gate-up 66 -> 52, a quarter of Qwen2-57B T = 64 36 -> 31
+// and, of five groups, which this leaves to the first rule, down 19.5 -> 26.1;
+// two items a slot, 32 experts of 2048 x 1024 at T = 8, 13.6 -> 14.8).
 int pick_mx4_waves(int groups, long items) {
+  if (2 * items >= 5 * (kStreamWaves / 4) && 7 * ((groups + 3) / 4 * 4) <= 8 * groups) return 4;
   int best = 1;
   long best_cost = -1;
   for (int w = 1; w <= 8 && w <= groups; w *= 2) {
