@@ -6,16 +6,15 @@
 
 namespace moe {
 
-// g / (1 + e^-g).  e^-g = 2^(t + r) with t = -g log2(e) rounded and r the rest
-// of the product: 2^t (1 + r ln 2) from the hardware's 2^x, and its reciprocal
-// (each within a step of fp32).  About a quarter of the instructions of the
-// library exponential and the division, which took 6 us a tile of 192 rows.
+// g / (1 + e^-g) by the hardware's 2^x and reciprocal (each within a step of
+// fp32).  Rounding g log2(e) leaves e^-g off by |g| 2^-23 of itself, a share of
+// the sum's own rounding error; an infinite e^-g gives a zero.  Two
+// transcendental instructions of sixteen cycles a wave and three others of
+// four: the library exponential and a division take several times that, and
+// keeping the rest of the product in a second term twice that, of an epilogue
+// that the whole CU waits for.
 __device__ __forceinline__ float mx4_silu(float g) {
-  constexpr float kLog2e = 1.44269504088896340736f, kLog2eLo = 1.92596299112661746887e-8f, kLn2 = 0.69314718055994530942f;
-  const float t = -g * kLog2e;
-  const float r = __builtin_fmaf(-g, kLog2e, -t) - g * kLog2eLo;
-  const float p = __builtin_fminf(__builtin_amdgcn_exp2f(t), 3.4028234664e38f);   // no inf times r
-  return g * __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(p * kLn2, r, p));
+  return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * g));
 }
 
 // Where the 32 columns `c32` of 16-row block `slot` go, for rows of `units`

@@ -30,11 +30,16 @@
 // whose number is fixed, so the wait at the head of a stage is an exact count.
 //
 // Measured (us, TB/s of weights with their scale codes): DeepSeek-V3-shaped
-// gate-up / down at T = 1024 609 (6.6) / 369 (5.4), at 4096 868 (4.6) / 486
-// (4.1).  Per CU a stage moves 70 KiB of weights and 17 to 52 KiB of token
-// rows, about 30 GB/s in all at every tile height, with the MFMA busy 29% of
-// the time at T = 4096 and the L1 stalled on pending data for 57%: what bounds
-// it is the CU's path to memory, which the token rows share with the weights.
+// gate-up / down at T = 1024 622 (6.4) / 372 (5.4), at 4096 827 (4.8) / 485
+// (4.1); Mixtral-8x7B-shaped T = 2048 293 / 166, 3.3 and 2.9 PFLOP/s.  Few
+// rows an expert run at the rate of the weight stream.  At T = 4096 the
+// gate-up takes 745 us without its token copies, 800 without its
+// multiplications and 560 without its weight loads: per CU a stage moves 70
+// KiB of weights and 17 to 52 KiB of token rows, about 30 GB/s in all at every
+// tile height, with the L1 stalled on pending data for 57% of the time: what
+// bounds it is the CU's path to memory, which the token rows share with the
+// weights.  (Four waves of twice the weight rows, half the LDS reads, ran in
+// the same time.)
 #include "lds_dma.h"
 #include "mx4_epilogue.h"
 
@@ -209,7 +214,8 @@ mx4_strip_kernel(moe_host::Mx4Args g) {
 
   const int num_tasks = min(g.header[kHdrNumTasks], g.max_tasks);
   const int n_strips = GATEUP ? g.N_out / 128 : (g.N_out + 255) / 256;
-  const int total = num_tasks * n_strips * g.split;   // < 2^31: see the launch
+  // tasks < 65536 / 64 + 512, strips <= 512, slices <= 8: under 2^23
+  const int total = num_tasks * n_strips * g.split; 
   const int nk = g.K / 128 / U / g.split;             // stages per item
   const int units2 = g.N_out / 128, G2 = units2 % 4 == 0 ? 4 : (units2 % 2 == 0 ? 2 : 1);
 
