@@ -120,8 +120,8 @@ struct Mx4Item {
 };
 
 // The item's token sources.  pairs: the pair index of each of the tile's rows
-// (LDS; gate-up only); inv_topk: 2^20 / topk rounded up (pair * inv_topk >> 20
-// is pair / topk: pair < 2^16, topk <= 16).
+// (LDS; gate-up only); inv_topk: 2^31 / topk rounded up (2 pair inv_topk / 2^32
+// is less than pair / topk + 2^-15: the quotient, as pair < 2^16, topk <= 16).
 template <int MB, int G, int GS, bool GATEUP>
 __device__ __forceinline__ Mx4Item<MB, G, GS> mx4_item(const moe_host::Mx4Args& g, const Mx4Place& at, const int* pairs,
                                                        uint32_t inv_topk, int wave, int lane) {
@@ -139,7 +139,7 @@ __device__ __forceinline__ Mx4Item<MB, G, GS> mx4_item(const moe_host::Mx4Args& 
     const int c = (wave + kMx4Waves * i) % (MB * St::U);   // chunk: row block c / U, unit c % U
     const int rb = c / St::U, u = c % St::U;
     if constexpr (GATEUP) {
-      const uint32_t tok = (uint32_t)pairs[rb * 16 + tok_copy_row(lane)] * inv_topk >> 20;
+      const uint32_t tok = __umulhi(2u * (uint32_t)pairs[rb * 16 + tok_copy_row(lane)], inv_topk);
       it.a[i] = tok * (uint32_t)(g.K / 2) + u * 64 + 16 * tok_copy_piece(lane);
     } else {
       it.a[i] = (rb * 16 < at.rows ? rb : 0) * block_bytes + u / G * (G * kMx4Unit) + u % G * 1024 + 16 * lane;
@@ -150,7 +150,7 @@ __device__ __forceinline__ Mx4Item<MB, G, GS> mx4_item(const moe_host::Mx4Args& 
     const int c = (wave + kMx4Waves * i) % (MB * GS);      // row block c / GS, group c % GS
     const int rb = c / GS, j = c % GS;
     if constexpr (GATEUP) {
-      const uint32_t tok = (uint32_t)pairs[rb * 16 + (lane & 15)] * inv_topk >> 20;
+      const uint32_t tok = __umulhi(2u * (uint32_t)pairs[rb * 16 + (lane & 15)], inv_topk);
       it.s[i] = tok * (uint32_t)(g.K / 32) + 4 * G * j + (((lane >> 4) * G) & ~3);
     } else {
       it.s[i] = (rb * 16 < at.rows ? rb : 0) * block_bytes + j * (G * kMx4Unit) + G * 1024 + ((lane * G) & ~3);
@@ -241,7 +241,7 @@ mx4_strip_kernel(moe_host::Mx4Args g) {
     // from pair indices that were copied to LDS an item earlier still (three
     // places, so that no wave overwrites what another still reads).  Past the
     // last item: the last one again, its first stage loaded and never used.
-    const uint32_t inv_topk = ((1u << 20) + g.topk - 1) / g.topk;
+    const uint32_t inv_topk = ((1u << 31) + g.topk - 1) / g.topk;
     auto place = [&](int i) __attribute__((always_inline)) { return mx4_place<MB>(g, vid + min(i, n_items - 1) * gs, n_strips, nk); };
     auto copy_pairs = [&](const Mx4Place& p, int i) __attribute__((always_inline)) {
       if constexpr (GATEUP) {

@@ -223,6 +223,13 @@ def test_layer_parity(lib, E, H, I, k, T, p_drop, bm):
     check_layer(lib, x, ids, w, W, out, routing, ws, (T, k, E, H, I), f"E={E} T={T}")
 
 
+@pytest.mark.parametrize("T,k,E,H,I", [(5000, 1, 16, 256, 128), (8192, 8, 64, 128, 256), (65536, 1, 128, 128, 128)])
+def test_thousands_of_tokens(lib, T, k, E, H, I):
+    # token indices over the whole range of pairs
+    x, ids, w, W, _, out, routing, ws = run_layer(lib, T, k, E, H, I, 70 + k, p_drop=0.01)
+    check_layer(lib, x, ids, w, W, out, routing, ws, (T, k, E, H, I), f"T={T}")
+
+
 @pytest.mark.parametrize("k,E,H,I", [(1, 4, 256, 256), (16, 1, 256, 384), (8, 64, 512, 512), (16, 40, 384, 768), (5, 5, 640, 640)])
 def test_one_token(lib, k, E, H, I):
     # the down launch adds the token's rows; one pair dropped, and two pairs of one expert
