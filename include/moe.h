@@ -460,8 +460,8 @@ int moe_forward_mxfp8(const void *x, const float *topk_w, const void *routing,
  * v * 2^-s rounded to nearest even, at most 6.  A block that holds an Inf or
  * a NaN takes scale code 255 (NaN) and zero codes: all its values are NaN.
  * Requires cols % 32 == 0, row_stride >= cols, row_stride * element size a
- * multiple of 16 bytes, x 16-byte and codes 4-byte aligned.  rows == 0
- * returns MOE_OK with no launch.
+ * multiple of 16 bytes, rows * cols * element size under 2^38, x 16-byte and
+ * codes 4-byte aligned.  rows == 0 returns MOE_OK with no launch.
  * moe_dequantize_mxfp4: the values of such codes, out (device, 16-byte
  * aligned) [rows][cols] of row_type, rounded to nearest even where the type
  * does not hold them (fp16: large and small scales; bf16: subnormals). */
@@ -487,8 +487,9 @@ int moe_pack_weights_mxfp4(const uint8_t *codes, const uint8_t *scales, int E, i
  * per token and SiLU(gate)*up per (token, expert) row by the rule of
  * moe_quantize_mxfp4; the products run on the scaled MFMA in its 4-bit mode
  * with fp32 accumulation, SiLU(gate)*up is formed and quantised from the fp32
- * sums, and the per-pair down rows are stored as bf16 (at T = 1 they are added
- * in fp32 and not stored).  A NaN or Inf in a token's row, in a weight or in an
+ * sums, and the per-pair down rows are stored as bf16 (as fp32 sums where
+ * moe_workspace_layout names slices of the down reduction; at T = 1 they are
+ * added in fp32 and not stored).  A NaN or Inf in a token's row, in a weight or in an
  * intermediate makes the values of its block NaN, and with them the outputs
  * that they enter.  H and I must be multiples of 128.
  * moe_route_forward_mxfp4: both in one call, with the same results; at most
@@ -523,7 +524,7 @@ int moe_route_forward_mxfp4(const int32_t *topk_ids, const void *x, const float 
  * then not read and may be NULL; with dtopk_w, topk_w must be given.
  * Dropped pairs add nothing, their weights are not read into any result and
  * their dw is 0; a token whose pairs are all dropped gets a zero row.  Sorted
- * rows behind the last valid one are neither read nor written.  Products and
+ * rows behind the last valid one take no part and are not written.  Products and
  * sums run in fp32, in ascending j (dw: in a fixed order), rounded once.
  * Requires 1 <= k <= 16, T*k <= 65536, 1 <= E <= 511, H a multiple of 8 (at
  * most 65536), rows 16-byte aligned, no overlap of inputs and outputs. */
@@ -547,7 +548,7 @@ int moe_combine_grad(const void *dout, const void *y, int row_type, const float 
  *   renormalize = 0   dl[e] = (w_j dw_j where e = e_j) - p[e] s
  * The choice itself is a constant, and so are the n_shared columns' weights.
  * logits is read with renormalize = 0 only (NULL otherwise allowed); a NaN
- * score has p = 0.  Same limits as moe_router_topk. */
+ * score has p = 0.  Same limits as moe_router_topk, and T at most 2^25. */
 int moe_router_topk_grad(const float *logits, const int32_t *topk_ids, const float *topk_w,
                          const float *dtopk_w, int T, int E, int k, int renormalize, int n_shared,
                          float *dlogits, void *stream);

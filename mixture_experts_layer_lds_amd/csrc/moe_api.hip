@@ -1793,6 +1793,10 @@ int row_bytes_of(int row_type) {
   return row_type == MOE_ROW_BF16 || row_type == MOE_ROW_FP16 ? 2 : (row_type == MOE_ROW_FP32 ? 4 : 0);
 }
 
+// Most rows of one MXFP4 pass: 2^38 bytes of them, whose threads (a 16-byte
+// vector each, four from 2^18 vectors on) a launch can count in 32 bits.
+int64_t max_mx4_rows(int cols, int esz) { return ((int64_t)1 << 38) / ((int64_t)cols * esz) - 1; }
+
 // Sizes and the routing buffer of a row operator, and its arguments from
 // them; *done: nothing to do (T == 0).
 int check_rows(int row_type, const void* routing, size_t routing_bytes, int T, int k, int E, int H,
@@ -2012,7 +2016,7 @@ int moe_quantize_mxfp4(const void* x, int row_type, int64_t rows, int cols, int6
                        uint8_t* scales, void* stream) {
   const int esz = row_bytes_of(row_type);
   if (!esz || rows < 0 || cols <= 0 || row_stride < cols) return MOE_ERR_INVALID_ARG;
-  if (cols % 32 || row_stride > (int64_t)1 << 40 || (row_stride * esz) % 16 || rows > (int64_t)1 << 40)
+  if (cols % 32 || row_stride > (int64_t)1 << 40 || (row_stride * esz) % 16 || rows > max_mx4_rows(cols, esz))
     return MOE_ERR_UNSUPPORTED_SHAPE;
   if (rows == 0) return MOE_OK;
   if (!x || !codes || !scales || !aligned(x, 16) || !aligned(codes, 4)) return MOE_ERR_INVALID_ARG;
@@ -2023,8 +2027,9 @@ int moe_quantize_mxfp4(const void* x, int row_type, int64_t rows, int cols, int6
 
 int moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols, int row_type, void* out,
                          void* stream) {
-  if (!row_bytes_of(row_type) || rows < 0 || cols <= 0) return MOE_ERR_INVALID_ARG;
-  if (cols % 32 || rows > (int64_t)1 << 40) return MOE_ERR_UNSUPPORTED_SHAPE;
+  const int esz = row_bytes_of(row_type);
+  if (!esz || rows < 0 || cols <= 0) return MOE_ERR_INVALID_ARG;
+  if (cols % 32 || rows > max_mx4_rows(cols, esz)) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (rows == 0) return MOE_OK;
   if (!codes || !scales || !out || !aligned(codes, 4) || !aligned(out, 16)) return MOE_ERR_INVALID_ARG;
   const hipError_t e = moe_host::launch_mx4_dequantize(codes, scales, (size_t)rows, cols, row_type, out,
@@ -2146,7 +2151,8 @@ int moe_router_topk_grad(const float* logits, const int32_t* topk_ids, const flo
                          int T, int E, int k, int renormalize, int n_shared, float* dlogits, void* stream) {
   if (T < 0 || E < 1 || k < 1 || k > E || n_shared < 0 || (renormalize != 0 && renormalize != 1))
     return MOE_ERR_INVALID_ARG;
-  if (E > moe_host::router_max_experts() || k + n_shared > moe::kMaxTopK || E + n_shared > moe::kMaxExperts)
+  if (E > moe_host::router_max_experts() || k + n_shared > moe::kMaxTopK || E + n_shared > moe::kMaxExperts ||
+      T > 1 << 25)
     return MOE_ERR_UNSUPPORTED_SHAPE;
   if (T == 0) return MOE_OK;
   if (!topk_ids || !topk_w || !dtopk_w || !dlogits || (!renormalize && !logits)) return MOE_ERR_INVALID_ARG;

@@ -88,6 +88,17 @@ def test_quantize_strided_rows(lib):
         assert torch.equal(codes.cpu(), rc) and torch.equal(scales.cpu(), rs)
 
 
+def test_quantize_past_32_bit_offsets(lib):
+    rows, cols = 66001, 65536        # 4.3e9 values
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_()
+    codes, scales = lib.moe_quantize_mxfp4(x)
+    back = lib.moe_dequantize_mxfp4(codes, scales)
+    for r in (0, 32767, 32768, 65535, 65536, rows - 1):
+        rc, rs = ref.quantize(x[r:r + 1].cpu())
+        assert torch.equal(codes[r:r + 1].cpu(), rc) and torch.equal(scales[r:r + 1].cpu(), rs), r
+        assert torch.equal(back[r:r + 1].cpu().double(), ref.dequantize(rc, rs)), r
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
 def test_dequantize_every_code_and_scale(lib, dtype):
     scales = torch.arange(256, dtype=torch.uint8).repeat_interleave(1).view(256, 1)

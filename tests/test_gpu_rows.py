@@ -128,6 +128,39 @@ def test_gradients(lib, T, k, E, H, p_drop, dtype):
     assert torch.equal(lib.moe_combine_grad(x.cuda(), routing, k, E, topk_w=w.cuda())[:n], dy[:n])
 
 
+def test_past_32_bit_offsets(lib):
+    # the largest count of pairs on the widest rows: 2^32 values of sorted rows
+    T, k, E, H = 4096, 16, 40, 65536
+    ids = random_ids(T, k, E, seed=3, p_drop=0.01)
+    w = torch.randn(T, k)
+    routing = lib.alloc_routing(T, k, E, 128, 128, "bf16")
+    lib.build_routing(ids.cuda(), E, 128, 128, routing, "bf16")
+    pos, _, off = ref.sorted_order(ids, E)
+    n, valid = int(off[E]), ((ids >= 0) & (ids < E))
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda").normal_()
+    xs = lib.moe_dispatch(x, routing, k, E, topk_w=w.cuda())
+    dx, dw = lib.moe_dispatch_grad(xs, routing, k, E, x=x, topk_w=w.cuda())
+    out = lib.moe_combine(xs, routing, k, E)
+    dy, dv = lib.moe_combine_grad(x, routing, k, E, y=xs, topk_w=w.cuda())
+    u = half_step(torch.bfloat16)
+    order = torch.argsort(pos)
+    for r in (0, 1, 32767, 32768, 65535 - (T * k - n), n // 2, n - 1):
+        p = int(order[r])
+        want = x[p // k].cpu().double() * w.double().flatten()[p]
+        within(xs[r], want, want.abs() * (U + u) + 2.0 ** -133, f"dispatch row {r}")
+        assert torch.equal(dy[r], xs[r]), f"combine gradient row {r}"
+    for t in (0, 2047, 2048, T - 1):
+        ok = valid[t]
+        rows = xs[pos.view(T, k)[t].clamp(max=n - 1).cuda()].cpu().double() * ok.unsqueeze(1)
+        ww = w[t].double().unsqueeze(1) * ok.unsqueeze(1)
+        for got, f, what in ((dx[t], ww, "dispatch gradient"), (out[t], torch.ones_like(ww), "combine")):
+            want, mag = (rows * f).sum(0), (rows * f).abs().sum(0)
+            within(got, want, (k + 1) * U * mag + u * want.abs() + 2.0 ** -133, f"{what} of token {t}")
+        prod = rows * x[t].cpu().double()
+        for got in (dw[t], dv[t]):   # four waves or more: H / 512 / 4 * 8 columns a lane
+            within(got, prod.sum(1), (H // 256 + 13) * U * prod.abs().sum(1), f"weight gradient of token {t}")
+
+
 def test_gradients_against_differences(lib):
     # fp32 rows: a step of one input along a direction changes <out, r> by the gradient's product with it
     T, k, E, H = 19, 4, 12, 264

@@ -131,6 +131,16 @@ def test_row_operator_refusals(m):
     assert g(NULL, NULL, NULL, NULL, 0, E, k, 1, 0, NULL, NULL) == 0
 
 
+def test_counts_past_the_launch_limits(m):
+    lib = m._lib
+    # rows of 2^38 bytes and more
+    for rows, cols, row_type in ((1 << 32, 32, 0), (1 << 31, 32, 2), (1 << 62, 64, 0), (64, 1 << 30, 2), ((1 << 63) - 1, 32, 1)):
+        assert lib.moe_quantize_mxfp4(FAKE, row_type, rows, cols, cols, FAKE, FAKE, NULL) == -2, (rows, cols)
+        assert lib.moe_dequantize_mxfp4(FAKE, FAKE, rows, cols, row_type, FAKE, NULL) == -2, (rows, cols)
+    for T in ((1 << 25) + 1, (1 << 31) - 1):
+        assert lib.moe_router_topk_grad(FAKE, FAKE, FAKE, FAKE, T, 8, 2, 1, 0, FAKE, NULL) == -2
+
+
 def test_binding_refuses_wrong_tensors(m):
     """Shapes, types, strides and devices are refused before the library is called."""
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
