@@ -760,6 +760,14 @@ def _empty(like, shape, dtype, stream):
         return like.new_empty(shape, dtype=dtype)
 
 
+def _output(name, t, like, shape, dtype, stream):
+    """The caller's output t, checked, or a new one."""
+    if t is None:
+        return _empty(like, shape, dtype, stream)
+    _is(name, t, dtype, shape)
+    return t
+
+
 def _row_type(name, t):
     if t.dtype not in ROW_TYPES:
         raise ValueError(f"{name}: expected bf16, fp16 or fp32 rows, got {t.dtype}")
@@ -771,21 +779,17 @@ def moe_quantize_mxfp4(x, codes=None, scales=None, stream=None):
     contiguous rows apart by x.stride(0)): (codes uint8 [..., cols / 2], scales
     uint8 [..., cols / 32]).  A block that holds Inf or NaN becomes NaN."""
     kind = _row_type("x", x)
-    if x.dim() < 1 or x.shape[-1] % 32 or x.shape[-1] == 0:
+    *lead, cols = x.shape or (0,)
+    if cols % 32 or cols == 0:
         raise ValueError(f"x: expected rows of a multiple of 32 values, got {tuple(x.shape)}")
-    cols = x.shape[-1]
     stride = cols
     if not x.is_contiguous():
         if x.dim() != 2 or x.stride(1) != 1 or x.stride(0) < cols:
             raise ValueError(f"x: expected contiguous rows, got strides {x.stride()}")
         stride = x.stride(0)
-    if codes is None:
-        codes = _empty(x, (*x.shape[:-1], cols // 2), torch.uint8, stream)
-    if scales is None:
-        scales = _empty(x, (*x.shape[:-1], cols // 32), torch.uint8, stream)
-    _is("codes", codes, torch.uint8, (*x.shape[:-1], cols // 2))
-    _is("scales", scales, torch.uint8, (*x.shape[:-1], cols // 32))
     dev = _check_device(x, codes, scales)
+    codes = _output("codes", codes, x, (*lead, cols // 2), torch.uint8, stream)
+    scales = _output("scales", scales, x, (*lead, cols // 32), torch.uint8, stream)
     _check("moe_quantize_mxfp4", _lib.moe_quantize_mxfp4(
         x.data_ptr(), kind, x.numel() // cols, cols, stride, codes.data_ptr(), scales.data_ptr(), _here(dev, stream)))
     return codes, scales
@@ -796,14 +800,13 @@ def moe_dequantize_mxfp4(codes, scales, dtype=torch.bfloat16, out=None, stream=N
     scale codes [..., cols / 32]."""
     if codes.dim() < 1 or codes.shape[-1] % 16 or codes.shape[-1] == 0:
         raise ValueError(f"codes: expected rows of a multiple of 16 bytes, got {tuple(codes.shape)}")
-    lead, cols = codes.shape[:-1], 2 * codes.shape[-1]
-    if out is None:
-        out = _empty(codes, (*lead, cols), dtype, stream)
-    kind = _row_type("out", out)
-    _is("codes", codes, torch.uint8, (*lead, cols // 2))
+    *lead, half = codes.shape
+    cols = 2 * half
+    _is("codes", codes, torch.uint8, codes.shape)
     _is("scales", scales, torch.uint8, (*lead, cols // 32))
-    _is("out", out, out.dtype, (*lead, cols))
     dev = _check_device(codes, scales, out)
+    out = _output("out", out, codes, (*lead, cols), dtype if out is None else out.dtype, stream)
+    kind = _row_type("out", out)
     _check("moe_dequantize_mxfp4", _lib.moe_dequantize_mxfp4(
         codes.data_ptr(), scales.data_ptr(), out.numel() // cols, cols, kind, out.data_ptr(), _here(dev, stream)))
     return out
@@ -877,14 +880,11 @@ def _rows(name, t, k, sorted_rows):
 def _move(name, fn, src, src_name, sorted_src, routing, k, E, topk_w, out, out_name, stream):
     kind = _row_type(src_name, src)
     T, H = _rows(src_name, src, k, sorted_src)
-    shape = (T, H) if sorted_src else (T * k, H)
-    if out is None:
-        out = _empty(src, shape, src.dtype, stream)
     _is(src_name, src, src.dtype, src.shape)
-    _is(out_name, out, src.dtype, shape)
     if topk_w is not None:
         _is("topk_w", topk_w, torch.float32, (T, k))
     dev = _check_device(src, out, topk_w, routing)
+    out = _output(out_name, out, src, (T, H) if sorted_src else (T * k, H), src.dtype, stream)
     _check(name, fn(src.data_ptr(), kind, _at(topk_w), routing.data_ptr(), routing.numel() * routing.element_size(),
                     T, k, E, H, out.data_ptr(), _here(dev, stream)))
     return out
@@ -911,18 +911,15 @@ def _move_grad(name, fn, grad, grad_name, sorted_grad, other, other_name, routin
     kind = _row_type(grad_name, grad)
     T, H = _rows(grad_name, grad, k, sorted_grad)
     shape = (T, H) if sorted_grad else (T * k, H)
-    if out is None:
-        out = _empty(grad, shape, grad.dtype, stream)
-    if other is not None and dw is None:
-        dw = _empty(grad, (T, k), torch.float32, stream)
     _is(grad_name, grad, grad.dtype, grad.shape)
-    _is(out_name, out, grad.dtype, shape)
     if topk_w is not None:
         _is("topk_w", topk_w, torch.float32, (T, k))
     if other is not None:
         _is(other_name, other, grad.dtype, shape)
-        _is("dtopk_w", dw, torch.float32, (T, k))
     dev = _check_device(grad, out, other, topk_w, dw, routing)
+    out = _output(out_name, out, grad, shape, grad.dtype, stream)
+    if other is not None:
+        dw = _output("dtopk_w", dw, grad, (T, k), torch.float32, stream)
     _check(name, fn(grad.data_ptr(), _at(other), kind, _at(topk_w), routing.data_ptr(),
                     routing.numel() * routing.element_size(), T, k, E, H, out.data_ptr(), _at(dw), _here(dev, stream)))
     return out if dw is None else (out, dw)
@@ -949,17 +946,17 @@ def moe_router_topk_grad(logits, topk_ids, topk_w, dtopk_w, renormalize=True, n_
     if logits.dim() != 2 or topk_ids.dim() != 2:
         raise ValueError("logits must be [T][E], topk_ids [T][k + n_shared]")
     T, E = logits.shape
-    ncol = topk_ids.shape[1]
-    if dlogits is None:
-        dlogits = _empty(logits, (T, E), torch.float32, stream)
-    _is("logits", logits, torch.float32, (T, E))
-    _is("topk_ids", topk_ids, torch.int32, (T, ncol))
-    _is("topk_w", topk_w, torch.float32, (T, ncol))
-    _is("dtopk_w", dtopk_w, torch.float32, (T, ncol))
-    _is("dlogits", dlogits, torch.float32, (T, E))
+    pairs = topk_ids.shape
+    _is("logits", logits, torch.float32, logits.shape)
+    _is("topk_ids", topk_ids, torch.int32, pairs)
+    if pairs[0] != T:
+        raise ValueError(f"topk_ids: expected {T} tokens, got {pairs[0]}")
+    _is("topk_w", topk_w, torch.float32, pairs)
+    _is("dtopk_w", dtopk_w, torch.float32, pairs)
     dev = _check_device(logits, topk_ids, topk_w, dtopk_w, dlogits)
+    dlogits = _output("dlogits", dlogits, logits, logits.shape, torch.float32, stream)
     _check("moe_router_topk_grad", _lib.moe_router_topk_grad(
-        logits.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(), dtopk_w.data_ptr(), T, E, ncol - n_shared,
+        logits.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(), dtopk_w.data_ptr(), T, E, pairs[1] - n_shared,
         1 if renormalize else 0, n_shared, dlogits.data_ptr(), _here(dev, stream)))
     return dlogits
 
