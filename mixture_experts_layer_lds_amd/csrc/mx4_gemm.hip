@@ -19,13 +19,16 @@
 //    one 16-byte store.
 //  * The group's weights (4 blocks x 1 KiB a unit) and scale codes (one dword
 //    a lane for all its units) go straight to registers, non-temporal, one
-//    group ahead of the one that is multiplied.
+//    group ahead of the one that is multiplied, the next item's first group
+//    ahead of the epilogue (Qwen3-30B-A3B-shaped T = 64 41.5 -> 39.8 us a
+//    layer, Mixtral-8x7B-shaped 145 -> 140, DeepSeek-V3-shaped T = 16 384 ->
+//    380).
 //  * The waves' sums meet in LDS and are added in ascending wave order.
 //
 // Measured, gate-up / down in us (TB/s of weights with their scale codes):
-// DeepSeek-V3-shaped T = 16 251 (6.5) / 126 (6.5), T = 64 518 (6.7) / 270
-// (6.4); Mixtral-8x7B-shaped T = 16 79 (6.3) / 41 (6.0); Qwen3-30B-A3B-shaped
-// T = 64 21 (4.0) / 12 (3.4), too short to reach the full rate.  One token,
+// DeepSeek-V3-shaped T = 16 249 (6.6) / 124 (6.6), T = 64 517 (6.7) / 266
+// (6.5); Mixtral-8x7B-shaped T = 16 78 (6.4) / 41 (6.0); Qwen3-30B-A3B-shaped
+// T = 64 19.5 (4.3) / 12 (3.4), too short to reach the full rate.  One token,
 // DeepSeek-V3-shaped: 20.5 (6.1) and, with the top-k sum, 14.3 (4.4).
 #include "decode_route.h"
 #include "lds_dma.h"
@@ -72,37 +75,43 @@ mx4_stream_kernel(moe_host::Mx4Args g) {
   const int per_xcd = gs / 8, extra = gs % 8;
   const int vid = (xcd < extra ? xcd * (per_xcd + 1) : extra * (per_xcd + 1) + (xcd - extra) * per_xcd) + slot;
 
-  for (int item = vid; item < total; item += gs) {
-    const int ti = item / n_groups;
-    const int cg = item - ti * n_groups;
-    const moe_task_t task = load_task_scalar(g.tasks + ti);
-    // 16-row weight blocks: gate 0, gate 1, up 0, up 1, or four of the output
-    const char* bp[kMx4NB];
+  if (vid >= total) return;
+  struct Stage {
+    u32x4 w[G][kMx4NB], t[G][MB];
+    uint32_t sw[kMx4NB], st[MB];
+  };
+  Stage s0, s1;
+  const char* bp[kMx4NB];
+  // 16-row weight blocks: gate 0, gate 1, up 0, up 1, or four of the output
+  auto blocks = [&](int expert, int cg) __attribute__((always_inline)) {
 #pragma unroll
     for (int q = 0; q < kMx4NB; q++) {
       const int blk = GATEUP ? (q & 1) + 2 * cg + (q >> 1) * (g.N_out / 16) : 4 * cg + q;
-      bp[q] = B + (size_t)task.expert * expert_bytes + (size_t)blk * block_bytes;
+      bp[q] = B + (size_t)expert * expert_bytes + (size_t)blk * block_bytes;
     }
-    struct Stage {
-      u32x4 w[G][kMx4NB], t[G][MB];
-      uint32_t sw[kMx4NB], st[MB];
-    };
-    auto load_weights = [&](Stage& f, int grp) __attribute__((always_inline)) {
-      const size_t at = (size_t)grp * (G * kMx4Unit);
+  };
+  auto load_weights = [&](Stage& f, int grp) __attribute__((always_inline)) {
+    const size_t at = (size_t)grp * (G * kMx4Unit);
+#pragma unroll
+    for (int q = 0; q < kMx4NB; q++)
+      f.sw[q] = __builtin_nontemporal_load(
+          reinterpret_cast<const uint32_t*>(mx4_piece<G>(bp[q] + at + G * 1024, lane)));
+#pragma unroll
+    for (int u = 0; u < G; u++)
 #pragma unroll
       for (int q = 0; q < kMx4NB; q++)
-        f.sw[q] = __builtin_nontemporal_load(
-            reinterpret_cast<const uint32_t*>(mx4_piece<G>(bp[q] + at + G * 1024, lane)));
-#pragma unroll
-      for (int u = 0; u < G; u++)
-#pragma unroll
-        for (int q = 0; q < kMx4NB; q++)
-          f.w[u][q] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(bp[q] + at + u * 1024 + 16 * lane));
-    };
-    // the first group's weights before the (dependent) look-up of the token rows
-    const int n = ngrp > wave ? (ngrp - wave + W - 1) / W : 0;
-    Stage s0, s1;
-    if (n > 0) load_weights(s0, wave);
+        f.w[u][q] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(bp[q] + at + u * 1024 + 16 * lane));
+  };
+  const int n = ngrp > wave ? (ngrp - wave + W - 1) / W : 0;   // groups of this wave
+  int item = vid, ti = item / n_groups;
+  moe_task_t task = load_task_scalar(g.tasks + ti);
+  blocks(task.expert, item - ti * n_groups);
+  // an item's first weights are loaded before the (dependent) look-up of its
+  // token rows, and from the second item on while the one before is finished
+  if (n > 0) load_weights(s0, wave);
+  for (;;) {
+    const int cg = item - ti * n_groups;
+    const int next = item + gs, next_ti = next < total ? next / n_groups : ti;
     // token rows: rows past the tile re-read its first row (a valid address
     // whose products land only in columns that are never stored)
     const char *ap[MB], *asp[MB];
@@ -158,8 +167,9 @@ mx4_stream_kernel(moe_host::Mx4Args g) {
     // Groups wave, wave + W, ...: no load sits under a condition inside the
     // loop, so each multiply waits for exactly its own group while the next
     // one is in flight.
+    if (n > 0) load_tokens(s0, wave);
+    const moe_task_t next_task = load_task_scalar(g.tasks + next_ti);
     if (n > 0) {
-      load_tokens(s0, wave);
       int i = 0;
       for (; i + 2 < n; i += 2) {
         load(s1, wave + (i + 1) * W);
@@ -176,11 +186,16 @@ mx4_stream_kernel(moe_host::Mx4Args g) {
       }
     }
 
+    if (next < total) {
+      blocks(next_task.expert, next - next_ti * n_groups);
+      if (n > 0) load_weights(s0, wave);
+    }
 #pragma unroll
     for (int m = 0; m < MB; m++)
 #pragma unroll
       for (int q = 0; q < kMx4NB; q++) red[wave][m][q][lane] = acc[m][q];
-    __syncthreads();
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the sums are in LDS
+    barrier_nofence();
 
     // Epilogue of row block m by wave m % W: lane holds token row lane % 16
     // and, of block q, output columns 8 (lane / 16) + 4 (q % 2) + i of its 32.
@@ -221,7 +236,12 @@ mx4_stream_kernel(moe_host::Mx4Args g) {
         }
       }
     }
-    __syncthreads();   // LDS free for the next item
+    if (next >= total) break;
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // this wave's reads of LDS are done
+    barrier_nofence();                    // LDS free for the next item
+    item = next;
+    ti = next_ti;
+    task = next_task;
   }
 }
 
