@@ -139,7 +139,8 @@ typedef struct {
 
 /* Byte offsets of the parts of a forward workspace (all 256-byte aligned);
  * an offset of (size_t)-1 marks a part these sizes do not use.  Three tilings
- * exist, chosen by a fixed function of the sizes and dtype (`tiling`):
+ * exist, chosen by a fixed function of the sizes and dtype (`tiling`; MXFP4
+ * down rows are fp32 in every one):
  *  0 register streaming (few rows per expert, e.g. decode): the waves of a
  *    workgroup split each reduction and add their sums in LDS; SiLU(gate)*up
  *    is formed in the gate-up GEMM's epilogue and the down rows are bf16;
@@ -173,7 +174,8 @@ typedef struct {
                            fp8 and int8 w8a8 at T = 1 with tiling 0 and an
                            even number of 64-byte steps in an I row, and on
                            MXFP4 at T = 1, where the down launch adds the
-                           token's top-k rows itself */
+                           token's top-k rows itself; MXFP4 otherwise: fp32
+                           [split_k2][P][H] */
     size_t total_bytes; /* minimum size of the workspace */
     int32_t split_k1;   /* slices of the gate-up reduction over H (1 unless tiling 2) */
     int32_t split_k2;   /* slices of the down reduction over I */
@@ -487,9 +489,9 @@ int moe_pack_weights_mxfp4(const uint8_t *codes, const uint8_t *scales, int E, i
  * per token and SiLU(gate)*up per (token, expert) row by the rule of
  * moe_quantize_mxfp4; the products run on the scaled MFMA in its 4-bit mode
  * with fp32 accumulation, SiLU(gate)*up is formed and quantised from the fp32
- * sums, and the per-pair down rows are stored as bf16 (as fp32 sums where
- * moe_workspace_layout names slices of the down reduction; at T = 1 they are
- * added in fp32 and not stored).  A NaN or Inf in a token's row, in a weight or in an
+ * sums, and the per-pair down rows are fp32 (one array for every slice of the
+ * down reduction that moe_workspace_layout names; at T = 1 they are added and
+ * not stored), so that out is rounded to bf16 once, whatever the plan.  A NaN or Inf in a token's row, in a weight or in an
  * intermediate makes the values of its block NaN, and with them the outputs
  * that they enter.  H and I must be multiples of 128.
  * moe_route_forward_mxfp4: both in one call, with the same results; at most

@@ -595,7 +595,7 @@ void workspace_layout(int dtype, int T, int k, int H, int I, const Plan& p,
     W->x_scale_rows = W->g = W->h_scale = kNone;
     W->h = take((size_t)p.max_tasks * p.mb * (I / 128) * moe::kMx4Unit);
     // one token: the down launch adds the top-k rows itself
-    W->y = p.dr_waves ? kNone : (p.split2 == 1 ? take(2 * P * H) : take(4 * (size_t)p.split2 * P * H));
+    W->y = p.dr_waves ? kNone : take(4 * (size_t)p.split2 * P * H);
     W->total_bytes = off;
     W->split_k1 = 1;
     W->split_k2 = p.split2;
@@ -930,7 +930,7 @@ int forward_mx(const void* x, const float* topk_w, const void* routing, const vo
 }
 
 // MXFP4 forward: x to MXFP4, gate-up whose epilogue writes SiLU(gate) * up
-// as MXFP4 blocks, down (bf16 rows, or with one token the weighted sum),
+// as MXFP4 blocks, down (fp32 rows, or with one token the weighted sum),
 // top-k reduction.
 int forward_mx4(const void* x, const float* topk_w, const void* routing, const void* w1, const void* w2, int T, int k,
                 int E, int H, int I, void* workspace, size_t workspace_bytes, void* out, void* stream,
@@ -1004,7 +1004,7 @@ int forward_mx4(const void* x, const float* topk_w, const void* routing, const v
   }
   if (!p.dr_waves) {
     StageScope st(s, 4);
-    if (p.split2 == 1) {   // bf16 rows: the weighted sum of moe_combine
+    if (p.split2 == 1) {   // the weighted sum of moe_combine
       moe_host::RowMoveArgs m{};
       m.rows = ws + W.y;
       m.w = topk_w;
@@ -1015,7 +1015,7 @@ int forward_mx4(const void* x, const float* topk_w, const void* routing, const v
       m.k = k;
       m.E = E;
       m.H = H;
-      e = moe_host::launch_rows_to_tokens(m, MOE_ROW_BF16, s);
+      e = moe_host::launch_rows_to_bf16_tokens(m, s);
     } else {
       e = moe_host::launch_reduce(ws + W.y, false, p.split2, P, topk_w, R.pair_pos, R.expert_offsets, nullptr, E, T, k,
                                   H, static_cast<uint16_t*>(out), s);

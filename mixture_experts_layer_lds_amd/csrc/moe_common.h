@@ -439,14 +439,14 @@ struct Mx4Args {
   const int32_t* header;
   const moe_task_t* tasks;
   void* c;                      // gate-up: SiLU(gate) * up as blocks of 16 rows x G units, mb blocks a task;
-                                // down: bf16 rows [P][N_out]
+                                // down: fp32 rows [split][P][N_out]
   int K;                        // reduction length
   int N_out;                    // output columns (I for gate-up, H for down)
   int w_rows;                   // weight rows per expert (2I or H)
   int topk;
   int max_tasks;
   const float* topk_w;          // one token, down: the routing weights
-  int split;                    // strips, down: K slices; with more than one, c is fp32 [split][P][N_out]
+  int split;                    // strips, down: K slices (else 1)
   int P;                        // sorted rows
 };
 // (mb, waves) = 16-row blocks per tile (1 or 2), waves per workgroup (1, 2, 4, 8)
@@ -470,6 +470,8 @@ struct RowMoveArgs {
 };
 hipError_t launch_rows_to_experts(const RowMoveArgs& a, int row_type, hipStream_t s);
 hipError_t launch_rows_to_tokens(const RowMoveArgs& a, int row_type, hipStream_t s);
+// fp32 rows to bf16 token rows
+hipError_t launch_rows_to_bf16_tokens(const RowMoveArgs& a, hipStream_t s);
 hipError_t launch_rows_grad(const RowMoveArgs& a, bool to_tokens, int row_type, hipStream_t s);
 // The router's gradient (rows.hip).
 hipError_t launch_router_topk_grad(const float* logits, const int32_t* ids, const float* w, const float* dw, int T,

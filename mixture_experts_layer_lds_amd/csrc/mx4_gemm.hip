@@ -15,8 +15,8 @@
 //  * A workgroup of W waves takes one item; wave w reduces every W-th group of
 //    units.  The weights are the first MFMA operand (16 weight rows), the
 //    tokens the second (16 columns), so a lane ends up with eight consecutive
-//    output columns of one token row: its codes are one dword, its bf16 values
-//    one 16-byte store.
+//    output columns of one token row: its codes are one dword, its fp32 sums
+//    two 16-byte stores.
 //  * The group's weights (4 blocks x 1 KiB a unit) and scale codes (one dword
 //    a lane for all its units) go straight to registers, non-temporal, one
 //    group ahead of the one that is multiplied, the next item's first group
@@ -226,14 +226,10 @@ mx4_stream_kernel(moe_host::Mx4Args g) {
           if (lgrp == 0) o.scale[lrow * o.G] = (char)code;
         }
       } else if (rr < task.rows) {
-        uint16_t* y = static_cast<uint16_t*>(g.c) + (size_t)(task.row_begin + rr) * g.N_out + 64 * cg + 8 * lgrp;
+        // fp32: the row is a term of the token's weighted sum, which rounds once
+        float* y = static_cast<float*>(g.c) + (size_t)(task.row_begin + rr) * g.N_out + 64 * cg + 8 * lgrp;
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-          u32x4 v;
-#pragma unroll
-          for (int i = 0; i < 4; i++) v[i] = bf16_pair(tot[2 * h + (i >> 1)][2 * (i & 1)], tot[2 * h + (i >> 1)][2 * (i & 1) + 1]);
-          *reinterpret_cast<u32x4*>(y + 32 * h) = v;
-        }
+        for (int q = 0; q < kMx4NB; q++) *reinterpret_cast<f32x4*>(y + 32 * (q >> 1) + 4 * (q & 1)) = tot[q];
       }
     }
     if (next >= total) break;

@@ -24,7 +24,7 @@
 //  * Gate-up epilogue: 32 columns of h are one MXFP4 block a row, held by two
 //    neighbouring waves; they exchange the rows' largest magnitudes through
 //    LDS and write codes and scale codes in the blocks that the down GEMM
-//    copies as contiguous chunks.  Down writes bf16 rows, 16 bytes a lane.
+//    copies as contiguous chunks.  Down writes fp32 rows, 32 bytes a lane.
 //
 // A wave's copies of a stage come before its weight loads of the same stage,
 // whose number is fixed, so the wait at the head of a stage is an exact count.
@@ -215,7 +215,7 @@ mx4_strip_kernel(moe_host::Mx4Args g) {
   const int num_tasks = min(g.header[kHdrNumTasks], g.max_tasks);
   const int n_strips = GATEUP ? g.N_out / 128 : (g.N_out + 255) / 256;
   // tasks < 65536 / 64 + 512, strips <= 512, slices <= 8: under 2^23
-  const int total = num_tasks * n_strips * g.split; 
+  const int total = num_tasks * n_strips * g.split;
   const int nk = g.K / 128 / U / g.split;             // stages per item
   const int units2 = g.N_out / 128, G2 = units2 % 4 == 0 ? 4 : (units2 % 2 == 0 ? 2 : 1);
 
@@ -430,24 +430,17 @@ mx4_strip_kernel(moe_host::Mx4Args g) {
           o.scale[at + lrow * o.G] = (char)code;   // (the same byte from every lane and wave of the row)
         }
       } else {
-        // rows past the tile are out of the buffer's bounds and dropped
-        const int esz = g.split > 1 ? 4 : 2;
+        // fp32 sums: the row is a term of the token's weighted sum, which rounds
+        // once.  Rows past the tile are out of the buffer's bounds and dropped
         const auto y = __builtin_amdgcn_make_buffer_rsrc(
-            static_cast<char*>(g.c) + ((size_t)cur.at.slice * g.P + cur.at.row_begin) * g.N_out * esz, 0,
-            blk.store ? cur.at.rows * g.N_out * esz : 0, 0x00027000);
+            static_cast<float*>(g.c) + ((size_t)cur.at.slice * g.P + cur.at.row_begin) * g.N_out, 0,
+            blk.store ? cur.at.rows * g.N_out * 4 : 0, 0x00027000);
 #pragma unroll
         for (int m = 0; m < MB; m++) {
           if (16 * m >= cur.at.rows) break;
-          const int at = ((16 * m + lrow) * g.N_out + 16 * blk.out + 8 * lgrp) * esz;
-          if (g.split > 1) {   // fp32 sums of this slice
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[m][0]), y, at, 0, 0);
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[m][1]), y, at + 16, 0, 0);
-          } else {
-            u32x4 v;
-#pragma unroll
-            for (int i = 0; i < 4; i++) v[i] = bf16_pair(acc[m][i >> 1][2 * (i & 1)], acc[m][i >> 1][2 * (i & 1) + 1]);
-            __builtin_amdgcn_raw_buffer_store_b128(v, y, at, 0, 0);
-          }
+          const int at = ((16 * m + lrow) * g.N_out + 16 * blk.out + 8 * lgrp) * 4;
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[m][0]), y, at, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[m][1]), y, at + 16, 0, 0);
         }
       }
       clear();

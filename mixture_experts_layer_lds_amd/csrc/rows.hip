@@ -63,7 +63,8 @@ rows_to_experts_kernel(moe_host::RowMoveArgs g) {
   }
 }
 
-template <typename R, int KM>
+// O: the type of the token rows (the rows' own, or bf16 for fp32 rows).
+template <typename R, typename O, int KM>
 __global__ void __launch_bounds__(kMoveThreads)
 rows_to_tokens_kernel(moe_host::RowMoveArgs g) {
   typedef typename R::elem elem;
@@ -91,7 +92,9 @@ rows_to_tokens_kernel(moe_host::RowMoveArgs g) {
 #pragma unroll
     for (int i = 0; i < N; i++) acc[i] = row[j] < 0 ? acc[i] : acc[i] + w[j] * v[i];
   }
-  row_store<R>(static_cast<elem*>(g.out) + (size_t)t * g.H + c, acc);
+  typename O::elem* out = static_cast<typename O::elem*>(g.out) + (size_t)t * g.H + c;
+  if constexpr (O::kVec == N) row_store<O>(out, acc);
+  else *reinterpret_cast<u32x2*>(out) = u32x2{bf16_pair(acc[0], acc[1]), bf16_pair(acc[2], acc[3])};
 }
 
 // The gradients with the weights': WPT waves a token.  TO_TOKENS (the
@@ -257,15 +260,22 @@ hipError_t launch_rows_to_experts(const RowMoveArgs& a, int row_type, hipStream_
   });
 }
 
-hipError_t launch_rows_to_tokens(const RowMoveArgs& a, int row_type, hipStream_t s) {
-  return moe::with_row_type(row_type, [&](auto r) {
-    const dim3 grid(a.T, (a.H / decltype(r)::kVec + moe::kMoveThreads - 1) / moe::kMoveThreads);
-    return moe::with_pairs(a.k, [&](auto km) {
-      hipLaunchKernelGGL((moe::rows_to_tokens_kernel<decltype(r), decltype(km)::value>), grid,
-                         dim3(moe::kMoveThreads), 0, s, a);
-      return hipGetLastError();
-    });
+// rows of type R, token rows of type O
+template <typename R, typename O>
+static hipError_t launch_rows_to_tokens_t(const RowMoveArgs& a, hipStream_t s) {
+  const dim3 grid(a.T, (a.H / R::kVec + moe::kMoveThreads - 1) / moe::kMoveThreads);
+  return moe::with_pairs(a.k, [&](auto km) {
+    hipLaunchKernelGGL((moe::rows_to_tokens_kernel<R, O, decltype(km)::value>), grid, dim3(moe::kMoveThreads), 0, s, a);
+    return hipGetLastError();
   });
+}
+
+hipError_t launch_rows_to_tokens(const RowMoveArgs& a, int row_type, hipStream_t s) {
+  return moe::with_row_type(row_type, [&](auto r) { return launch_rows_to_tokens_t<decltype(r), decltype(r)>(a, s); });
+}
+
+hipError_t launch_rows_to_bf16_tokens(const RowMoveArgs& a, hipStream_t s) {
+  return launch_rows_to_tokens_t<moe::RowFp32, moe::RowBf16>(a, s);
 }
 
 hipError_t launch_rows_grad(const RowMoveArgs& a, bool to_tokens, int row_type, hipStream_t s) {
