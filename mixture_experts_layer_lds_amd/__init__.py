@@ -35,10 +35,12 @@ plus allocation helpers (alloc_routing, alloc_workspace), pack_weights() for a
 whole weight dict, and a convenience moe_layer() that runs routing + forward
 with freshly allocated buffers.  The forward calls take W1/W2 packed by
 moe_pack_weights (a one-time byte permutation into MFMA-fragment order).
+A size that does not fit the library's C int raises ctypes.ArgumentError.
 """
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 import torch  # loads the HIP runtime that libmoe.so binds to
@@ -129,69 +131,81 @@ EXPORTS = ("moe_status_string", "moe_pack_weights", "moe_describe_packed_weights
            "moe_combine_grad", "moe_router_topk_grad")
 
 
+class _CInt:
+    """A C int argument.  ctypes.c_int would keep the low 32 bits of a larger
+    number, and the library would check and run that size."""
+
+    @staticmethod
+    def from_param(value):
+        value = operator.index(value)
+        if -0x80000000 <= value <= 0x7fffffff:
+            return value
+        raise ValueError(f"{value} does not fit the library's 32-bit sizes")
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run `python mixture_experts_layer_lds_amd/build.py` (or __graft_entry__.build())")
     L = ctypes.CDLL(LIB_PATH)
-    i, P, sz = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
+    i, r, P, sz = _CInt, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
     L.moe_status_string.restype = ctypes.c_char_p
     L.moe_status_string.argtypes = [i]
-    L.moe_pack_weights.restype = i
+    L.moe_pack_weights.restype = r
     L.moe_pack_weights.argtypes = [P, i, i, i, i, P, ctypes.POINTER(PackedWeightsDesc), P]
-    L.moe_describe_packed_weights.restype = i
+    L.moe_describe_packed_weights.restype = r
     L.moe_describe_packed_weights.argtypes = [P, i, i, i, i, ctypes.POINTER(PackedWeightsDesc)]
-    L.moe_routing_layout.restype = i
+    L.moe_routing_layout.restype = r
     L.moe_routing_layout.argtypes = [i, i, i, i, i, i, ctypes.POINTER(RoutingLayout)]
-    L.moe_workspace_layout.restype = i
+    L.moe_workspace_layout.restype = r
     L.moe_workspace_layout.argtypes = [i, i, i, i, i, i, ctypes.POINTER(WorkspaceLayout)]
     for n in ("moe_build_routing_bf16", "moe_build_routing_fp8"):
         f = getattr(L, n)
-        f.restype = i
+        f.restype = r
         f.argtypes = [P, i, i, i, i, i, P, sz, P]
-    L.moe_router_topk.restype = i
-    L.moe_router_pair_bytes.restype = i
+    L.moe_router_topk.restype = r
+    L.moe_router_pair_bytes.restype = r
     L.moe_router_pair_bytes.argtypes = [i, i, ctypes.POINTER(ctypes.c_size_t)]
-    L.moe_router_split_weights.restype = i
+    L.moe_router_split_weights.restype = r
     L.moe_router_split_weights.argtypes = [P, i, i, P, sz, P]
-    L.moe_router_workspace_bytes.restype = i
+    L.moe_router_workspace_bytes.restype = r
     L.moe_router_workspace_bytes.argtypes = [i, i, i, ctypes.POINTER(ctypes.c_size_t)]
-    L.moe_router_gemm.restype = i
+    L.moe_router_gemm.restype = r
     L.moe_router_gemm.argtypes = [P, P, i, i, i, P, sz, P, P]
-    L.moe_router_gemm_topk.restype = i
+    L.moe_router_gemm_topk.restype = r
     L.moe_router_gemm_topk.argtypes = [P, P, i, i, i, i, i, i, P, sz, P, P, P, P]
     L.moe_router_topk.argtypes = [P, i, i, i, i, i, P, P, P]
-    L.moe_forward_bf16.restype = i
+    L.moe_forward_bf16.restype = r
     D = ctypes.POINTER(PackedWeightsDesc)
     L.moe_forward_bf16.argtypes = [P, P, P, D, D, i, i, i, i, i, P, sz, P, P]
-    L.moe_forward_fp8.restype = i
+    L.moe_forward_fp8.restype = r
     L.moe_forward_fp8.argtypes = [P, P, P, D, P, D, P, i, i, i, i, i, P, sz, P, P]
-    L.moe_forward_mxfp8.restype = i
+    L.moe_forward_mxfp8.restype = r
     L.moe_forward_mxfp8.argtypes = [P, P, P, D, P, D, P, i, i, i, i, i, P, sz, P, P]
-    L.moe_forward_fp8_block.restype = i
+    L.moe_forward_fp8_block.restype = r
     L.moe_forward_fp8_block.argtypes = [P, P, P, D, P, D, P, i, i, i, i, i, P, sz, P, P]
-    L.moe_forward_int4.restype = i
+    L.moe_forward_int4.restype = r
     L.moe_forward_int4.argtypes = [P, P, P, D, P, D, P, i, i, i, i, i, P, sz, P, P]
-    L.moe_forward_int8.restype = i
+    L.moe_forward_int8.restype = r
     L.moe_forward_int8.argtypes = [P, P, P, D, P, D, P, i, i, i, i, i, P, sz, P, P]
-    L.moe_forward_int8_w8a16.restype = i
+    L.moe_forward_int8_w8a16.restype = r
     L.moe_forward_int8_w8a16.argtypes = [P, P, P, D, P, D, P, i, i, i, i, i, P, sz, P, P]
-    L.moe_set_stage_events.restype = i
+    L.moe_set_stage_events.restype = r
     L.moe_set_stage_events.argtypes = [ctypes.POINTER(P), i]
-    L.moe_device_cu_count.restype = i
+    L.moe_device_cu_count.restype = r
     L.moe_device_cu_count.argtypes = []
-    L.moe_forward_fp8_noalloc.restype = i
+    L.moe_forward_fp8_noalloc.restype = r
     L.moe_forward_fp8_noalloc.argtypes = [P, P, P, D, P, D, P, i, i, i, i, i, P, P]
-    L.moe_stream_read.restype = i
+    L.moe_stream_read.restype = r
     L.moe_stream_read.argtypes = [P, sz, P, sz, P]
-    L.moe_tile_copy_read.restype = i
+    L.moe_tile_copy_read.restype = r
     L.moe_tile_copy_read.argtypes = [i, P, sz, i, i, P, sz, P]
-    L.moe_route_forward_bf16.restype = i
+    L.moe_route_forward_bf16.restype = r
     L.moe_route_forward_bf16.argtypes = [P, P, P, P, sz, D, D, i, i, i, i, i, P, sz, P, P]
-    L.moe_route_forward_fp8.restype = i
+    L.moe_route_forward_fp8.restype = r
     L.moe_route_forward_fp8.argtypes = [P, P, P, P, sz, D, P, D, P, i, i, i, i, i, P, sz, P, P]
     for f in (L.moe_route_forward_int8, L.moe_route_forward_fp8_block, L.moe_route_forward_mxfp8,
               L.moe_route_forward_int4, L.moe_route_forward_int8_w8a16):
-        f.restype = i
+        f.restype = r
         f.argtypes = [P, P, P, P, sz, D, P, D, P, i, i, i, i, i, P, sz, P, P]
     i64 = ctypes.c_int64
     for n, args in (("moe_quantize_mxfp4", [P, i, i64, i, i64, P, P, P]),
@@ -206,7 +220,7 @@ def _load():
                     ("moe_combine_grad", [P, P, i, P, P, sz, i, i, i, i, P, P, P]),
                     ("moe_router_topk_grad", [P, P, P, P, i, i, i, i, i, P, P])):
         f = getattr(L, n)
-        f.restype = i
+        f.restype = r
         f.argtypes = args
     return L
 

@@ -2,6 +2,7 @@
 nothing is launched)."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
@@ -175,3 +176,46 @@ def test_binding_refuses_wrong_tensors(m):
         m.moe_router_topk_grad(torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2), torch.zeros(4, 3))
     with pytest.raises(ValueError, match="packed MXFP4"):
         m.moe_describe_packed_weights(torch.zeros(1, 32, 64, dtype=torch.uint8), "mxfp4")
+
+
+def test_sizes_past_32_bits_are_refused(m, monkeypatch):
+    """Sizes whose low 32 bits are good ones: none may reach the library as those."""
+    lib, over = m._lib, 1 << 32
+    n = m.moe_routing_layout(4, 2, 8, 128, 128, "bf16")["total_bytes"]
+    # of sizes that would return MOE_OK without a launch, or describe nothing
+    for f, args in ((lib.moe_quantize_mxfp4, (FAKE, 0, 0, over + 64, over + 64, FAKE, FAKE, NULL)),
+                    (lib.moe_dequantize_mxfp4, (FAKE, FAKE, 0, over + 64, 0, FAKE, NULL)),
+                    (lib.moe_dispatch, (FAKE, 0, NULL, FAKE, n, over, 2, 8, 64, FAKE, NULL)),
+                    (lib.moe_combine, (FAKE, 0, NULL, FAKE, n, 0, over + 2, 8, 64, FAKE, NULL)),
+                    (lib.moe_dispatch_grad, (FAKE, NULL, 0, NULL, FAKE, n, 0, 2, over + 8, 64, FAKE, NULL, NULL)),
+                    (lib.moe_combine_grad, (FAKE, NULL, 0, NULL, FAKE, n, 0, 2, 8, over + 64, FAKE, NULL, NULL)),
+                    (lib.moe_router_topk_grad, (FAKE, FAKE, FAKE, FAKE, over, 8, 2, 1, 0, FAKE, NULL)),
+                    (lib.moe_router_topk, (FAKE, over, 8, 2, 1, 0, FAKE, FAKE, NULL)),
+                    (lib.moe_build_routing_mxfp4, (FAKE, over, 2, 8, 128, 128, FAKE, n, NULL)),
+                    (lib.moe_build_routing_bf16, (FAKE, -over, 2, 8, 128, 128, FAKE, n, NULL)),
+                    (lib.moe_forward_bf16, (FAKE, FAKE, FAKE, NULL, NULL, over, 2, 8, 128, 128, FAKE, n, FAKE, NULL))):
+        with pytest.raises(ctypes.ArgumentError, match="32-bit"):
+            f(*args)
+    for f, args in ((m.moe_routing_layout, (over + 4, 2, 8, 128, 128)), (m.moe_workspace_layout, (4, 2, 8, over + 128, 128, "mxfp4")),
+                    (m.alloc_routing, (4, 2, over + 8, 128, 128)), (m.moe_router_pair_bytes, (over + 8, 64))):
+        with pytest.raises(ctypes.ArgumentError, match="32-bit"):
+            f(*args)
+    # through the binding, on tensors without memory
+    monkeypatch.setattr(m, "_check_device", lambda *t: 0)
+    monkeypatch.setattr(m, "_here", lambda dev, stream: None)
+    r = torch.zeros(n, dtype=torch.uint8)
+    rows = torch.empty(1, over + 64, dtype=torch.bfloat16, device="meta")
+    tall = torch.empty(over + 4, 64, dtype=torch.bfloat16, device="meta")
+    codes = torch.empty(1, over + 64, dtype=torch.uint8, device="meta")
+    scores = torch.empty(over + 5, 1, device="meta")
+    for f, args in ((m.moe_quantize_mxfp4, (rows,)),
+                    (m.moe_dequantize_mxfp4, (codes, torch.empty(1, (over + 64) // 16, dtype=torch.uint8, device="meta"))),
+                    (m.moe_dispatch, (tall, r, 1, 8)), (m.moe_combine, (tall, r, 1, 8)),
+                    (m.moe_dispatch_grad, (tall, r, 1, 8)), (m.moe_combine_grad, (tall, r, 1, 8)),
+                    (m.moe_router_topk_grad, (scores, torch.empty(over + 5, 1, dtype=torch.int32, device="meta"), scores, scores))):
+        with pytest.raises(ctypes.ArgumentError, match="32-bit"):
+            f(*args)
+    # every size that fits still reaches the library's own checks, numpy's integers too
+    assert lib.moe_router_topk_grad(FAKE, FAKE, FAKE, FAKE, (1 << 31) - 1, 8, 2, 1, 0, FAKE, NULL) == -2
+    assert lib.moe_router_topk_grad(FAKE, FAKE, FAKE, FAKE, -(1 << 31), 8, 2, 1, 0, FAKE, NULL) == -1
+    assert m.moe_routing_layout(np.int64(4), np.int32(2), 8, 128, 128) == m.moe_routing_layout(4, 2, 8, 128, 128)
