@@ -419,15 +419,17 @@ mx4_strip_kernel(moe_host::Mx4Args g) {
         const Mx4Out o = mx4_out(g.c, (size_t)cur.at.ti * MB, blk.out / 2, units2, G2);
         // whole blocks, also of rows past the tile's last one: their places are
         // this task's and never read
+        int row = lrow;   // (opaque: the places below formed here, not kept in registers through the stages)
+        __asm__ volatile("" : "+v"(row));
 #pragma unroll
         for (int m = 0; m < MB; m++) {
           if (16 * m >= cur.at.rows) break;
           const uint32_t mx = max(amax[(wave * MB + m) * 16 + lrow], amax[((wave ^ 1) * MB + m) * 16 + lrow]);
           const uint32_t code = mx4_scale_code(mx);
           const uint32_t at = m * (uint32_t)units2 * kMx4Unit;
-          *reinterpret_cast<uint16_t*>(o.codes + at + 16 * lrow + 4 * lgrp + 2 * (wave & 1)) =
+          *reinterpret_cast<uint16_t*>(o.codes + at + 16 * row + 4 * lgrp + 2 * (wave & 1)) =
               (uint16_t)mx4_encode4(acc[m][0], code);
-          o.scale[at + lrow * o.G] = (char)code;   // (the same byte from every lane and wave of the row)
+          o.scale[at + row * o.G] = (char)code;   // (the same byte from every lane and wave of the row)
         }
       } else {
         // fp32 sums: the row is a term of the token's weighted sum, which rounds
