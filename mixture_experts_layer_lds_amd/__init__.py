@@ -845,6 +845,7 @@ def moe_pack_weights_mxfp4(codes, scales, out=None, stream=None):
 
 
 def moe_build_routing_mxfp4(topk_ids, E, H, I, routing, stream=None):
+    _check_device(topk_ids, routing)
     _build_routing(_lib.moe_build_routing_mxfp4, "moe_build_routing_mxfp4", topk_ids, E, H, I, routing, stream)
 
 

@@ -219,3 +219,13 @@ def test_sizes_past_32_bits_are_refused(m, monkeypatch):
     assert lib.moe_router_topk_grad(FAKE, FAKE, FAKE, FAKE, (1 << 31) - 1, 8, 2, 1, 0, FAKE, NULL) == -2
     assert lib.moe_router_topk_grad(FAKE, FAKE, FAKE, FAKE, -(1 << 31), 8, 2, 1, 0, FAKE, NULL) == -1
     assert m.moe_routing_layout(np.int64(4), np.int32(2), 8, 128, 128) == m.moe_routing_layout(4, 2, 8, 128, 128)
+
+
+def test_mxfp4_routing_refuses_host_tensors(m):
+    # host ids would be read, and a host routing buffer written, by the kernel
+    ids, r = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4096, dtype=torch.uint8)
+    w = m.moe_describe_packed_weights(torch.zeros(8, 256, 68, dtype=torch.uint8), "mxfp4")
+    for call in (lambda: m.moe_build_routing_mxfp4(ids, 8, 128, 128, r), lambda: m.build_routing(ids, 8, 128, 128, r, "mxfp4"),
+                 lambda: m.moe_layer(torch.zeros(4, 128, dtype=torch.bfloat16), ids, torch.zeros(4, 2), {"w1": w, "w2": w}, "mxfp4")):
+        with pytest.raises(ValueError, match="current GPU"):
+            call()
