@@ -752,8 +752,12 @@ def _check_device(*tensors):
 
 
 def _here(dev, stream):
-    """The hipStream_t of `stream`, or of device dev's current stream."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    """The hipStream_t of `stream`, which has to be device dev's, or of its current stream."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"stream: expected one of GPU {dev}, got one of GPU {stream.device_index}")
+    return stream.cuda_stream
 
 
 def _is(name, t, dtype, shape):
@@ -837,15 +841,15 @@ def moe_pack_weights_mxfp4(codes, scales, out=None, stream=None):
     if out is None:
         out = _empty(codes, (E, rows, cols // 2 + cols // 32), torch.uint8, stream)
     _check_tensor("out", out, torch.uint8, (E, rows, cols // 2 + cols // 32))
-    _check_device(codes, scales, out)
+    dev = _check_device(codes, scales, out)
     desc = PackedWeightsDesc()
     _check("moe_pack_weights_mxfp4", _lib.moe_pack_weights_mxfp4(
-        _ptr(codes), _ptr(scales), E, rows, cols, _ptr(out), ctypes.byref(desc), _stream(stream)))
+        _ptr(codes), _ptr(scales), E, rows, cols, _ptr(out), ctypes.byref(desc), _here(dev, stream)))
     return PackedWeight(out, desc)
 
 
 def moe_build_routing_mxfp4(topk_ids, E, H, I, routing, stream=None):
-    _check_device(topk_ids, routing)
+    _here(_check_device(topk_ids, routing), stream)
     _build_routing(_lib.moe_build_routing_mxfp4, "moe_build_routing_mxfp4", topk_ids, E, H, I, routing, stream)
 
 

@@ -1,6 +1,7 @@
 """Host-side refusals of the MXFP4 and expert-order row entry points (no GPU,
 nothing is launched)."""
 import ctypes
+import types
 
 import numpy as np
 import pytest
@@ -229,3 +230,23 @@ def test_mxfp4_routing_refuses_host_tensors(m):
                  lambda: m.moe_layer(torch.zeros(4, 128, dtype=torch.bfloat16), ids, torch.zeros(4, 2), {"w1": w, "w2": w}, "mxfp4")):
         with pytest.raises(ValueError, match="current GPU"):
             call()
+
+
+def test_streams_of_another_gpu_are_refused(m, monkeypatch):
+    # a launch goes to the current device, where the tensors are
+    monkeypatch.setattr(m, "_check_device", lambda *t: 0)
+    here, there = types.SimpleNamespace(device_index=0, cuda_stream=4096), types.SimpleNamespace(device_index=1, cuda_stream=4096)
+    assert m._here(0, here) == 4096
+    r = torch.zeros(4096, dtype=torch.uint8)
+    x, y, w = torch.zeros(4, 64), torch.zeros(8, 64), torch.zeros(4, 2)
+    ids, codes = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(1, 32, 64, dtype=torch.uint8)
+    scales = torch.zeros(1, 32, 4, dtype=torch.uint8)
+    for f, args in ((m.moe_quantize_mxfp4, (x, torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(4, 2, dtype=torch.uint8))),
+                    (m.moe_dequantize_mxfp4, (codes, scales, None, torch.zeros(1, 32, 128))),
+                    (m.moe_pack_weights_mxfp4, (codes, scales, torch.zeros(1, 32, 68, dtype=torch.uint8))),
+                    (m.moe_build_routing_mxfp4, (ids, 8, 128, 128, r)),
+                    (m.moe_dispatch, (x, r, 2, 8, None, y)), (m.moe_combine, (y, r, 2, 8, None, x)),
+                    (m.moe_dispatch_grad, (y, r, 2, 8, None, None, x)), (m.moe_combine_grad, (x, r, 2, 8, None, None, y)),
+                    (m.moe_router_topk_grad, (torch.zeros(4, 8), ids, w, w, True, 0, torch.zeros(4, 8)))):
+        with pytest.raises(ValueError, match="stream"):
+            f(*args, stream=there)
