@@ -751,6 +751,13 @@ def _check_device(*tensors):
     return dev
 
 
+def _bytes(name, t):
+    """Bytes of a routing buffer or workspace, which the library takes as one run."""
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous buffer, got strides {t.stride()}")
+    return t.nbytes
+
+
 def _here(dev, stream):
     """The hipStream_t of `stream`, which has to be device dev's, or of its current stream."""
     if stream is None:
@@ -850,6 +857,7 @@ def moe_pack_weights_mxfp4(codes, scales, out=None, stream=None):
 
 def moe_build_routing_mxfp4(topk_ids, E, H, I, routing, stream=None):
     _here(_check_device(topk_ids, routing), stream)
+    _bytes("routing", routing)
     _build_routing(_lib.moe_build_routing_mxfp4, "moe_build_routing_mxfp4", topk_ids, E, H, I, routing, stream)
 
 
@@ -874,7 +882,7 @@ def moe_forward_mxfp4(x, topk_w, routing, w1, w2, workspace, out, stream=None):
     sizes, desc, dev = _mxfp4_sizes(x, topk_w, w1, w2, routing, workspace, out)
     _check("moe_forward_mxfp4", _lib.moe_forward_mxfp4(
         x.data_ptr(), topk_w.data_ptr(), routing.data_ptr(), *desc, *sizes, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), out.data_ptr(), _here(dev, stream)))
+        _bytes("workspace", workspace), out.data_ptr(), _here(dev, stream)))
     return out
 
 
@@ -884,8 +892,8 @@ def moe_route_forward_mxfp4(topk_ids, x, topk_w, routing, w1, w2, workspace, out
     _is("topk_ids", topk_ids, torch.int32, sizes[:2])
     _check("moe_route_forward_mxfp4", _lib.moe_route_forward_mxfp4(
         topk_ids.data_ptr(), x.data_ptr(), topk_w.data_ptr(), routing.data_ptr(),
-        routing.numel() * routing.element_size(), *desc, *sizes, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), out.data_ptr(), _here(dev, stream)))
+        _bytes("routing", routing), *desc, *sizes, workspace.data_ptr(), _bytes("workspace", workspace),
+        out.data_ptr(), _here(dev, stream)))
     return out
 
 
@@ -904,7 +912,7 @@ def _move(name, fn, src, src_name, sorted_src, routing, k, E, topk_w, out, out_n
         _is("topk_w", topk_w, torch.float32, (T, k))
     dev = _check_device(src, out, topk_w, routing)
     out = _output(out_name, out, src, (T, H) if sorted_src else (T * k, H), src.dtype, stream)
-    _check(name, fn(src.data_ptr(), kind, _at(topk_w), routing.data_ptr(), routing.numel() * routing.element_size(),
+    _check(name, fn(src.data_ptr(), kind, _at(topk_w), routing.data_ptr(), _bytes("routing", routing),
                     T, k, E, H, out.data_ptr(), _here(dev, stream)))
     return out
 
@@ -940,7 +948,7 @@ def _move_grad(name, fn, grad, grad_name, sorted_grad, other, other_name, routin
     if other is not None:
         dw = _output("dtopk_w", dw, grad, (T, k), torch.float32, stream)
     _check(name, fn(grad.data_ptr(), _at(other), kind, _at(topk_w), routing.data_ptr(),
-                    routing.numel() * routing.element_size(), T, k, E, H, out.data_ptr(), _at(dw), _here(dev, stream)))
+                    _bytes("routing", routing), T, k, E, H, out.data_ptr(), _at(dw), _here(dev, stream)))
     return out if dw is None else (out, dw)
 
 

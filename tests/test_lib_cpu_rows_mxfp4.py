@@ -250,3 +250,22 @@ def test_streams_of_another_gpu_are_refused(m, monkeypatch):
                     (m.moe_router_topk_grad, (torch.zeros(4, 8), ids, w, w, True, 0, torch.zeros(4, 8)))):
         with pytest.raises(ValueError, match="stream"):
             f(*args, stream=there)
+
+
+def test_buffers_that_are_no_run_of_bytes_are_refused(m, monkeypatch):
+    # an expanded tensor counts bytes that it does not have
+    monkeypatch.setattr(m, "_check_device", lambda *t: 0)
+    monkeypatch.setattr(m, "_here", lambda dev, stream: None)
+    E, H, I, T, k = 8, 128, 128, 4, 2
+    r, bad = torch.zeros(4096, dtype=torch.uint8), torch.zeros(1, dtype=torch.uint8).expand(1 << 20)
+    x, out, ids, w = torch.zeros(T, H, dtype=torch.bfloat16), torch.zeros(T, H, dtype=torch.bfloat16), torch.zeros(T, k, dtype=torch.int32), torch.zeros(T, k)
+    y = torch.zeros(T * k, H, dtype=torch.bfloat16)
+    w1 = m.moe_describe_packed_weights(torch.zeros(E, 2 * I, 68, dtype=torch.uint8), "mxfp4")
+    w2 = m.moe_describe_packed_weights(torch.zeros(E, H, 68, dtype=torch.uint8), "mxfp4")
+    for f, args, name in ((m.moe_build_routing_mxfp4, (ids, E, H, I, bad), "routing"), (m.moe_dispatch, (x, bad, k, E), "routing"),
+                          (m.moe_combine, (y, r.repeat(2)[::2], k, E), "routing"), (m.moe_dispatch_grad, (y, bad, k, E), "routing"),
+                          (m.moe_combine_grad, (x, bad, k, E), "routing"), (m.moe_forward_mxfp4, (x, w, r, w1, w2, bad, out), "workspace"),
+                          (m.moe_route_forward_mxfp4, (ids, x, w, bad, w1, w2, r, out), "routing"),
+                          (m.moe_route_forward_mxfp4, (ids, x, w, r, w1, w2, bad, out), "workspace")):
+        with pytest.raises(ValueError, match=name + ": expected a contiguous buffer"):
+            f(*args)
