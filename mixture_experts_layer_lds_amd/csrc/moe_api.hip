@@ -1703,8 +1703,9 @@ int forward(int dtype, const void* x, const float* topk_w, const void* routing, 
 // Routing build and forward pass in one call.  A decode batch of at most 64
 // pairs on the register-streaming plan is routed inside the forward's first
 // kernel (the x quantisation on the dtypes with quantised activations, the
-// gate-up GEMM on bf16); otherwise the routing build runs as its own launch
-// first.  Every dtype of the forward calls.
+// gate-up GEMM on bf16), an MXFP4 batch of at most mx4_route_pairs() pairs on
+// any plan in the launch of its x quantisation; otherwise the routing build
+// runs as its own launch first.  Every dtype of the forward calls.
 int route_forward(int dtype, const int32_t* ids, const void* x, const float* topk_w, void* routing,
                   size_t routing_bytes, const void* w1, const void* w1_scale, const void* w2,
                   const void* w2_scale, int T, int k, int E, int H, int I, void* workspace,

@@ -179,8 +179,8 @@ mx4_pack_kernel(const u32x4* __restrict__ codes, const uint8_t* __restrict__ sca
 
 namespace moe_host {
 
-// Workgroups of a grid-stride pass over n items: eight per compute unit of
-// the largest part (256), fewer when there is less to do.
+// Workgroups of a grid-stride pass over n items: at most sixteen per compute
+// unit (of 256), fewer when there is less to do.
 static unsigned pass_grid(size_t n) {
   const size_t b = (n + 255) / 256;
   return (unsigned)(b < 4096 ? b : 4096);

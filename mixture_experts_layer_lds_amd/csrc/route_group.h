@@ -16,7 +16,7 @@ static_assert(kOneGroupPairs <= kRouteWaves * kWave * kBatch,
               "the one-workgroup build holds each wave's segment in one batch of registers");
 
 // Largest of in[0..n) (n >= 0; 0 when empty) by one wave, returned to every lane.
-__device__ int wave_max_tiles(const int* in, int n, int lane) {
+static __device__ int wave_max_tiles(const int* in, int n, int lane) {
   int m = 0;
   for (int i = lane; i < n; i += kWave) m = max(m, in[i]);
 #pragma unroll
@@ -26,7 +26,7 @@ __device__ int wave_max_tiles(const int* in, int n, int lane) {
 
 // Exclusive prefix sum of in[0..n) into out[0..n) by one wave (n <= 64*64);
 // in and out may alias.  Returns the total to every lane.
-__device__ int wave_exclusive_scan(const int* in, int* out, int n, int lane) {
+static __device__ int wave_exclusive_scan(const int* in, int* out, int n, int lane) {
   const int per = (n + kWave - 1) / kWave;
   const int b = lane * per;
   const int e = min(b + per, n);

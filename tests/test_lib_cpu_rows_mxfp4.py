@@ -1,6 +1,7 @@
 """Host-side refusals of the MXFP4 and expert-order row entry points (no GPU,
 nothing is launched)."""
 import ctypes
+import pathlib
 import types
 
 import numpy as np
@@ -269,3 +270,12 @@ def test_buffers_that_are_no_run_of_bytes_are_refused(m, monkeypatch):
                           (m.moe_route_forward_mxfp4, (ids, x, w, r, w1, w2, bad, out), "workspace")):
         with pytest.raises(ValueError, match=name + ": expected a contiguous buffer"):
             f(*args)
+
+
+def test_headers_define_no_external_device_function(m):
+    # a header in two sources would define it twice under relocatable device code
+    for path in pathlib.Path(m.LIB_PATH).parent.glob("csrc/*.h"):
+        lines = path.read_text().splitlines()
+        for i, line in enumerate(lines):
+            if line.startswith("__device__") and not lines[i - 1].startswith("template"):
+                assert "__forceinline__" in line or "inline" in line, f"{path.name}: {line}"
