@@ -137,7 +137,8 @@ class _CInt:
 
     @staticmethod
     def from_param(value):
-        value = operator.index(value)
+        if value.__class__ is not int:
+            value = operator.index(value)
         if -0x80000000 <= value <= 0x7fffffff:
             return value
         raise ValueError(f"{value} does not fit the library's 32-bit sizes")
