@@ -224,6 +224,12 @@ int pick_mx4_waves(int groups, long items) {
 // 989, Qwen3-30B-A3B-shaped T = 256 73 / 60 (768 and 1024 items);
 // Mixtral-8x7B-shaped T = 64 140 / 148 (896 and 128), Qwen2-57B-shaped slice
 // T = 100 68 / 78 (320 and 896).
+// Tile heights by the mean rows (64, 96, 128, 160 and 192 rows up to 40, 72, 96
+// and 128 and above).  Graph replay, us, the lower against the upper height at
+// the border: at 40 DeepSeek-V3-shaped 1105 / 1107, Qwen2-57B-shaped slice 96.5 /
+// 97.7, Mixtral-8x7B-shaped 156 / 155; at 72 1236 / 1232, 118.9 / 116.9, 167 / 166;
+// at 96 (the latter two) 130 / 132, 176 / 181; at 128 1600 / 1563, 143 / 150,
+// 197 / 196.
 void plan_mx4(int T, int k, int E, int H, int I, Plan* p) {
   const long P = (long)T * k, active = std::min(P, (long)E);
   const long avg = active > 0 ? (P + active - 1) / active : 1;

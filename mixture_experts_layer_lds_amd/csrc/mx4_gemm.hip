@@ -26,9 +26,9 @@
 //  * The waves' sums meet in LDS and are added in ascending wave order.
 //
 // Measured, gate-up / down in us (TB/s of weights with their scale codes):
-// DeepSeek-V3-shaped T = 16 249 (6.6) / 124 (6.6), T = 64 517 (6.7) / 266
-// (6.5); Mixtral-8x7B-shaped T = 16 78 (6.4) / 41 (6.0); Qwen3-30B-A3B-shaped
-// T = 64 19.5 (4.3) / 12 (3.4), too short to reach the full rate.  One token,
+// DeepSeek-V3-shaped T = 16 251 (6.5) / 125 (6.5), T = 64 517 (6.7) / 276
+// (6.3); Mixtral-8x7B-shaped T = 16 79 (6.3) / 42 (6.0); Qwen3-30B-A3B-shaped
+// T = 64 19.7 (4.2) / 13.2 (3.2), too short to reach the full rate.  One token,
 // DeepSeek-V3-shaped: 20.5 (6.1) and, with the top-k sum, 14.3 (4.4).
 #include "decode_route.h"
 #include "lds_dma.h"

@@ -29,17 +29,26 @@
 // A wave's copies of a stage come before its weight loads of the same stage,
 // whose number is fixed, so the wait at the head of a stage is an exact count.
 //
-// Measured (us, TB/s of weights with their scale codes): DeepSeek-V3-shaped
-// gate-up / down at T = 1024 622 (6.4) / 372 (5.4), at 4096 827 (4.8) / 485
-// (4.1); Mixtral-8x7B-shaped T = 2048 293 / 166, 3.3 and 2.9 PFLOP/s.  Few
-// rows an expert run at the rate of the weight stream.  At T = 4096 the
-// gate-up takes 745 us without its token copies, 800 without its
-// multiplications and 560 without its weight loads: per CU a stage moves 70
-// KiB of weights and 17 to 52 KiB of token rows, about 30 GB/s in all at every
-// tile height, with the L1 stalled on pending data for 57% of the time: what
-// bounds it is the CU's path to memory, which the token rows share with the
-// weights.  (Four waves of twice the weight rows, half the LDS reads, ran in
-// the same time.)
+// Measured (us by events, passes in a row; TB/s of weights with their scale
+// codes): DeepSeek-V3-shaped gate-up / down at T = 1024 610 (6.6) / 386 (5.2),
+// at 4096 829 (4.8) / 577 (3.5; with the fp32 rows 5.1, the rate of a large
+// copy); Mixtral-8x7B-shaped T = 2048 312 / 173, 3.1 and 2.8 PFLOP/s (303 to 317
+// and 170 to 175 from session to session).  Few rows an expert run at the rate
+// of the weight stream.  At many, no one part bounds the gate-up.  Copies of the
+// kernel with parts left out took, in one session:
+//                          DeepSeek-V3 T = 4096    Mixtral-8x7B T = 2048
+//   whole                          829                     312
+//   no multiplications             767                     237
+//   no token copies                750                     233
+//   no weight loads                496                     254
+//   no epilogue                    766                     260
+//   neither load                   428                     220
+//   loads, products left out       246                     141
+//   all four left out              171                      79
+// The first is nearest to its weights (4.0 GB, 568 us at the rate of a large
+// read), which the token copies share the CU's queue with; the second takes
+// 220 of 312 without a load, 116 of them the MFMA's own time.  (Four waves of
+// twice the weight rows, half the LDS reads, ran in the same time.)
 #include "lds_dma.h"
 #include "mx4_epilogue.h"
 

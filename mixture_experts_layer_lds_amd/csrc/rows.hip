@@ -237,6 +237,9 @@ router_topk_grad_kernel(const float* __restrict__ logits, const int32_t* __restr
   }
 }
 
+// f(KM) for the next instance of k pairs.  The places past k load row 0 and drop
+// it: to tokens, T = 4096, 7168 bf16 values, k = 6 and 10 reach 4.9 TB/s where 8
+// and 16 reach 5.2 and 5.4 (half of eight pairs dropped: 4.5).
 template <typename F>
 static hipError_t with_pairs(int k, F&& f) {
   if (k <= 2) return f(std::integral_constant<int, 2>{});
@@ -283,8 +286,11 @@ hipError_t launch_rows_grad(const RowMoveArgs& a, bool to_tokens, int row_type, 
     return moe::with_pairs(a.k, [&](auto km) {
       using R = decltype(r);
       constexpr int KM = decltype(km)::value;
-      // waves a token by its 1 KiB runs: one, two or four up to as many, four
-      // for longer rows, and sixteen where few tokens leave compute units idle
+      // waves a token by its 1 KiB runs: one or two for as many (of combine,
+      // 8192 tokens of 512 bf16 values, top-8, on one, two and four waves 32, 35
+      // and 48 us), four for longer rows, and sixteen for up to 512 tokens, where
+      // four leave compute units idle (7168 values, four against sixteen waves:
+      // T = 256 21.1 / 17.5, 512 30.0 / 28.7, 768 40.8 / 44.2, 4096 196 / 202)
       const int runs = (a.H / R::kVec + 63) / 64;
       auto launch = [&](auto wpt) {
         constexpr int W = decltype(wpt)::value, tpb = W < 4 ? 4 / W : 1;
