@@ -127,3 +127,52 @@ def test_silu_over_the_range_of_gates(lib, T, bm):   # noqa: F811
     bad = got != want
     assert not bad.any(), f"{int(bad[0].sum())} of {n} codes, gates {gate[bad[0]][:8].tolist()}"
     assert torch.equal(hc, hc[:1].expand_as(hc))
+
+
+@pytest.mark.parametrize("T", [1, 12, 50])
+def test_silu_of_extreme_gates(lib, T):   # noqa: F811
+    """Gates whose e^-g fp32 does not hold, or whose exponent's product with log2(e)
+    it does not: SiLU is the gate itself or 0 there, never NaN."""
+    E, H, I, k = 1, 128, 128, 1
+    # (gate code, its exponent, up's exponent, SiLU(gate) * up)
+    cases = [(3, 126, -126, 1.5), (11, 126, -126, 0.0), (2, 127, -127, 1.0), (10, 127, 126, 0.0), (3, 7, -7, 1.5), (11, 7, 60, 0.0),
+             (2, 10, -9, 2.0), (10, 10, 100, 0.0), (0, 0, 100, 0.0), (2, -126, 126, 0.5), (3, 40, -39, 3.0), (2, 3, 0, 8 / (1 + math.exp(-8.0)))]
+    c1 = torch.zeros(E, 2 * I, H, dtype=torch.uint8)
+    s1 = torch.full((E, 2 * I, H // 32), 127, dtype=torch.uint8)
+    want = torch.zeros(I, dtype=torch.float64)
+    for i, (gc, ge, ue, h) in enumerate(cases):
+        c1[0, i, 0], s1[0, i, 0] = gc, ge + 127
+        c1[0, I + i, 0], s1[0, I + i, 0] = 2, ue + 127
+        want[i] = h
+    c1 = c1[..., 0::2] | (c1[..., 1::2] << 4)
+    c2, s2 = torch.zeros(E, H, I // 2, dtype=torch.uint8), torch.full((E, H, I // 32), 127, dtype=torch.uint8)
+    x = torch.zeros(T, H)
+    x[:, 0] = 1
+    _, _, _, _, _, _, routing, ws = run_layer(lib, T, k, E, H, I, T, ids=torch.zeros(T, k, dtype=torch.int32), x=x, W=((c1, s1), (c2, s2)))
+    hc, hs, _ = ref.read_h(lib, ws, routing, T, k, E, H, I)
+    assert (hs[:, 0] == 127).all()       # the largest is 7.997
+    got = torch.stack((hc & 15, hc >> 4), -1).flatten(1).long() & 7
+    assert torch.equal(got, ref.round_codes(want).expand_as(got))
+
+
+def test_down_rows_past_32_bit_offsets(lib):   # noqa: F811
+    # 65536 down rows of 16640 fp32 values: 4.4 GB of them
+    T, k, E, H, I = 8192, 8, 8, 16640, 128
+    x, ids, w, W, _, out, routing, ws = run_layer(lib, T, k, E, H, I, 5, p_drop=0.01)
+    W_ = lib.moe_workspace_layout(T, k, E, H, I, "mxfp4")
+    assert W_["y"] + 4 * T * k * H <= W_["total_bytes"] and 4 * T * k * H > 1 << 32
+    hc, hs, _ = ref.read_h(lib, ws[:W_["y"]], routing, T, k, E, H, I)
+    pos, _, off = ref.sorted_order(ids, E)
+    for p in (0, 1, 32767, 40000, int(off[E]) - 2, int(off[E]) - 1):
+        t = int((pos == p).nonzero()) // k       # the token of sorted row p, with its other rows
+        rows = pos.view(T, k)[t]
+        want, sums = torch.zeros(H, dtype=torch.float64), torch.zeros(H, dtype=torch.float64)
+        for j in range(k):
+            e = int(ids[t, j])
+            if 0 <= e < E:
+                h, w2 = ref.dequantize(hc[rows[j]], hs[rows[j]]), ref.dequantize(W[1][0][e], W[1][1][e])
+                want += w[t, j].double() * (w2 @ h)
+                sums += w[t, j].double().abs() * (w2.abs() @ h.abs())
+        sums = (I // 128 + 8 + k + 1) * U23 * sums
+        err = (out[t].cpu().double() - want).abs()
+        assert (err <= sums + BF16 * (want.abs() + sums) + 2.0 ** -133).all(), f"token {t}"
