@@ -489,11 +489,13 @@ int moe_pack_weights_mxfp4(const uint8_t *codes, const uint8_t *scales, int E, i
  * per token and SiLU(gate)*up per (token, expert) row by the rule of
  * moe_quantize_mxfp4; the products run on the scaled MFMA in its 4-bit mode
  * with fp32 accumulation, SiLU(gate)*up is formed and quantised from the fp32
- * sums, and the per-pair down rows are fp32 (one array for every slice of the
- * down reduction that moe_workspace_layout names; at T = 1 they are added and
- * not stored), so that out is rounded to bf16 once, whatever the plan.  A NaN or Inf in a token's row, in a weight or in an
- * intermediate makes the values of its block NaN, and with them the outputs
- * that they enter.  H and I must be multiples of 128.
+ * sums (0 for a gate below -88.7, whose e^-gate fp32 does not hold), and the
+ * per-pair down rows are fp32 (one array for every slice of the down reduction
+ * that moe_workspace_layout names; at T = 1 they are added and not stored), so
+ * that out is rounded to bf16 once, whatever the plan.  A NaN or Inf in a
+ * token's row, in a weight or in an intermediate makes the values of its block
+ * NaN, and with them the outputs that they enter.  H and I must be multiples of
+ * 128.
  * moe_route_forward_mxfp4: both in one call, with the same results; at most
  * 4096 pairs are routed inside the x quantisation's launch. */
 int moe_build_routing_mxfp4(const int32_t *topk_ids, int T, int k, int E, int H, int I,
