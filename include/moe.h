@@ -98,6 +98,16 @@ typedef enum {
     MOE_ROW_FP32 = 2
 } moe_row_type_t;
 
+/* Activation of the linear layers (moe_grouped_linear, moe_linear and their
+ * gradients). */
+typedef enum {
+    MOE_ACT_NONE = 0,    /* y = z */
+    MOE_ACT_SILU = 1,    /* y = z sigma(z) */
+    MOE_ACT_GELU = 2,    /* y = z Phi(z), Phi the normal distribution function */
+    MOE_ACT_SWIGLU = 3   /* y[m] = z[m] sigma(z[m]) z[M + m]: M values from 2M, gate before up
+                            (as W1's rows stand) */
+} moe_act_t;
+
 /* One row tile of the task map: rows [row_begin, row_begin + rows) of the
  * expert-sorted order, all routed to `expert`; rows <= block_m. */
 typedef struct {
@@ -556,6 +566,69 @@ int moe_combine_grad(const void *dout, const void *y, int row_type, const float 
 int moe_router_topk_grad(const float *logits, const int32_t *topk_ids, const float *topk_w,
                          const float *dtopk_w, int T, int E, int k, int renormalize, int n_shared,
                          float *dlogits, void *stream);
+
+/* Linear layers over rows in expert order, for experts of a program's own
+ * between moe_dispatch and moe_combine, and over plain rows with one matrix (a
+ * shared expert), and their gradients.  Rows and matrices are bf16 or fp16
+ * (row_type MOE_ROW_BF16 or MOE_ROW_FP16); sums, bias, activation and residual
+ * are fp32, and every output is rounded once.
+ *
+ * moe_grouped_linear: row r of expert e (expert_offsets[e] <= r <
+ * expert_offsets[e+1] in `routing`, a routing buffer of any dtype's build for
+ * the same T, k and E)
+ *   z[r][n] = sum over i of w[e][n][i] xs[r][i] + bias[e][n],  y[r] = residual[r] + act(z[r])
+ * with xs [T*k][K], w [E][N][K], bias [E][N] (NULL: none), y and residual
+ * [T*k][N] (MOE_ACT_SWIGLU: [T*k][N/2]; residual NULL: none; residual may be y
+ * itself), act a moe_act_t.  z NULL, or [T*k][N]: receives the sums with the
+ * bias, rounded, as the gradients below take them (y is formed from the
+ * unrounded ones).
+ * moe_grouped_linear_grad_x: dx[r][i] = sum over n of dy[r][n] w[e][n][i], from
+ * dy [T*k][N], dx [T*k][K].  With act other than MOE_ACT_NONE, z (the z of the
+ * product whose y was this one's xs) and dx are [T*k][K] (MOE_ACT_SWIGLU:
+ * [T*k][2K]) and dx receives the gradient of that z instead: the sum times
+ * act'(z) (SWIGLU: the gate's, then the up value's).  With MOE_ACT_NONE z is
+ * not read and may be NULL.
+ * moe_grouped_linear_grad_w: dw[e][n][i] = sum over the expert's rows of
+ * dy[r][n] xs[r][i] and, with dbias not NULL, dbias[e][n] = sum of dy[r][n]; 0
+ * for an expert without rows.  dw [E][N][K] and dbias [E][N] are of dw_type: the
+ * row type or MOE_ROW_FP32.  accumulate = 1 adds them to what dw and dbias hold
+ * (one rounding of the sum), 0 overwrites.
+ * moe_grouped_act_grad: dz[r] = dy[r] act'(z[r]) for an activation that no
+ * product follows; dy [T*k][M], z and dz [T*k][M] (MOE_ACT_SWIGLU: [T*k][2M]);
+ * act other than MOE_ACT_NONE.
+ * The calls without `grouped` take `rows` plain rows, w [N][K], bias, dw and
+ * dbias likewise.
+ *
+ * Rows behind the last valid one take no part and are not written.  An Inf or
+ * NaN in a row stays in that row's outputs (in the gradient of w: in its
+ * expert's); SiLU and GELU of -Inf are NaN.  The order of every sum depends on
+ * the sizes and on the expert's number of rows alone, so results repeat bit for
+ * bit.  rows == 0 (T == 0) returns MOE_OK with no launch, but for the gradient
+ * of w, which then is 0 (accumulate: unchanged).
+ * Requires N and K (M) positive multiples of 8, at most 65536, N * K at most
+ * 2^30; SWIGLU in the forward call N a multiple of 16, in the gradient of x K at
+ * most 32768, in the gradient of the activation M at most 32768; 1 <= k <= 16,
+ * T*k <= 65536, 1 <= E <= 511; rows <= 2^24; every buffer 16-byte aligned; no
+ * overlap of outputs with each other or with inputs, but for residual. */
+int moe_grouped_linear(const void *xs, const void *w, const void *bias, const void *residual,
+                       int row_type, int act, const void *routing, size_t routing_bytes, int T, int k,
+                       int E, int N, int K, void *z, void *y, void *stream);
+int moe_grouped_linear_grad_x(const void *dy, const void *w, const void *z, int row_type, int act,
+                              const void *routing, size_t routing_bytes, int T, int k, int E, int N,
+                              int K, void *dx, void *stream);
+int moe_grouped_linear_grad_w(const void *dy, const void *xs, int row_type, int dw_type, int accumulate,
+                              const void *routing, size_t routing_bytes, int T, int k, int E, int N,
+                              int K, void *dw, void *dbias, void *stream);
+int moe_grouped_act_grad(const void *dy, const void *z, int row_type, int act, const void *routing,
+                         size_t routing_bytes, int T, int k, int E, int M, void *dz, void *stream);
+int moe_linear(const void *x, const void *w, const void *bias, const void *residual, int row_type,
+               int act, int rows, int N, int K, void *z, void *y, void *stream);
+int moe_linear_grad_x(const void *dy, const void *w, const void *z, int row_type, int act, int rows,
+                      int N, int K, void *dx, void *stream);
+int moe_linear_grad_w(const void *dy, const void *x, int row_type, int dw_type, int accumulate, int rows,
+                      int N, int K, void *dw, void *dbias, void *stream);
+int moe_act_grad(const void *dy, const void *z, int row_type, int act, int rows, int M, void *dz,
+                 void *stream);
 
 /* int8 w8a8 with per-channel weight scales (SGLang tuning guide: the
  * int8_w8a8 dtype with per-channel quantisation).  As the fp8 pair, with

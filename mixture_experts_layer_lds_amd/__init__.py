@@ -30,6 +30,11 @@ Functions carry the C names:
     moe_combine(y, routing, k, E, topk_w)               -> rows in token order
     moe_dispatch_grad / moe_combine_grad                (gradients of the rows and of topk_w)
     moe_router_topk_grad(logits, topk_ids, topk_w, dtopk_w) -> gradient of the router scores
+    moe_grouped_linear(xs, w, routing, k, ...) / moe_linear(x, w, ...)
+                                                        -> act(x w^T + bias) + residual, by expert / of plain rows
+    moe_grouped_linear_grad_x / moe_linear_grad_x       (gradient of the rows, or of the pre-activation before them)
+    moe_grouped_linear_grad_w / moe_linear_grad_w       (gradients of the matrices and biases)
+    moe_grouped_act_grad / moe_act_grad                 (gradient of an activation by itself)
 
 plus allocation helpers (alloc_routing, alloc_workspace), pack_weights() for a
 whole weight dict, and a convenience moe_layer() that runs routing + forward
@@ -60,6 +65,7 @@ DTYPES = {"bf16": MOE_DTYPE_BF16, "fp8": MOE_DTYPE_FP8_W8A8, "mxfp8": MOE_DTYPE_
           "int8": MOE_DTYPE_INT8_W8A8, "int4": MOE_DTYPE_INT4_W4A16, "fp8b": MOE_DTYPE_FP8_BLOCK,
           "int8w": MOE_DTYPE_INT8_W8A16, "mxfp4": MOE_DTYPE_MXFP4}
 ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+ACTS = {"none": 0, "silu": 1, "gelu": 2, "swiglu": 3}
 
 
 class MoeError(RuntimeError):
@@ -128,7 +134,9 @@ EXPORTS = ("moe_status_string", "moe_pack_weights", "moe_describe_packed_weights
            "moe_route_forward_int4", "moe_route_forward_int8_w8a16", "moe_tile_copy_read",
            "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_pack_weights_mxfp4", "moe_build_routing_mxfp4",
            "moe_forward_mxfp4", "moe_route_forward_mxfp4", "moe_dispatch", "moe_combine", "moe_dispatch_grad",
-           "moe_combine_grad", "moe_router_topk_grad")
+           "moe_combine_grad", "moe_router_topk_grad", "moe_grouped_linear", "moe_grouped_linear_grad_x",
+           "moe_grouped_linear_grad_w", "moe_grouped_act_grad", "moe_linear", "moe_linear_grad_x", "moe_linear_grad_w",
+           "moe_act_grad")
 
 
 class _CInt:
@@ -219,7 +227,15 @@ def _load():
                     ("moe_combine", [P, i, P, P, sz, i, i, i, i, P, P]),
                     ("moe_dispatch_grad", [P, P, i, P, P, sz, i, i, i, i, P, P, P]),
                     ("moe_combine_grad", [P, P, i, P, P, sz, i, i, i, i, P, P, P]),
-                    ("moe_router_topk_grad", [P, P, P, P, i, i, i, i, i, P, P])):
+                    ("moe_router_topk_grad", [P, P, P, P, i, i, i, i, i, P, P]),
+                    ("moe_grouped_linear", [P, P, P, P, i, i, P, sz, i, i, i, i, i, P, P, P]),
+                    ("moe_grouped_linear_grad_x", [P, P, P, i, i, P, sz, i, i, i, i, i, P, P]),
+                    ("moe_grouped_linear_grad_w", [P, P, i, i, i, P, sz, i, i, i, i, i, P, P, P]),
+                    ("moe_grouped_act_grad", [P, P, i, i, P, sz, i, i, i, i, P, P]),
+                    ("moe_linear", [P, P, P, P, i, i, i, i, i, P, P, P]),
+                    ("moe_linear_grad_x", [P, P, P, i, i, i, i, i, P, P]),
+                    ("moe_linear_grad_w", [P, P, i, i, i, i, i, i, P, P, P]),
+                    ("moe_act_grad", [P, P, i, i, i, i, P, P])):
         f = getattr(L, n)
         f.restype = r
         f.argtypes = args
@@ -987,6 +1003,176 @@ def moe_router_topk_grad(logits, topk_ids, topk_w, dtopk_w, renormalize=True, n_
         logits.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(), dtopk_w.data_ptr(), T, E, pairs[1] - n_shared,
         1 if renormalize else 0, n_shared, dlogits.data_ptr(), _here(dev, stream)))
     return dlogits
+
+
+def _act(act):
+    if act not in ACTS:
+        raise ValueError(f"act: expected one of {', '.join(ACTS)}, got {act!r}")
+    return ACTS[act]
+
+
+def _linear_type(name, t):
+    """Row type of a linear layer's rows: bf16 or fp16."""
+    kind = ROW_TYPES.get(t.dtype, 2)
+    if kind == 2:
+        raise ValueError(f"{name}: expected bf16 or fp16 rows, got {t.dtype}")
+    return kind
+
+
+def _two(name, t):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected [rows][values], got {tuple(t.shape)}")
+    return t.shape
+
+
+def _matrices(w, grouped):
+    """(E, N, K) of the experts' matrices, or of the one of plain rows."""
+    if w.dim() != (3 if grouped else 2):
+        raise ValueError(f"w: expected {'[E][N][K]' if grouped else '[N][K]'}, got {tuple(w.shape)}")
+    return w.shape if grouped else (1, *w.shape)
+
+
+def _groups(R, k, routing):
+    """The routing arguments of a grouped call up to T and k; none for plain rows."""
+    if routing is None:
+        return ()
+    if k < 1 or R % k:
+        raise ValueError(f"expected T * k rows, got {R} with k = {k}")
+    return routing.data_ptr(), _bytes("routing", routing), R // k, k
+
+
+def _linear(name, fn, x, x_name, w, routing, k, bias, act, residual, want_z, z, out, stream):
+    code, kind = _act(act), _linear_type(x_name, x)
+    E, N, K = _matrices(w, routing is not None)
+    R = _two(x_name, x)[0]
+    M = N // 2 if code == 3 else N
+    _is(x_name, x, x.dtype, (R, K))
+    _is("w", w, x.dtype, w.shape)
+    if bias is not None:
+        _is("bias", bias, x.dtype, w.shape[:-1])
+    if residual is not None:
+        _is("residual", residual, x.dtype, (R, M))
+    dev = _check_device(x, w, bias, residual, z, out, routing)
+    groups = _groups(R, k, routing)
+    out = _output("out", out, x, (R, M), x.dtype, stream)
+    if want_z or z is not None:
+        z = _output("z", z, x, (R, N), x.dtype, stream)
+    sizes = (*groups, E, N, K) if groups else (R, N, K)
+    _check(name, fn(x.data_ptr(), w.data_ptr(), _at(bias), _at(residual), kind, code, *sizes, _at(z), out.data_ptr(),
+                    _here(dev, stream)))
+    return out if z is None else (out, z)
+
+
+def moe_grouped_linear(xs, w, routing, k, bias=None, act="none", residual=None, want_z=False, z=None, out=None,
+                       stream=None):
+    """residual + act(xs w^T + bias) of rows xs [T * k][K] in expert order (bf16 or
+    fp16) with their experts' matrices w [E][N][K] and biases [E][N]: [T * k][N]
+    (act "swiglu": [T * k][N / 2]).  With want_z or z also the sums before the
+    activation, [T * k][N], which the gradients take: (out, z).  Rows behind the last
+    valid pair are not written; residual may be out."""
+    return _linear("moe_grouped_linear", _lib.moe_grouped_linear, xs, "xs", w, routing, k, bias, act, residual, want_z,
+                   z, out, stream)
+
+
+def moe_linear(x, w, bias=None, act="none", residual=None, want_z=False, z=None, out=None, stream=None):
+    """moe_grouped_linear of plain rows x [rows][K] with one matrix w [N][K] (bias [N])."""
+    return _linear("moe_linear", _lib.moe_linear, x, "x", w, None, 1, bias, act, residual, want_z, z, out, stream)
+
+
+def _linear_grad_x(name, fn, dy, w, routing, k, z, act, dx, stream):
+    code, kind = _act(act), _linear_type("dy", dy)
+    E, N, K = _matrices(w, routing is not None)
+    R = _two("dy", dy)[0]
+    Z = 2 * K if code == 3 else K
+    _is("dy", dy, dy.dtype, (R, N))
+    _is("w", w, dy.dtype, w.shape)
+    if (z is None) != (code == 0):
+        raise ValueError(f"{name}: z goes with an activation, got act {act!r} {'without' if z is None else 'and'} z")
+    if z is not None:
+        _is("z", z, dy.dtype, (R, Z))
+    dev = _check_device(dy, w, z, dx, routing)
+    groups = _groups(R, k, routing)
+    dx = _output("dx", dx, dy, (R, Z), dy.dtype, stream)
+    sizes = (*groups, E, N, K) if groups else (R, N, K)
+    _check(name, fn(dy.data_ptr(), w.data_ptr(), _at(z), kind, code, *sizes, dx.data_ptr(), _here(dev, stream)))
+    return dx
+
+
+def moe_grouped_linear_grad_x(dy, w, routing, k, z=None, act="none", dx=None, stream=None):
+    """Gradient of moe_grouped_linear's rows, dx [T * k][K], from dy [T * k][N], the
+    gradient of its sums.  With act and z, the pre-activation of the product whose
+    output those rows were: the gradient of that z ([T * k][K], "swiglu": [T * k][2K])."""
+    return _linear_grad_x("moe_grouped_linear_grad_x", _lib.moe_grouped_linear_grad_x, dy, w, routing, k, z, act, dx, stream)
+
+
+def moe_linear_grad_x(dy, w, z=None, act="none", dx=None, stream=None):
+    """moe_grouped_linear_grad_x of plain rows with one matrix w [N][K]."""
+    return _linear_grad_x("moe_linear_grad_x", _lib.moe_linear_grad_x, dy, w, None, 1, z, act, dx, stream)
+
+
+def _linear_grad_w(name, fn, dy, x, x_name, routing, k, E, want_bias, dw, dbias, dtype, accumulate, stream):
+    kind = _linear_type("dy", dy)
+    (R, N), K = _two("dy", dy), _two(x_name, x)[1]
+    _is("dy", dy, dy.dtype, dy.shape)
+    _is(x_name, x, dy.dtype, (R, K))
+    if dtype is None:
+        dtype = dw.dtype if dw is not None else dy.dtype
+    if dtype not in (dy.dtype, torch.float32):
+        raise ValueError(f"dtype: expected {dy.dtype} or torch.float32, got {dtype}")
+    want_bias = want_bias or dbias is not None
+    if accumulate and (dw is None or (want_bias and dbias is None)):
+        raise ValueError(f"{name}: accumulate adds to the dw and dbias that it is given")
+    lead = () if routing is None else (E,)
+    dev = _check_device(dy, x, dw, dbias, routing)
+    groups = _groups(R, k, routing)
+    dw = _output("dw", dw, dy, (*lead, N, K), dtype, stream)
+    if want_bias:
+        dbias = _output("dbias", dbias, dy, (*lead, N), dtype, stream)
+    sizes = (*groups, E, N, K) if groups else (R, N, K)
+    _check(name, fn(dy.data_ptr(), x.data_ptr(), kind, ROW_TYPES[dtype], 1 if accumulate else 0, *sizes, dw.data_ptr(),
+                    _at(dbias), _here(dev, stream)))
+    return dw if dbias is None else (dw, dbias)
+
+
+def moe_grouped_linear_grad_w(dy, xs, routing, k, E, want_bias=False, dw=None, dbias=None, dtype=None, accumulate=False,
+                              stream=None):
+    """Gradient of moe_grouped_linear's matrices, dw [E][N][K], from dy [T * k][N] and
+    the rows xs [T * k][K]; with want_bias or dbias also the biases': (dw, dbias).
+    dtype: the rows' own (or dw's) or torch.float32; accumulate adds to dw and dbias."""
+    return _linear_grad_w("moe_grouped_linear_grad_w", _lib.moe_grouped_linear_grad_w, dy, xs, "xs", routing, k, E,
+                          want_bias, dw, dbias, dtype, accumulate, stream)
+
+
+def moe_linear_grad_w(dy, x, want_bias=False, dw=None, dbias=None, dtype=None, accumulate=False, stream=None):
+    """moe_grouped_linear_grad_w of plain rows: dw [N][K], dbias [N]."""
+    return _linear_grad_w("moe_linear_grad_w", _lib.moe_linear_grad_w, dy, x, "x", None, 1, 1, want_bias, dw, dbias,
+                          dtype, accumulate, stream)
+
+
+def _act_grad(name, fn, dy, z, routing, k, E, act, dz, stream):
+    code, kind = _act(act), _linear_type("dy", dy)
+    R, M = _two("dy", dy)
+    shape = (R, 2 * M if code == 3 else M)
+    _is("dy", dy, dy.dtype, dy.shape)
+    _is("z", z, dy.dtype, shape)
+    dev = _check_device(dy, z, dz, routing)
+    groups = _groups(R, k, routing)
+    dz = _output("dz", dz, dy, shape, dy.dtype, stream)
+    sizes = (*groups, E, M) if groups else (R, M)
+    _check(name, fn(dy.data_ptr(), z.data_ptr(), kind, code, *sizes, dz.data_ptr(), _here(dev, stream)))
+    return dz
+
+
+def moe_grouped_act_grad(dy, z, routing, k, E, act, dz=None, stream=None):
+    """Gradient of an activation's argument z from that of its value, dy [T * k][M];
+    z and dz [T * k][M] ("swiglu": [T * k][2M]).  Rows behind the last valid pair are
+    not written."""
+    return _act_grad("moe_grouped_act_grad", _lib.moe_grouped_act_grad, dy, z, routing, k, E, act, dz, stream)
+
+
+def moe_act_grad(dy, z, act, dz=None, stream=None):
+    """moe_grouped_act_grad of plain rows."""
+    return _act_grad("moe_act_grad", _lib.moe_act_grad, dy, z, None, 1, 1, act, dz, stream)
 
 
 def moe_set_stage_events(events):

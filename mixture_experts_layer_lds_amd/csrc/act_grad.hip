@@ -1,0 +1,63 @@
+// Gradient of an activation over rows: dz = dy act'(z), eight values a thread.
+// Bound by the rows' bytes, each read and written once; rows behind the last
+// valid one are not touched.
+#include "act.h"
+
+namespace moe {
+
+constexpr int kActThreads = 256;
+
+template <typename R, int ACT>
+__global__ void __launch_bounds__(kActThreads)
+act_grad_kernel(moe_host::ActGradArgs g) {
+  typedef typename R::elem elem;
+  constexpr int V = R::kVec;
+  const int rows = g.expert_offsets ? min(max(g.expert_offsets[g.E], 0), g.rows) : g.rows;
+  const int per_row = g.M / V;
+  const size_t total = (size_t)rows * per_row;
+  for (size_t i = (size_t)blockIdx.x * kActThreads + threadIdx.x; i < total; i += (size_t)gridDim.x * kActThreads) {
+    const size_t o = i * V;
+    float d[V], z[V];
+    row_load<R>(static_cast<const elem*>(g.dy) + o, d);
+    if constexpr (ACT == MOE_ACT_SWIGLU) {
+      const size_t row = i / per_row, at = row * 2 * g.M + (o - row * g.M);
+      float up[V], dg[V], du[V];
+      row_load<R>(static_cast<const elem*>(g.z) + at, z);
+      row_load<R>(static_cast<const elem*>(g.z) + at + g.M, up);
+#pragma unroll
+      for (int j = 0; j < V; j++) {
+        dg[j] = d[j] * up[j] * silu_slope(z[j]);
+        du[j] = d[j] * silu(z[j]);
+      }
+      row_store<R>(static_cast<elem*>(g.dz) + at, dg);
+      row_store<R>(static_cast<elem*>(g.dz) + at + g.M, du);
+    } else {
+      row_load<R>(static_cast<const elem*>(g.z) + o, z);
+#pragma unroll
+      for (int j = 0; j < V; j++) d[j] *= act_slope(z[j], ACT);
+      row_store<R>(static_cast<elem*>(g.dz) + o, d);
+    }
+  }
+}
+
+template <typename R>
+static hipError_t act_grad(const moe_host::ActGradArgs& a, int cus, hipStream_t s) {
+  const size_t groups = ((size_t)a.rows * (a.M / R::kVec) + kActThreads - 1) / kActThreads, most = (size_t)cus * 32;
+  const dim3 grid((unsigned)(groups < most ? groups : most));
+  switch (a.act) {
+    case MOE_ACT_SILU: hipLaunchKernelGGL((act_grad_kernel<R, MOE_ACT_SILU>), grid, dim3(kActThreads), 0, s, a); break;
+    case MOE_ACT_GELU: hipLaunchKernelGGL((act_grad_kernel<R, MOE_ACT_GELU>), grid, dim3(kActThreads), 0, s, a); break;
+    default: hipLaunchKernelGGL((act_grad_kernel<R, MOE_ACT_SWIGLU>), grid, dim3(kActThreads), 0, s, a); break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace moe
+
+namespace moe_host {
+
+hipError_t launch_act_grad(const ActGradArgs& a, int row_type, int cus, hipStream_t s) {
+  return row_type == MOE_ROW_BF16 ? moe::act_grad<moe::RowBf16>(a, cus, s) : moe::act_grad<moe::RowFp16>(a, cus, s);
+}
+
+}  // namespace moe_host

@@ -1,0 +1,22 @@
+// Gradient of the experts' matrices and biases (linear_tile.h).
+#include "linear_tile.h"
+
+namespace moe {
+
+typedef LinearShape<128, 128, 2, 2, 1> Tile128;
+
+template <typename Elem>
+static hipError_t grad_w(const moe_host::LinearArgs& a, int cus, hipStream_t s) {
+  const long items = (long)a.E * ((a.N + 127) / 128) * ((a.K + 127) / 128);
+  return launch_linear_tile<Elem, kGradW, Tile128>(a, items, cus, s);
+}
+
+}  // namespace moe
+
+namespace moe_host {
+
+hipError_t launch_linear_grad_w(const LinearArgs& a, int row_type, int cus, hipStream_t s) {
+  return row_type == MOE_ROW_BF16 ? moe::grad_w<moe::ElemBf16>(a, cus, s) : moe::grad_w<moe::ElemFp16>(a, cus, s);
+}
+
+}  // namespace moe_host

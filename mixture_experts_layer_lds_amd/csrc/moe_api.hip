@@ -1829,6 +1829,87 @@ int check_rows(int row_type, const void* routing, size_t routing_bytes, int T, i
   return MOE_OK;
 }
 
+// The sizes of a linear layer: N x K matrices of row_type elements.
+int check_linear(int row_type, int act, int N, int K) {
+  if ((row_type != MOE_ROW_BF16 && row_type != MOE_ROW_FP16) || act < MOE_ACT_NONE || act > MOE_ACT_SWIGLU || N <= 0 ||
+      K <= 0)
+    return MOE_ERR_INVALID_ARG;
+  if (N % 8 || K % 8 || N > 65536 || K > 65536 || (long)N * K > 1l << 30) return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+// The rows of a grouped call: the routing buffer's expert ranges.
+int grouped_rows(const void* routing, size_t routing_bytes, int T, int k, int E, int* rows, const int32_t** offsets) {
+  moe_host::RowMoveArgs a;
+  bool done;
+  const int rc = check_rows(MOE_ROW_BF16, routing, routing_bytes, T, k, E, 8, &a, &done);
+  if (rc != MOE_OK) return rc;
+  *rows = T * k;
+  *offsets = done ? nullptr : a.expert_offsets;
+  return MOE_OK;
+}
+
+constexpr int kMaxPlainRows = 1 << 24;
+
+int plain_rows(int rows) {
+  return rows < 0 ? MOE_ERR_INVALID_ARG : rows > kMaxPlainRows ? MOE_ERR_UNSUPPORTED_SHAPE : MOE_OK;
+}
+
+int run(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
+
+int linear(moe_host::LinearArgs a, int row_type, void* stream) {
+  const int rc = check_linear(row_type, a.act, a.N, a.K);
+  if (rc != MOE_OK) return rc;
+  if (a.act == MOE_ACT_SWIGLU && a.N % 16) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (a.rows == 0) return MOE_OK;
+  if (!a.rows_in || !a.w || !a.out) return MOE_ERR_INVALID_ARG;
+  for (const void* p : {a.rows_in, a.w, a.bias, a.residual, (const void*)a.z_out, (const void*)a.out})
+    if (!aligned(p, 16)) return MOE_ERR_INVALID_ARG;
+  int cus = 0;
+  if (cu_count(&cus) != MOE_OK) return MOE_ERR_HIP;
+  return run(moe_host::launch_linear(a, row_type, cus, static_cast<hipStream_t>(stream)));
+}
+
+int linear_grad_x(moe_host::LinearArgs a, int row_type, void* stream) {
+  const int rc = check_linear(row_type, a.act, a.N, a.K);
+  if (rc != MOE_OK) return rc;
+  if (a.act == MOE_ACT_SWIGLU && a.K > 32768) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (a.rows == 0) return MOE_OK;
+  if (!a.rows_in || !a.w || !a.out || (a.act != MOE_ACT_NONE && !a.z_in)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(a.rows_in, 16) || !aligned(a.w, 16) || !aligned(a.z_in, 16) || !aligned(a.out, 16)) return MOE_ERR_INVALID_ARG;
+  int cus = 0;
+  if (cu_count(&cus) != MOE_OK) return MOE_ERR_HIP;
+  return run(moe_host::launch_linear_grad_x(a, row_type, cus, static_cast<hipStream_t>(stream)));
+}
+
+int linear_grad_w(moe_host::LinearArgs a, int row_type, int dw_type, int accumulate, void* stream) {
+  const int rc = check_linear(row_type, MOE_ACT_NONE, a.N, a.K);
+  if (rc != MOE_OK) return rc;
+  if ((dw_type != row_type && dw_type != MOE_ROW_FP32) || (accumulate != 0 && accumulate != 1)) return MOE_ERR_INVALID_ARG;
+  if (!a.out || !aligned(a.out, 16) || !aligned(a.dbias, 16)) return MOE_ERR_INVALID_ARG;
+  if (a.rows == 0) {
+    if (accumulate) return MOE_OK;
+  } else if (!a.rows_in || !a.x || !aligned(a.rows_in, 16) || !aligned(a.x, 16)) {
+    return MOE_ERR_INVALID_ARG;
+  }
+  a.out_fp32 = dw_type == MOE_ROW_FP32;
+  a.accumulate = accumulate != 0;
+  int cus = 0;
+  if (cu_count(&cus) != MOE_OK) return MOE_ERR_HIP;
+  return run(moe_host::launch_linear_grad_w(a, row_type, cus, static_cast<hipStream_t>(stream)));
+}
+
+int act_grad(moe_host::ActGradArgs a, int row_type, void* stream) {
+  if ((row_type != MOE_ROW_BF16 && row_type != MOE_ROW_FP16) || a.act <= MOE_ACT_NONE || a.act > MOE_ACT_SWIGLU || a.M <= 0)
+    return MOE_ERR_INVALID_ARG;
+  if (a.M % 8 || a.M > (a.act == MOE_ACT_SWIGLU ? 32768 : 65536)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (a.rows == 0) return MOE_OK;
+  if (!a.dy || !a.z || !a.dz || !aligned(a.dy, 16) || !aligned(a.z, 16) || !aligned(a.dz, 16)) return MOE_ERR_INVALID_ARG;
+  int cus = 0;
+  if (cu_count(&cus) != MOE_OK) return MOE_ERR_HIP;
+  return run(moe_host::launch_act_grad(a, row_type, cus, static_cast<hipStream_t>(stream)));
+}
+
 void describe(const void* packed, int E, int rows, int cols, int dtype, moe_packed_weights_t* desc) {
   moe_packed_weights_t d{};
   d.data = packed;
@@ -2169,6 +2250,87 @@ int moe_router_topk_grad(const float* logits, const int32_t* topk_ids, const flo
   const hipError_t e = moe_host::launch_router_topk_grad(logits, topk_ids, topk_w, dtopk_w, T, E, k, renormalize != 0,
                                                          n_shared, dlogits, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int moe_grouped_linear(const void* xs, const void* w, const void* bias, const void* residual, int row_type, int act,
+                       const void* routing, size_t routing_bytes, int T, int k, int E, int N, int K, void* z, void* y,
+                       void* stream) {
+  moe_host::LinearArgs a{};
+  const int rc = grouped_rows(routing, routing_bytes, T, k, E, &a.rows, &a.expert_offsets);
+  if (rc != MOE_OK) return rc;
+  a.rows_in = xs, a.w = w, a.bias = bias, a.residual = residual, a.z_out = z, a.out = y;
+  a.E = E, a.N = N, a.K = K, a.act = act;
+  return linear(a, row_type, stream);
+}
+
+int moe_linear(const void* x, const void* w, const void* bias, const void* residual, int row_type, int act, int rows,
+               int N, int K, void* z, void* y, void* stream) {
+  const int rc = plain_rows(rows);
+  if (rc != MOE_OK) return rc;
+  moe_host::LinearArgs a{};
+  a.rows_in = x, a.w = w, a.bias = bias, a.residual = residual, a.z_out = z, a.out = y;
+  a.rows = rows, a.E = 1, a.N = N, a.K = K, a.act = act;
+  return linear(a, row_type, stream);
+}
+
+int moe_grouped_linear_grad_x(const void* dy, const void* w, const void* z, int row_type, int act, const void* routing,
+                              size_t routing_bytes, int T, int k, int E, int N, int K, void* dx, void* stream) {
+  moe_host::LinearArgs a{};
+  const int rc = grouped_rows(routing, routing_bytes, T, k, E, &a.rows, &a.expert_offsets);
+  if (rc != MOE_OK) return rc;
+  a.rows_in = dy, a.w = w, a.z_in = z, a.out = dx;
+  a.E = E, a.N = N, a.K = K, a.act = act;
+  return linear_grad_x(a, row_type, stream);
+}
+
+int moe_linear_grad_x(const void* dy, const void* w, const void* z, int row_type, int act, int rows, int N, int K,
+                      void* dx, void* stream) {
+  const int rc = plain_rows(rows);
+  if (rc != MOE_OK) return rc;
+  moe_host::LinearArgs a{};
+  a.rows_in = dy, a.w = w, a.z_in = z, a.out = dx;
+  a.rows = rows, a.E = 1, a.N = N, a.K = K, a.act = act;
+  return linear_grad_x(a, row_type, stream);
+}
+
+int moe_grouped_linear_grad_w(const void* dy, const void* xs, int row_type, int dw_type, int accumulate,
+                              const void* routing, size_t routing_bytes, int T, int k, int E, int N, int K, void* dw,
+                              void* dbias, void* stream) {
+  moe_host::LinearArgs a{};
+  const int rc = grouped_rows(routing, routing_bytes, T, k, E, &a.rows, &a.expert_offsets);
+  if (rc != MOE_OK) return rc;
+  a.rows_in = dy, a.x = xs, a.out = dw, a.dbias = dbias;
+  a.E = E, a.N = N, a.K = K;
+  return linear_grad_w(a, row_type, dw_type, accumulate, stream);
+}
+
+int moe_linear_grad_w(const void* dy, const void* x, int row_type, int dw_type, int accumulate, int rows, int N, int K,
+                      void* dw, void* dbias, void* stream) {
+  const int rc = plain_rows(rows);
+  if (rc != MOE_OK) return rc;
+  moe_host::LinearArgs a{};
+  a.rows_in = dy, a.x = x, a.out = dw, a.dbias = dbias;
+  a.rows = rows, a.E = 1, a.N = N, a.K = K;
+  return linear_grad_w(a, row_type, dw_type, accumulate, stream);
+}
+
+int moe_grouped_act_grad(const void* dy, const void* z, int row_type, int act, const void* routing, size_t routing_bytes,
+                         int T, int k, int E, int M, void* dz, void* stream) {
+  moe_host::ActGradArgs a{};
+  const int rc = grouped_rows(routing, routing_bytes, T, k, E, &a.rows, &a.expert_offsets);
+  if (rc != MOE_OK) return rc;
+  a.dy = dy, a.z = z, a.dz = dz;
+  a.E = E, a.M = M, a.act = act;
+  return act_grad(a, row_type, stream);
+}
+
+int moe_act_grad(const void* dy, const void* z, int row_type, int act, int rows, int M, void* dz, void* stream) {
+  const int rc = plain_rows(rows);
+  if (rc != MOE_OK) return rc;
+  moe_host::ActGradArgs a{};
+  a.dy = dy, a.z = z, a.dz = dz;
+  a.rows = rows, a.E = 1, a.M = M, a.act = act;
+  return act_grad(a, row_type, stream);
 }
 
 int moe_build_routing_fp8_block(const int32_t* topk_ids, int T, int k, int E, int H, int I,

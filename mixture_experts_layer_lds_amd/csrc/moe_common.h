@@ -477,6 +477,36 @@ hipError_t launch_rows_grad(const RowMoveArgs& a, bool to_tokens, int row_type, 
 hipError_t launch_router_topk_grad(const float* logits, const int32_t* ids, const float* w, const float* dw, int T,
                                    int E, int k, bool renorm, int n_shared, float* dl, hipStream_t s);
 
+// Linear layers over rows in expert order or plain rows, and their gradients
+// (linear.hip, linear_grad_w.hip, act_grad.hip).
+struct LinearArgs {
+  const void* rows_in;            // forward: x [rows][K]; gradients: dy [rows][N]
+  const void* x;                  // grad w: x [rows][K]
+  const void* w;                  // [E][N][K]
+  const void* bias;               // forward: [E][N], or null
+  const void* residual;           // forward: [rows][N or N / 2], or null
+  const void* z_in;               // grad x: the pre-activation of the rows, or null
+  void* z_out;                    // forward: [rows][N], or null
+  void* out;                      // y, dx or dw
+  void* dbias;                    // grad w: [E][N], or null
+  const int32_t* expert_offsets;  // null: all rows are expert 0's
+  int rows, E, N, K;              // rows: T * k, or the plain rows
+  int act;                        // moe_act_t
+  bool out_fp32, accumulate;      // grad w
+};
+hipError_t launch_linear(const LinearArgs& a, int row_type, int cus, hipStream_t s);
+hipError_t launch_linear_grad_x(const LinearArgs& a, int row_type, int cus, hipStream_t s);
+hipError_t launch_linear_grad_w(const LinearArgs& a, int row_type, int cus, hipStream_t s);
+// dz = dy act'(z): dy and dz rows of M values (SwiGLU: z and dz of 2 M).
+struct ActGradArgs {
+  const void* dy;
+  const void* z;
+  void* dz;
+  const int32_t* expert_offsets;  // null: every row
+  int rows, E, M, act;
+};
+hipError_t launch_act_grad(const ActGradArgs& a, int row_type, int cus, hipStream_t s);
+
 // fp32 rows -> e4m3 codes with the row amax held in h_scale (replaced by the scale).
 hipError_t launch_requant_rows(const float* h32, int P, int I, const int32_t* expert_offsets,
                                int E, uint8_t* hq, float* h_scale, bool find_amax, hipStream_t s);
