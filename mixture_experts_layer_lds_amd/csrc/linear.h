@@ -97,18 +97,26 @@ struct OperandTile {
     if constexpr (TRANS) return (((p >> 1) ^ swizzle(copy_row(i, lane))) << 5) | (p & 1) << 4;
     return (p ^ (lane >> 3)) * 16;   // copy_row % 8 is lane / 8
   }
-  // Fragment of block b (16 values of m or c) for the q of half h (32 q).
-  static __device__ __forceinline__ u32x4 fragment(const char* tile, int b, int h, int lane) {
+  // A lane's place in the fragments of the wave's first block, and the fragment
+  // of its block `block` for the 32 q of half h, `at` being that place in the
+  // stage.  The wave's blocks are `first` with the bits of `block` set, which
+  // are none of first's.
+  static __device__ __forceinline__ uint32_t lane_place(int first, int lane) {
+    const int g = lane >> 4;
+    if constexpr (!TRANS) return (first * 16 + (lane & 15)) * 128 + ((g ^ (lane & 7)) << 4);
+    const int q = 8 * g + ((lane & 15) >> 2);
+    return q * kPitch + (((first & 7) ^ swizzle(q)) << 5) + ((first & ~7) << 5) + 8 * (lane & 3);
+  }
+  static __device__ __forceinline__ u32x4 fragment(uint32_t at, int block, int h) {
     if constexpr (!TRANS) {
-      const char* p = tile + (b * 16 + (lane & 15)) * 128 + (((h * 4 + (lane >> 4)) ^ (lane & 7)) << 4);
-      return *reinterpret_cast<const u32x4*>(p);
+      typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+      return *reinterpret_cast<lds_u32x4*>((at ^ (h << 6)) + block * 2048);
     } else {
       typedef short s16x4 __attribute__((ext_vector_type(4)));
       typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-      const int q = h * 32 + 8 * (lane >> 4) + ((lane & 15) >> 2);
-      const char* p = tile + q * kPitch + ((b ^ swizzle(q)) << 5) + 8 * (lane & 3);
-      const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p));
-      const u32x2 c = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * kPitch)));
+      const uint32_t p = (at ^ ((block & 7) << 5)) + ((block & ~7) << 5) + h * 32 * kPitch;
+      const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(p)));
+      const u32x2 c = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(p + 4 * kPitch)));
       return u32x4{a[0], a[1], c[0], c[1]};
     }
   }
@@ -124,8 +132,11 @@ struct LinearShape {
   static constexpr int kSub = (BM + BC) * kStepQ * 2;          // bytes of a sub-step
   static constexpr int kStage = kSub * KG;
   static constexpr int kStages = 2;
-  static constexpr int kRanges = 4 * (kMaxExperts + 1);        // first item of every expert
+  static constexpr int kRanges = 3 * 4 * (kMaxExperts + 1);    // first item and rows of every expert
   static constexpr int kLds = kStage * kStages + kRanges;
+  // workgroups that share a CU's LDS, and the waves on a SIMD that they make
+  static constexpr int kOccupancy = kLds <= 80 * 1024 && kThreads <= 256 ? 2 : 1;
+  static constexpr int kWavesASimd = kOccupancy * kWaves / 4;
 };
 
 }  // namespace moe

@@ -4,18 +4,18 @@
 
 namespace moe {
 
-typedef LinearShape<128, 128, 2, 2, 1> Tile128;
+typedef LinearShape<256, 256, 2, 4, 1> Tile128;
 
 template <typename Elem>
 static hipError_t forward(const moe_host::LinearArgs& a, int cus, hipStream_t s) {
   const bool gated = a.act == MOE_ACT_SWIGLU;
-  const long tiles_c = gated ? (a.N / 2 + 63) / 64 : (a.N + 127) / 128;
-  return launch_linear_tile<Elem, kForward, Tile128>(a, max_tiles(a, 128) * tiles_c, cus, s);
+  const long tiles_c = gated ? (a.N / 2 + 127) / 128 : (a.N + 255) / 256;
+  return launch_linear_tile<Elem, kForward, Tile128>(a, max_tiles(a, 256) * tiles_c, cus, s);
 }
 
 template <typename Elem>
 static hipError_t grad_x(const moe_host::LinearArgs& a, int cus, hipStream_t s) {
-  return launch_linear_tile<Elem, kGradX, Tile128>(a, max_tiles(a, 128) * ((a.K + 127) / 128), cus, s);
+  return launch_linear_tile<Elem, kGradX, Tile128>(a, max_tiles(a, 256) * ((a.K + 255) / 256), cus, s);
 }
 
 }  // namespace moe

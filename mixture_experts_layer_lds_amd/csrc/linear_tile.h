@@ -6,17 +6,35 @@
 //    the sizes alone.  Neighbouring items share an operand's tile; workgroups
 //    are renumbered so that an XCD takes a run of them.
 //  * A stage is KG sub-steps of 64 q of both operands, copied straight to LDS
-//    while the stage before is multiplied.  Rows behind an expert's last, and q
-//    behind the end, are outside the copy's buffer range and come as zeros.
+//    while the stage before is multiplied; the copies of an item's first stages
+//    go out ahead of the item before's epilogue.  Rows behind an expert's last,
+//    and q behind the end, are outside the copy's buffer range and come as zeros.
+//  * An expert's rows are cut into tiles of nearly equal height, and the blocks
+//    of 16 rows go to the waves in turn, so that a tile of few rows costs few
+//    multiplications on every wave.
 //  * Sums are fp32; bias, activation, residual and the one rounding happen on
 //    the accumulators.
 #pragma once
+
+#include <type_traits>
 
 #include "linear.h"
 
 namespace moe {
 
 constexpr int kXcds = 8;
+
+typedef std::integral_constant<bool, true> Yes;
+typedef std::integral_constant<bool, false> No;
+
+// f(0), f(1) .. f(N - 1), each number a constant of its own type.
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void repeat(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    repeat<N, I + 1>(f);
+  }
+}
 
 // Workgroups are dealt to the XCDs in turn: renumber them so that each XCD has a run.
 __device__ __forceinline__ int xcd_order(int b, int G) {
@@ -30,28 +48,35 @@ __device__ __forceinline__ void wait_all() { __builtin_amdgcn_s_waitcnt(0x0070);
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// Rows [begin, end) of expert e, kept inside [0, rows): a routing buffer that
-// does not belong to these sizes cannot lead an access out of bounds.
+// Rows [begin, end) of an expert.
 struct RowRange {
   int begin, end;
 };
-__device__ __forceinline__ RowRange expert_rows(const moe_host::LinearArgs& g, int e) {
-  if (!g.expert_offsets) return {0, g.rows};
-  const int a = min(max(g.expert_offsets[e], 0), g.rows);
-  return {a, min(max(g.expert_offsets[e + 1], a), g.rows)};
-}
 
-// first[e]: the first item of expert e, first[E] their number; wave 0 fills it.
-template <int BM>
-__device__ __forceinline__ void count_items(const moe_host::LinearArgs& g, int tiles_c, int* first, int lane) {
+// What every workgroup knows of the experts: the first item of each (at E their
+// number) and its rows, kept inside [0, rows) so that a routing buffer that does
+// not belong to these sizes cannot lead an access out of bounds.
+struct Experts {
+  int first[kMaxExperts + 1];
+  RowRange rows[kMaxExperts + 1];
+};
+
+// Wave 0 fills it; `tiles` are an expert's items by its number of rows.
+template <typename F>
+__device__ __forceinline__ void count_items(const moe_host::LinearArgs& g, Experts* x, int lane, F&& tiles) {
   int n[8], sum = 0;
 #pragma unroll
   for (int i = 0; i < 8; i++) {
     const int e = lane * 8 + i;
     n[i] = 0;
     if (e < g.E) {
-      const RowRange r = expert_rows(g, e);
-      n[i] = (r.end - r.begin + BM - 1) / BM * tiles_c;
+      RowRange r = {0, g.rows};
+      if (g.expert_offsets) {
+        r.begin = min(max(g.expert_offsets[e], 0), g.rows);
+        r.end = min(max(g.expert_offsets[e + 1], r.begin), g.rows);
+      }
+      x->rows[e] = r;
+      n[i] = tiles(r.end - r.begin);
     }
     sum += n[i];
   }
@@ -64,100 +89,113 @@ __device__ __forceinline__ void count_items(const moe_host::LinearArgs& g, int t
   before -= sum;
 #pragma unroll
   for (int i = 0; i < 8; i++) {
-    if (lane * 8 + i <= g.E) first[lane * 8 + i] = before;
+    if (lane * 8 + i <= g.E) x->first[lane * 8 + i] = before;
     before += n[i];
   }
 }
 
 // The expert of an item: the last whose first item is not behind it.
-__device__ __forceinline__ int find_expert(const int* first, int E, int item, int lane) {
+__device__ __forceinline__ int find_expert(const Experts* x, int E, int item, int lane) {
   int n = 0;
   for (int e0 = 0; e0 < E; e0 += 64) {
     const int e = e0 + lane;
-    n += __popcll(__ballot(e < E && first[e] <= item));
+    n += __popcll(__ballot(e < E && x->first[e] <= item));
   }
-  return n - 1;
+  return uniform(n - 1);
+}
+
+// Eight neighbouring values of a row from two blocks of accumulators: of blocks
+// a and b (16 values each), a lane gets those at 8 (lane / 32) of a or, in odd
+// groups of 16 lanes, of b.
+__device__ __forceinline__ void pair_blocks(const f32x4& a, const f32x4& b, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(a[i]), __float_as_uint(b[i]), false, false);
+    v[i] = __uint_as_float(s[0]);
+    v[4 + i] = __uint_as_float(s[1]);
+  }
 }
 
 template <typename Elem, LinearOp OP, typename S>
-__global__ void __launch_bounds__(S::kThreads, 2)
+__global__ void __launch_bounds__(S::kThreads, S::kWavesASimd)
 linear_tile_kernel(moe_host::LinearArgs g) {
+  typedef typename Elem::Row Row;
+  typedef typename Row::elem elem;
   constexpr bool TR = OP == kGradW, TC = OP != kForward;
-  constexpr int BM = S::BM, BC = S::BC, KG = S::KG, MB = S::MB, CB = S::CB;
+  constexpr int BM = S::BM, BC = S::BC, KG = S::KG, WM = S::WM, WC = S::WC, MB = S::MB, CB = S::CB;
   typedef OperandTile<TR, BM> TileR;
   typedef OperandTile<TC, BC> TileC;
   static_assert(KG * TileR::kCopies % S::kWaves == 0 && KG * TileC::kCopies % S::kWaves == 0, "whole copies a wave");
   constexpr int NR = KG * TileR::kCopies / S::kWaves, NC = KG * TileC::kCopies / S::kWaves;
   __shared__ __attribute__((aligned(1024))) char lds[S::kLds];
-  int* const first = reinterpret_cast<int*>(lds + S::kStage * S::kStages);
+  Experts* const experts = reinterpret_cast<Experts*>(lds + S::kStage * S::kStages);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void*)lds;
 
   const int lane = threadIdx.x & 63;
   const int wave = uniform(threadIdx.x >> 6);
-  const int kg = wave / (S::WM * S::WC), wm = wave / S::WC % S::WM, wc = wave % S::WC;
+  const int kg = wave / (WM * WC), wm = wave / WC % WM, wc = wave % WC;
 
   const bool gated = OP == kForward && g.act == MOE_ACT_SWIGLU;
   const int N = g.N, K = g.K;
   const int width_c = OP == kForward ? (gated ? N / 2 : N) : K;   // values of c of an output row
   const int step_c = gated ? BC / 2 : BC;                         // ... and of a tile
   const int tiles_c = (width_c + step_c - 1) / step_c;
-  const int tiles_w = (N + BM - 1) / BM;                          // grad w: tiles of m
-  int total;
-  if constexpr (OP == kGradW) {
-    total = g.E * tiles_w * tiles_c;
-  } else {
-    if (wave == 0) count_items<BM>(g, tiles_c, first, lane);
-    __syncthreads();
-    total = uniform(first[g.E]);
+  if (wave == 0) {
+    count_items(g, experts, lane, [&](int rows) {
+      return (OP == kGradW ? (N + BM - 1) / BM : (rows + BM - 1) / BM) * tiles_c;
+    });
   }
+  __syncthreads();
+  const int total = uniform(experts->first[g.E]);
 
-  const int G = gridDim.x;
-  for (int item = xcd_order(blockIdx.x, G); item < total; item += G) {
-    // --- which tile
-    int e, tiles_m, at;
-    if constexpr (OP == kGradW) {
-      tiles_m = tiles_w;
-      e = item / (tiles_m * tiles_c);
-      at = item - e * tiles_m * tiles_c;
-    } else {
-      e = uniform(find_expert(first, g.E, item, lane));
-      at = item - uniform(first[e]);
-    }
-    const RowRange range = expert_rows(g, e);
-    const int begin = uniform(range.begin), rows = uniform(range.end - range.begin);
-    if constexpr (OP != kGradW) tiles_m = (rows + BM - 1) / BM;
+  // --- an item's tile, and where its operands are
+  struct Tile {
+    int e, begin, rows;   // rows: of m (forward, grad x: of the tile; grad w: N, all of them)
+    int m0, c0, tc;
+    int Q, steps;
+  };
+  Tile t;
+  const char* baseR;
+  const char* baseC;
+  uint32_t bytesR, bytesC;        // of the operands that are contiguous in q
+  uint32_t offR[NR], offC[NC];    // a lane's offset of each of its copies, but for the stage's
+  const size_t ldR = OP == kForward ? (size_t)K * 2 : (size_t)N * 2, ldC = (size_t)K * 2;   // bytes a row in memory
+
+  auto locate = [&](int item) {
+    t.e = find_expert(experts, g.E, item, lane);
+    const int at = item - uniform(experts->first[t.e]);
+    const int begin = uniform(experts->rows[t.e].begin), rows = uniform(experts->rows[t.e].end) - begin;
+    const int len_m = OP == kGradW ? N : rows, tiles_m = (len_m + BM - 1) / BM;
     // tiles of m in groups of up to 8, c by c: a run of items is a block of both
     const int group = 8 * tiles_c, m_group = at / group;
     const int ms = min(8, tiles_m - m_group * 8), in_group = at - m_group * group;
-    const int tc = in_group / ms, tm = m_group * 8 + in_group - tc * ms;
-    const int m0 = tm * BM, c0 = tc * step_c;
-
-    // --- where the operands are
-    const int Q = OP == kForward ? K : OP == kGradX ? N : rows;
-    const int steps = (Q + kStepQ * KG - 1) / (kStepQ * KG);
-    const char* baseR;
-    const char* baseC;
-    uint32_t bytesR = 0, bytesC = 0;   // of the operands that are contiguous in q
-    size_t ldR, ldC;                   // bytes a row in memory
+    t.tc = in_group / ms;
+    const int tm = m_group * 8 + in_group - t.tc * ms;
+    // rows of a tile: an expert's share, in whole rounds of blocks over the waves
+    const int height = OP == kGradW ? BM : min(BM, ((rows + tiles_m - 1) / tiles_m + 16 * WM - 1) / (16 * WM) * (16 * WM));
+    t.m0 = tm * height;
+    t.c0 = t.tc * step_c;
+    t.begin = begin;
+    t.rows = OP == kGradW ? N : min(rows, t.m0 + height);
+    t.Q = OP == kForward ? K : OP == kGradX ? N : rows;
+    t.steps = (t.Q + kStepQ * KG - 1) / (kStepQ * KG);
+    bytesR = bytesC = 0;
     if constexpr (OP == kGradW) {
-      ldR = (size_t)N * 2, ldC = (size_t)K * 2;
-      baseR = static_cast<const char*>(g.rows_in) + (size_t)begin * ldR + m0 * 2;
-      baseC = static_cast<const char*>(g.x) + (size_t)begin * ldC + c0 * 2;
+      baseR = static_cast<const char*>(g.rows_in) + (size_t)begin * ldR + t.m0 * 2;
+      baseC = static_cast<const char*>(g.x) + (size_t)begin * ldC + t.c0 * 2;
     } else {
-      ldR = (size_t)Q * 2, ldC = (size_t)K * 2;
-      baseR = static_cast<const char*>(g.rows_in) + (size_t)(begin + m0) * ldR;
-      bytesR = (uint32_t)(min(rows - m0, BM) * ldR);
-      const char* w = static_cast<const char*>(g.w) + (size_t)e * N * ldC;
+      baseR = static_cast<const char*>(g.rows_in) + (size_t)(begin + t.m0) * ldR;
+      bytesR = (uint32_t)((t.rows - t.m0) * ldR);
+      const char* w = static_cast<const char*>(g.w) + (size_t)t.e * N * ldC;
       if constexpr (OP == kForward) {
-        baseC = w + (size_t)c0 * ldC;
-        bytesC = (uint32_t)((size_t)(N - c0) * ldC);
+        baseC = w + (size_t)t.c0 * ldC;
+        bytesC = (uint32_t)((size_t)(N - t.c0) * ldC);
       } else {
-        baseC = w + (size_t)c0 * 2;
+        baseC = w + (size_t)t.c0 * 2;
       }
     }
     baseR = uniform_ptr(baseR);
     baseC = uniform_ptr(baseC);
-    // a lane's offset of each of its copies, but for the stage's
-    uint32_t offR[NR], offC[NC];
 #pragma unroll
     for (int j = 0; j < NR; j++) {
       const int id = j * S::kWaves + wave, sub = id / TileR::kCopies, i = id % TileR::kCopies;
@@ -172,29 +210,68 @@ linear_tile_kernel(moe_host::LinearArgs g) {
       if (gated) row = (row / 32) * 16 + row % 16 + ((row / 16) % 2) * (N / 2);
       offC[j] = (uint32_t)(row * ldC) + TileC::copy_byte(i, lane) + (TC ? 0 : sub * 128);
     }
+  };
 
-    auto copy = [&](int step) {
-      char* const stage = lds + (step % S::kStages) * S::kStage;
-      const int q0 = step * kStepQ * KG;
-      const bool tail = q0 + kStepQ * KG > Q;
-      const int left = min(Q - q0, kStepQ * KG);
-      auto one = [&](auto tile, bool trans, int j, const char* base, uint32_t bytes, size_t ld, int skip, uint32_t off, int part) {
-        typedef decltype(tile) T;
-        const int id = j * S::kWaves + wave, sub = id / T::kCopies, i = id % T::kCopies;
-        char* const dst = stage + sub * S::kSub + part + i * 1024;
-        if (trans) {
-          range_dma16(range_rsrc(base + (size_t)q0 * ld, (uint32_t)(left * ld) - skip), off, 0, dst);
-        } else {
-          const int q = q0 * 2 + sub * 128 + T::copy_byte(i, lane);
-          range_dma16(range_rsrc(base, bytes), tail && q >= Q * 2 ? kOutside : off, q0 * 2, dst);
-        }
-      };
+  // The copies of a stage: where they come from, and copy j of the wave.
+  struct Source {
+    __amdgpu_buffer_rsrc_t r, c;
+    int q2;
+    char* stage;
+  };
+  auto source = [&](int step) {
+    Source from;
+    const int q0 = step * kStepQ * KG, left = min(t.Q - q0, kStepQ * KG);
+    // an operand that is contiguous in q moves along its rows; the other's range moves over them
+    from.r = TR ? range_rsrc(baseR + (size_t)q0 * ldR, (uint32_t)(left * ldR) - t.m0 * 2) : range_rsrc(baseR, bytesR);
+    from.c = TC ? range_rsrc(baseC + (size_t)q0 * ldC, (uint32_t)(left * ldC) - t.c0 * 2) : range_rsrc(baseC, bytesC);
+    from.q2 = q0 * 2;
+    from.stage = lds + (step % S::kStages) * S::kStage;
+    return from;
+  };
+  auto copy_one = [&](const Source& from, auto at) {
+    constexpr int j = at;
+    if constexpr (j < NR) {
+      const int id = j * S::kWaves + wave, sub = id / TileR::kCopies, i = id % TileR::kCopies;
+      range_dma16(from.r, offR[j], TR ? 0 : from.q2, from.stage + sub * S::kSub + i * 1024);
+    } else {
+      const int id = (j - NR) * S::kWaves + wave, sub = id / TileC::kCopies, i = id % TileC::kCopies;
+      range_dma16(from.c, offC[j - NR], TC ? 0 : from.q2, from.stage + sub * S::kSub + BM * 128 + i * 1024);
+    }
+  };
+  // Ahead of the last stage's copies: no q behind the end.
+  auto cut = [&]() {
+    const int q2 = (t.steps - 1) * kStepQ * KG * 2;
+    if constexpr (!TR) {
 #pragma unroll
-      for (int j = 0; j < NR; j++) one(TileR{}, TR, j, baseR, bytesR, ldR, m0 * 2, offR[j], 0);
+      for (int j = 0; j < NR; j++) {
+        const int id = j * S::kWaves + wave;
+        if (q2 + id / TileR::kCopies * 128 + TileR::copy_byte(id % TileR::kCopies, lane) >= t.Q * 2) offR[j] = kOutside;
+      }
+    }
+    if constexpr (!TC) {
 #pragma unroll
-      for (int j = 0; j < NC; j++) one(TileC{}, TC, j, baseC, bytesC, ldC, c0 * 2, offC[j], BM * 128);
-    };
+      for (int j = 0; j < NC; j++) {
+        const int id = j * S::kWaves + wave;
+        if (q2 + id / TileC::kCopies * 128 + TileC::copy_byte(id % TileC::kCopies, lane) >= t.Q * 2) offC[j] = kOutside;
+      }
+    }
+  };
+  auto copy = [&](int step) {
+    if (step == t.steps - 1) cut();
+    const Source from = source(step);
+    repeat<NR + NC>([&](auto j) { copy_one(from, j); });
+  };
+  auto start = [&](int item) {
+    locate(item);
+    if (t.steps > 0) copy(0);
+    if (t.steps > 1) copy(1);
+  };
 
+  const int G = gridDim.x;
+  int item = xcd_order(blockIdx.x, G);
+  if (item >= total) return;
+  start(item);
+  for (;;) {
     f32x4 acc[CB][MB];
 #pragma unroll
     for (int c = 0; c < CB; c++)
@@ -203,37 +280,98 @@ linear_tile_kernel(moe_host::LinearArgs g) {
     float colsum[MB];   // grad w: sums of dy over the rows, the bias's gradient
 #pragma unroll
     for (int m = 0; m < MB; m++) colsum[m] = 0.0f;
-    const bool with_bias = OP == kGradW && g.dbias && tc == 0 && wc == 0;
-    const bool busy = OP == kGradW || m0 + wm * MB * 16 < rows;   // whether the wave has rows
+    const bool with_bias = OP == kGradW && g.dbias && t.tc == 0 && wc == 0;
 
-    if (steps > 0) copy(0);
-    for (int step = 0; step < steps; step++) {
-      wait_all();          // this stage's copies, and the LDS reads of the one before
-      barrier_nofence();
-      if (step + 1 < steps) copy(step + 1);
-      if (busy) {
-        const char* const stage = lds + (step % S::kStages) * S::kStage + kg * S::kSub;
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-          u32x4 a[CB], b[MB];
-#pragma unroll
-          for (int c = 0; c < CB; c++) a[c] = TileC::fragment(stage + BM * 128, wc * CB + c, h, lane);
-#pragma unroll
-          for (int m = 0; m < MB; m++) b[m] = TileR::fragment(stage, wm * MB + m, h, lane);
-#pragma unroll
-          for (int m = 0; m < MB; m++)
-#pragma unroll
-            for (int c = 0; c < CB; c++) acc[c][m] = Elem::mfma(a[c], b[m], acc[c][m]);
-          if (with_bias) {
-#pragma unroll
-            for (int m = 0; m < MB; m++) {
-              float v[8];
-              Elem::Row::unpack(b[m], v);
-#pragma unroll
-              for (int i = 0; i < 8; i++) colsum[m] += v[i];
-            }
-          }
+    // The stages.  A phase multiplies CB blocks of c by MP blocks of m for 32 q,
+    // and between its multiplications reads the fragments of the next phase.  The
+    // last phase of a stage first meets the other waves: the next stage has come
+    // then, and this one, read to its end, takes the copies of the one after,
+    // issued between the multiplications too.  MA: blocks of m that have rows.
+    auto stages = [&](auto blocks, auto with_sum) {
+      constexpr int MA = blocks, MP = MA % 2 ? MA : 2, MH = MA / MP, PHASES = 2 * MH;
+      u32x4 fa[2][CB], fb[2][MP];
+      const uint32_t sub = lds0 + kg * S::kSub;
+      const uint32_t placeR = sub + TileR::lane_place(wm, lane);
+      const uint32_t placeC = sub + BM * 128 + TileC::lane_place(wc * CB, lane);
+      uint32_t atR = placeR, atC = placeC;
+      auto turn = [&](int step) {   // the places in the stage of `step`
+        const uint32_t stage = (step % S::kStages) * S::kStage;
+        atR = placeR + stage;
+        atC = placeC + stage;
+        __asm__ volatile("" : "+v"(atR), "+v"(atC));   // two registers, and not one for every block
+      };
+      // fragment r of the reads ahead of phase ph: the first of m, those of c, the others of m
+      auto read_one = [&](auto phase, auto at) {
+        constexpr int ph = phase, h = ph / MH, mh = ph % MH, r = at, nc = mh == 0 ? CB : 0;
+        if constexpr (r == 0 || r > nc) {
+          constexpr int m = r == 0 ? 0 : r - nc;
+          fb[ph % 2][m] = TileR::fragment(atR, (mh * MP + m) * WM, h);
+        } else {
+          fa[h][r - 1] = TileC::fragment(atC, r - 1, h);
         }
+      };
+      auto one_stage = [&](int step, auto has_next, auto has_copies) {
+        repeat<PHASES>([&](auto phase) {
+          constexpr int ph = phase, h = ph / MH, mh = ph % MH, next = (ph + 1) % PHASES;
+          constexpr bool last = ph == PHASES - 1, copies = last && has_copies();
+          constexpr int reads = last && !has_next() ? 0 : MP + (next % MH == 0 ? CB : 0);
+          constexpr int extra = reads + (copies ? NR + NC : 0), mults = MP * CB;
+          if constexpr (last && has_next()) {
+            wait_all();
+            barrier_nofence();
+            turn(step + 1);
+          }
+          Source from;
+          if constexpr (copies) from = source(step + 2);
+          __builtin_amdgcn_sched_barrier(0);
+          // as many of them after each multiplication as it takes, none behind the last one
+          constexpr int each = (extra + mults - 1) / mults;
+          repeat<mults>([&](auto at) {
+            constexpr int i = at, m = i / CB, c = i % CB;
+            acc[c][mh * MP + m] = Elem::mfma(fa[h][c], fb[ph % 2][m], acc[c][mh * MP + m]);
+            repeat<each>([&](auto x) {
+              constexpr int k = i * each + x;
+              if constexpr (k < reads) read_one(std::integral_constant<int, next>{}, std::integral_constant<int, k>{});
+              else if constexpr (k < extra) copy_one(from, std::integral_constant<int, k - reads>{});
+            });
+            __builtin_amdgcn_sched_barrier(0);
+          });
+          if constexpr (with_sum()) {
+#pragma unroll
+            for (int m = 0; m < MP; m++) {
+              float v[8];
+              Row::unpack(fb[ph % 2][m], v);
+#pragma unroll
+              for (int i = 0; i < 8; i++) colsum[mh * MP + m] += v[i];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        });
+      };
+      const int steps = t.steps;
+      turn(0);
+      repeat<MP + CB>([&](auto r) { read_one(std::integral_constant<int, 0>{}, r); });
+      for (int step = 0; step + 2 < steps; step++) {
+        if (step + 3 == steps) cut();
+        one_stage(step, Yes{}, Yes{});
+      }
+      if (steps > 1) one_stage(steps - 2, Yes{}, No{});
+      one_stage(steps - 1, No{}, No{});
+    };
+    if (t.steps > 0) {
+      // the first stage's copies; the second's may be on their way
+      if (t.steps > 1) wait_vm<NR + NC>();
+      else wait_vm<0>();
+      barrier_nofence();
+      if constexpr (OP == kGradW) {
+        if (with_bias) stages(std::integral_constant<int, MB>{}, Yes{});
+        else stages(std::integral_constant<int, MB>{}, No{});
+      } else {
+        const int active = (t.rows - t.m0 + 16 * WM - 1) / (16 * WM);
+        if (MB >= 2 && active <= MB / 4) stages(std::integral_constant<int, (MB >= 4 ? MB / 4 : 1)>{}, No{});
+        else if (MB >= 2 && active <= MB / 2) stages(std::integral_constant<int, (MB >= 2 ? MB / 2 : 1)>{}, No{});
+        else if (MB >= 8 && active <= MB / 4 * 3) stages(std::integral_constant<int, (MB >= 8 ? MB / 4 * 3 : 1)>{}, No{});
+        else stages(std::integral_constant<int, MB>{}, No{});
       }
     }
     wait_all();
@@ -242,17 +380,16 @@ linear_tile_kernel(moe_host::LinearArgs g) {
     // --- the groups' sums, in ascending order
     if constexpr (KG > 1) {
       f32x4* const part = reinterpret_cast<f32x4*>(lds);
-      float* const part_sum = reinterpret_cast<float*>(lds + (KG - 1) * S::WM * S::WC * CB * MB * 1024);
-      const int w = wave % (S::WM * S::WC);
-      static_assert((KG - 1) * S::WM * S::WC * MB * (CB * 1024 + 256) <= S::kStage * S::kStages, "partial sums fit");
+      float* const part_sum = reinterpret_cast<float*>(lds + (KG - 1) * WM * WC * CB * MB * 1024);
+      const int w = wave % (WM * WC);
+      static_assert((KG - 1) * WM * WC * MB * (CB * 1024 + 256) <= S::kStage * S::kStages, "partial sums fit");
       if (kg > 0) {
 #pragma unroll
         for (int c = 0; c < CB; c++)
 #pragma unroll
-          for (int m = 0; m < MB; m++)
-            part[((((kg - 1) * S::WM * S::WC + w) * CB + c) * MB + m) * 64 + lane] = acc[c][m];
+          for (int m = 0; m < MB; m++) part[((((kg - 1) * WM * WC + w) * CB + c) * MB + m) * 64 + lane] = acc[c][m];
 #pragma unroll
-        for (int m = 0; m < MB; m++) part_sum[(((kg - 1) * S::WM * S::WC + w) * MB + m) * 64 + lane] = colsum[m];
+        for (int m = 0; m < MB; m++) part_sum[(((kg - 1) * WM * WC + w) * MB + m) * 64 + lane] = colsum[m];
       }
       __syncthreads();
       if (kg == 0) {
@@ -260,170 +397,172 @@ linear_tile_kernel(moe_host::LinearArgs g) {
 #pragma unroll
           for (int c = 0; c < CB; c++)
 #pragma unroll
-            for (int m = 0; m < MB; m++)
-              acc[c][m] += part[(((k * S::WM * S::WC + w) * CB + c) * MB + m) * 64 + lane];
+            for (int m = 0; m < MB; m++) acc[c][m] += part[(((k * WM * WC + w) * CB + c) * MB + m) * 64 + lane];
 #pragma unroll
-          for (int m = 0; m < MB; m++) colsum[m] += part_sum[((k * S::WM * S::WC + w) * MB + m) * 64 + lane];
+          for (int m = 0; m < MB; m++) colsum[m] += part_sum[((k * WM * WC + w) * MB + m) * 64 + lane];
         }
       }
       __syncthreads();
-      if (kg > 0) continue;
     }
 
-    // --- epilogue: lane holds c = 4 (lane / 16) + 0..3 of row lane % 16 of every block
-    typedef typename Elem::Row::elem elem;
-    const int lm = lane & 15, lc = 4 * (lane >> 4);
-    if constexpr (OP == kGradW) {
+    // --- the next item's first copies, then this one's epilogue
+    const Tile d = t;
+    item += G;
+    const bool more = item < total;
+    if (more) start(item);
+
+    // A lane has row lane % 16 of every block of m, and of two blocks of c (pair_blocks)
+    // the eight values from `place` on.
+    const int lm = lane & 15, place = 8 * (lane >> 5) + 16 * ((lane >> 4) & 1);
+    auto load8 = [](const void* p, size_t at, float (&v)[8]) { row_load<Row>(static_cast<const elem*>(p) + at, v); };
+    auto store8 = [](void* p, size_t at, const float (&v)[8]) { row_store<Row>(static_cast<elem*>(p) + at, v); };
+    if (kg == 0) {
 #pragma unroll
       for (int m = 0; m < MB; m++) {
-        const int n = m0 + (wm * MB + m) * 16 + lm;
-        if (n >= N) continue;
-        const size_t row = ((size_t)e * N + n) * K;
+        const int r = d.m0 + (m * WM + wm) * 16 + lm;
+        if constexpr (OP == kGradW) {
+          if (r < N) {
+            const size_t row = ((size_t)d.e * N + r) * K;
+            if (g.out_fp32) {
 #pragma unroll
-        for (int c = 0; c < CB; c++) {
-          const int k = c0 + (wc * CB + c) * 16 + lc;
-          if (k >= K) continue;
-          if (g.out_fp32) {
-            f32x4* const p = reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + row + k);
-            *p = g.accumulate ? *p + acc[c][m] : acc[c][m];
-          } else {
-            u32x2* const p = reinterpret_cast<u32x2*>(static_cast<elem*>(g.out) + row + k);
-            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (g.accumulate) Elem::unpack4(*p, v);
-#pragma unroll
-            for (int i = 0; i < 4; i++) v[i] += acc[c][m][i];
-            *p = Elem::pack4(v);
-          }
-        }
-      }
-      if (with_bias) {
-#pragma unroll
-        for (int m = 0; m < MB; m++) {
-          float s = colsum[m];
-          s += __shfl_xor(s, 16, 64);
-          s += __shfl_xor(s, 32, 64);
-          const int n = m0 + (wm * MB + m) * 16 + lm;
-          if (lane >= 16 || n >= N) continue;
-          const size_t at_n = (size_t)e * N + n;
-          if (g.out_fp32) {
-            float* const p = static_cast<float*>(g.dbias) + at_n;
-            *p = g.accumulate ? *p + s : s;
-          } else {
-            elem* const p = static_cast<elem*>(g.dbias) + at_n;
-            *p = Elem::round(g.accumulate ? Elem::widen(*p) + s : s);
-          }
-        }
-      }
-    } else {
-      if (!busy) continue;
-      if (gated) {
-        if constexpr (OP == kForward) {
-#pragma unroll
-          for (int m = 0; m < MB; m++) {
-            const int r = m0 + (wm * MB + m) * 16 + lm;
-            if (r >= rows) continue;
-            const size_t row = begin + r;
-#pragma unroll
-            for (int c = 0; c < CB / 2; c++) {
-              const int n = c0 + (wc * CB / 2 + c) * 16 + lc;
-              if (n >= width_c) continue;
-              float gate[4], up[4], y[4];
-#pragma unroll
-              for (int i = 0; i < 4; i++) gate[i] = acc[2 * c][m][i], up[i] = acc[2 * c + 1][m][i];
-              if (g.bias) {
-                const elem* const b = static_cast<const elem*>(g.bias) + (size_t)e * N + n;
-                float v[4];
-                Elem::unpack4(*reinterpret_cast<const u32x2*>(b), v);
-#pragma unroll
-                for (int i = 0; i < 4; i++) gate[i] += v[i];
-                Elem::unpack4(*reinterpret_cast<const u32x2*>(b + N / 2), v);
-#pragma unroll
-                for (int i = 0; i < 4; i++) up[i] += v[i];
+              for (int c = 0; c < CB; c++) {
+                const int k = d.c0 + (wc * CB + c) * 16 + 4 * (lane >> 4);
+                if (k >= K) continue;
+                f32x4* const p = reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + row + k);
+                *p = g.accumulate ? *p + acc[c][m] : acc[c][m];
               }
-              if (g.z_out) {
-                elem* const z = static_cast<elem*>(g.z_out) + row * N + n;
-                *reinterpret_cast<u32x2*>(z) = Elem::pack4(gate);
-                *reinterpret_cast<u32x2*>(z + N / 2) = Elem::pack4(up);
-              }
-#pragma unroll
-              for (int i = 0; i < 4; i++) y[i] = silu(gate[i]) * up[i];
-              const size_t o = row * width_c + n;
-              if (g.residual) {
-                float v[4];
-                Elem::unpack4(*reinterpret_cast<const u32x2*>(static_cast<const elem*>(g.residual) + o), v);
-#pragma unroll
-                for (int i = 0; i < 4; i++) y[i] += v[i];
-              }
-              *reinterpret_cast<u32x2*>(static_cast<elem*>(g.out) + o) = Elem::pack4(y);
             }
           }
-        }
-        continue;
-      }
+          if (!g.out_fp32) {
 #pragma unroll
-      for (int m = 0; m < MB; m++) {
-        const int r = m0 + (wm * MB + m) * 16 + lm;
-        if (r >= rows) continue;
-        const size_t row = begin + r;
+            for (int c = 0; c < CB; c += 2) {
+              float v[8];
+              pair_blocks(acc[c][m], acc[c + 1][m], v);
+              const int k = d.c0 + (wc * CB + c) * 16 + place;
+              if (r >= N || k >= K) continue;
+              const size_t at = ((size_t)d.e * N + r) * K + k;
+              if (g.accumulate) {
+                float b[8];
+                load8(g.out, at, b);
 #pragma unroll
-        for (int c = 0; c < CB; c++) {
-          const int n = c0 + (wc * CB + c) * 16 + lc;
-          if (n >= width_c) continue;
-          float v[4], y[4];
-#pragma unroll
-          for (int i = 0; i < 4; i++) v[i] = acc[c][m][i];
-          const size_t o = row * width_c + n;
+                for (int i = 0; i < 8; i++) v[i] += b[i];
+              }
+              store8(g.out, at, v);
+            }
+          }
+          if (with_bias) {
+            float s = colsum[m];
+            s += __shfl_xor(s, 16, 64);
+            s += __shfl_xor(s, 32, 64);
+            if (lane < 16 && r < N) {
+              const size_t at = (size_t)d.e * N + r;
+              if (g.out_fp32) {
+                float* const p = static_cast<float*>(g.dbias) + at;
+                *p = g.accumulate ? *p + s : s;
+              } else {
+                elem* const p = static_cast<elem*>(g.dbias) + at;
+                *p = Elem::round(g.accumulate ? Elem::widen(*p) + s : s);
+              }
+            }
+          }
+        } else {
+          const size_t row = (size_t)d.begin + r;
           if constexpr (OP == kForward) {
-            if (g.bias) {
-              float b[4];
-              Elem::unpack4(*reinterpret_cast<const u32x2*>(static_cast<const elem*>(g.bias) + (size_t)e * N + n), b);
+            if (gated) {
+              // blocks of gate and up values in turn: two of each give eight columns
 #pragma unroll
-              for (int i = 0; i < 4; i++) v[i] += b[i];
+              for (int c = 0; c + 3 < CB; c += 4) {
+                float gate[8], up[8], y[8];
+                pair_blocks(acc[c][m], acc[c + 2][m], gate);
+                pair_blocks(acc[c + 1][m], acc[c + 3][m], up);
+                const int n = d.c0 + (wc * CB + c) * 8 + place;
+                if (r >= d.rows || n >= width_c) continue;
+                if (g.bias) {
+                  float b[8];
+                  load8(g.bias, (size_t)d.e * N + n, b);
+#pragma unroll
+                  for (int i = 0; i < 8; i++) gate[i] += b[i];
+                  load8(g.bias, (size_t)d.e * N + width_c + n, b);
+#pragma unroll
+                  for (int i = 0; i < 8; i++) up[i] += b[i];
+                }
+                if (g.z_out) {
+                  store8(g.z_out, row * N + n, gate);
+                  store8(g.z_out, row * N + width_c + n, up);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; i++) y[i] = silu(gate[i]) * up[i];
+                const size_t o = row * width_c + n;
+                if (g.residual) {
+                  float b[8];
+                  load8(g.residual, o, b);
+#pragma unroll
+                  for (int i = 0; i < 8; i++) y[i] += b[i];
+                }
+                store8(g.out, o, y);
+              }
+              continue;
             }
-            if (g.z_out) *reinterpret_cast<u32x2*>(static_cast<elem*>(g.z_out) + o) = Elem::pack4(v);
+          }
 #pragma unroll
-            for (int i = 0; i < 4; i++) y[i] = activate(v[i], g.act);
-            if (g.residual) {
-              float b[4];
-              Elem::unpack4(*reinterpret_cast<const u32x2*>(static_cast<const elem*>(g.residual) + o), b);
+          for (int c = 0; c < CB; c += 2) {
+            float v[8], y[8];
+            pair_blocks(acc[c][m], acc[c + 1][m], v);
+            const int n = d.c0 + (wc * CB + c) * 16 + place;
+            if (r >= d.rows || n >= width_c) continue;
+            const size_t o = row * width_c + n;
+            if constexpr (OP == kForward) {
+              if (g.bias) {
+                float b[8];
+                load8(g.bias, (size_t)d.e * N + n, b);
 #pragma unroll
-              for (int i = 0; i < 4; i++) y[i] += b[i];
+                for (int i = 0; i < 8; i++) v[i] += b[i];
+              }
+              if (g.z_out) store8(g.z_out, o, v);
+              if (g.act != MOE_ACT_NONE) {
+#pragma unroll
+                for (int i = 0; i < 8; i++) v[i] = activate(v[i], g.act);
+              }
+              if (g.residual) {
+                float b[8];
+                load8(g.residual, o, b);
+#pragma unroll
+                for (int i = 0; i < 8; i++) v[i] += b[i];
+              }
+              store8(g.out, o, v);
+            } else if (g.act == MOE_ACT_SWIGLU) {
+              const size_t oz = row * 2 * width_c + n;
+              float gate[8], up[8];
+              load8(g.z_in, oz, gate);
+              load8(g.z_in, oz + width_c, up);
+#pragma unroll
+              for (int i = 0; i < 8; i++) {
+                y[i] = v[i] * silu(gate[i]);
+                v[i] = v[i] * up[i] * silu_slope(gate[i]);
+              }
+              store8(g.out, oz, v);
+              store8(g.out, oz + width_c, y);
+            } else {
+              if (g.act != MOE_ACT_NONE) {
+                float z[8];
+                load8(g.z_in, o, z);
+#pragma unroll
+                for (int i = 0; i < 8; i++) v[i] *= act_slope(z[i], g.act);
+              }
+              store8(g.out, o, v);
             }
-            *reinterpret_cast<u32x2*>(static_cast<elem*>(g.out) + o) = Elem::pack4(y);
-          } else if (g.act == MOE_ACT_SWIGLU) {
-            const size_t oz = row * 2 * width_c + n;
-            const elem* const z = static_cast<const elem*>(g.z_in) + oz;
-            float gate[4], up[4];
-            Elem::unpack4(*reinterpret_cast<const u32x2*>(z), gate);
-            Elem::unpack4(*reinterpret_cast<const u32x2*>(z + width_c), up);
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-              y[i] = v[i] * silu(gate[i]);
-              v[i] = v[i] * up[i] * silu_slope(gate[i]);
-            }
-            elem* const out = static_cast<elem*>(g.out) + oz;
-            *reinterpret_cast<u32x2*>(out) = Elem::pack4(v);
-            *reinterpret_cast<u32x2*>(out + width_c) = Elem::pack4(y);
-          } else {
-            if (g.act != MOE_ACT_NONE) {
-              float z[4];
-              Elem::unpack4(*reinterpret_cast<const u32x2*>(static_cast<const elem*>(g.z_in) + o), z);
-#pragma unroll
-              for (int i = 0; i < 4; i++) v[i] *= act_slope(z[i], g.act);
-            }
-            *reinterpret_cast<u32x2*>(static_cast<elem*>(g.out) + o) = Elem::pack4(v);
           }
         }
       }
     }
+    if (!more) break;
   }
 }
 
-// A persistent grid for at most `items` items, `occupancy` workgroups a CU.
+// A persistent grid for at most `items` items.
 template <typename Elem, LinearOp OP, typename S>
 static hipError_t launch_linear_tile(const moe_host::LinearArgs& a, long items, int cus, hipStream_t s) {
-  constexpr int kOccupancy = S::kLds <= 80 * 1024 && S::kThreads <= 256 ? 2 : 1;
-  const long grid = items < (long)cus * kOccupancy ? items : (long)cus * kOccupancy;
+  const long most = (long)cus * S::kOccupancy, grid = items < most ? items : most;
   if (grid <= 0) return hipSuccess;
   hipLaunchKernelGGL((linear_tile_kernel<Elem, OP, S>), dim3((unsigned)grid), dim3(S::kThreads), 0, s, a);
   return hipGetLastError();
