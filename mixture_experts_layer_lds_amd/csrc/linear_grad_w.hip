@@ -8,7 +8,8 @@ typedef LinearShape<256, 256, 2, 4, 1> Tile128;
 template <typename Elem>
 static hipError_t grad_w(const moe_host::LinearArgs& a, int cus, hipStream_t s) {
   const long items = (long)a.E * ((a.N + 255) / 256) * ((a.K + 255) / 256);
-  return launch_linear_tile<Elem, kGradW, Tile128>(a, items, cus, s);
+  return a.dbias ? launch_linear_tile<Elem, kGradW, Tile128, true>(a, items, cus, s)
+                 : launch_linear_tile<Elem, kGradW, Tile128, false>(a, items, cus, s);
 }
 
 }  // namespace moe

@@ -116,7 +116,8 @@ __device__ __forceinline__ void pair_blocks(const f32x4& a, const f32x4& b, floa
   }
 }
 
-template <typename Elem, LinearOp OP, typename S>
+// SUM: grad w with the bias's gradient.
+template <typename Elem, LinearOp OP, typename S, bool SUM>
 __global__ void __launch_bounds__(S::kThreads, S::kWavesASimd)
 linear_tile_kernel(moe_host::LinearArgs g) {
   typedef typename Elem::Row Row;
@@ -221,9 +222,10 @@ linear_tile_kernel(moe_host::LinearArgs g) {
   auto source = [&](int step) {
     Source from;
     const int q0 = step * kStepQ * KG, left = min(t.Q - q0, kStepQ * KG);
+    const bool any = left > 0;   // stages behind the last one are copies of nothing
     // an operand that is contiguous in q moves along its rows; the other's range moves over them
-    from.r = TR ? range_rsrc(baseR + (size_t)q0 * ldR, (uint32_t)(left * ldR) - t.m0 * 2) : range_rsrc(baseR, bytesR);
-    from.c = TC ? range_rsrc(baseC + (size_t)q0 * ldC, (uint32_t)(left * ldC) - t.c0 * 2) : range_rsrc(baseC, bytesC);
+    from.r = TR ? range_rsrc(baseR + (size_t)q0 * ldR, any ? (uint32_t)(left * ldR) - t.m0 * 2 : 0) : range_rsrc(baseR, any ? bytesR : 0);
+    from.c = TC ? range_rsrc(baseC + (size_t)q0 * ldC, any ? (uint32_t)(left * ldC) - t.c0 * 2 : 0) : range_rsrc(baseC, any ? bytesC : 0);
     from.q2 = q0 * 2;
     from.stage = lds + (step % S::kStages) * S::kStage;
     return from;
@@ -263,8 +265,9 @@ linear_tile_kernel(moe_host::LinearArgs g) {
   };
   auto start = [&](int item) {
     locate(item);
-    if (t.steps > 0) copy(0);
-    if (t.steps > 1) copy(1);
+    if (t.steps == 0) return;
+    copy(0);
+    copy(1);
   };
 
   const int G = gridDim.x;
@@ -280,20 +283,22 @@ linear_tile_kernel(moe_host::LinearArgs g) {
     float colsum[MB];   // grad w: sums of dy over the rows, the bias's gradient
 #pragma unroll
     for (int m = 0; m < MB; m++) colsum[m] = 0.0f;
-    const bool with_bias = OP == kGradW && g.dbias && t.tc == 0 && wc == 0;
+    const bool with_bias = SUM && t.tc == 0 && wc == 0;
 
     // The stages.  A phase multiplies CB blocks of c by MP blocks of m for 32 q,
     // and between its multiplications reads the fragments of the next phase.  The
     // last phase of a stage first meets the other waves: the next stage has come
     // then, and this one, read to its end, takes the copies of the one after,
-    // issued between the multiplications too.  MA: blocks of m that have rows.
-    auto stages = [&](auto blocks, auto with_sum) {
-      constexpr int MA = blocks, MP = MA % 2 ? MA : 2, MH = MA / MP, PHASES = 2 * MH;
+    // issued between the multiplications too.  (Behind the last stage the same
+    // code copies and reads nothing of use: one loop, whose accumulators stay in
+    // their registers.)  MA: blocks of m that have rows.
+    auto stages = [&](auto blocks) {
+      constexpr int MA = blocks, MP = MA > 4 ? MA / 2 : MA, MH = MA / MP, PHASES = 2 * MH;
       u32x4 fa[2][CB], fb[2][MP];
       const uint32_t sub = lds0 + kg * S::kSub;
       const uint32_t placeR = sub + TileR::lane_place(wm, lane);
       const uint32_t placeC = sub + BM * 128 + TileC::lane_place(wc * CB, lane);
-      uint32_t atR = placeR, atC = placeC;
+      uint32_t atR, atC;
       auto turn = [&](int step) {   // the places in the stage of `step`
         const uint32_t stage = (step % S::kStages) * S::kStage;
         atR = placeR + stage;
@@ -310,19 +315,21 @@ linear_tile_kernel(moe_host::LinearArgs g) {
           fa[h][r - 1] = TileC::fragment(atC, r - 1, h);
         }
       };
-      auto one_stage = [&](int step, auto has_next, auto has_copies) {
+      turn(0);
+      repeat<MP + CB>([&](auto r) { read_one(std::integral_constant<int, 0>{}, r); });
+      for (int step = 0; step < t.steps; step++) {
+        if (step + 3 == t.steps) cut();
         repeat<PHASES>([&](auto phase) {
           constexpr int ph = phase, h = ph / MH, mh = ph % MH, next = (ph + 1) % PHASES;
-          constexpr bool last = ph == PHASES - 1, copies = last && has_copies();
-          constexpr int reads = last && !has_next() ? 0 : MP + (next % MH == 0 ? CB : 0);
-          constexpr int extra = reads + (copies ? NR + NC : 0), mults = MP * CB;
-          if constexpr (last && has_next()) {
+          constexpr bool last = ph == PHASES - 1;
+          constexpr int reads = MP + (next % MH == 0 ? CB : 0), extra = reads + (last ? NR + NC : 0), mults = MP * CB;
+          Source from;
+          if constexpr (last) {
             wait_all();
             barrier_nofence();
             turn(step + 1);
+            from = source(step + 2);
           }
-          Source from;
-          if constexpr (copies) from = source(step + 2);
           __builtin_amdgcn_sched_barrier(0);
           // as many of them after each multiplication as it takes, none behind the last one
           constexpr int each = (extra + mults - 1) / mults;
@@ -336,49 +343,38 @@ linear_tile_kernel(moe_host::LinearArgs g) {
             });
             __builtin_amdgcn_sched_barrier(0);
           });
-          if constexpr (with_sum()) {
+          if constexpr (SUM) {
+            if (with_bias) {
 #pragma unroll
-            for (int m = 0; m < MP; m++) {
-              float v[8];
-              Row::unpack(fb[ph % 2][m], v);
+              for (int m = 0; m < MP; m++) {
+                float v[8];
+                Row::unpack(fb[ph % 2][m], v);
 #pragma unroll
-              for (int i = 0; i < 8; i++) colsum[mh * MP + m] += v[i];
+                for (int i = 0; i < 8; i++) colsum[mh * MP + m] += v[i];
+              }
             }
-            __builtin_amdgcn_sched_barrier(0);
           }
         });
-      };
-      const int steps = t.steps;
-      turn(0);
-      repeat<MP + CB>([&](auto r) { read_one(std::integral_constant<int, 0>{}, r); });
-      for (int step = 0; step + 2 < steps; step++) {
-        if (step + 3 == steps) cut();
-        one_stage(step, Yes{}, Yes{});
       }
-      if (steps > 1) one_stage(steps - 2, Yes{}, No{});
-      one_stage(steps - 1, No{}, No{});
     };
     if (t.steps > 0) {
-      // the first stage's copies; the second's may be on their way
-      if (t.steps > 1) wait_vm<NR + NC>();
-      else wait_vm<0>();
+      wait_vm<NR + NC>();   // the first stage's copies; the second's may be on their way
       barrier_nofence();
       if constexpr (OP == kGradW) {
-        if (with_bias) stages(std::integral_constant<int, MB>{}, Yes{});
-        else stages(std::integral_constant<int, MB>{}, No{});
+        stages(std::integral_constant<int, MB>{});
       } else {
         const int active = (t.rows - t.m0 + 16 * WM - 1) / (16 * WM);
-        if (MB >= 2 && active <= MB / 4) stages(std::integral_constant<int, (MB >= 4 ? MB / 4 : 1)>{}, No{});
-        else if (MB >= 2 && active <= MB / 2) stages(std::integral_constant<int, (MB >= 2 ? MB / 2 : 1)>{}, No{});
-        else if (MB >= 8 && active <= MB / 4 * 3) stages(std::integral_constant<int, (MB >= 8 ? MB / 4 * 3 : 1)>{}, No{});
-        else stages(std::integral_constant<int, MB>{}, No{});
+        if (MB >= 2 && active <= MB / 4) stages(std::integral_constant<int, (MB >= 4 ? MB / 4 : 1)>{});
+        else if (MB >= 2 && active <= MB / 2) stages(std::integral_constant<int, (MB >= 2 ? MB / 2 : 1)>{});
+        else if (MB >= 8 && active <= MB / 4 * 3) stages(std::integral_constant<int, (MB >= 8 ? MB / 4 * 3 : 1)>{});
+        else stages(std::integral_constant<int, MB>{});
       }
     }
-    wait_all();
-    barrier_nofence();   // the stages are free again
 
     // --- the groups' sums, in ascending order
     if constexpr (KG > 1) {
+      wait_all();
+      barrier_nofence();   // no copy is on its way, the stages are free
       f32x4* const part = reinterpret_cast<f32x4*>(lds);
       float* const part_sum = reinterpret_cast<float*>(lds + (KG - 1) * WM * WC * CB * MB * 1024);
       const int w = wave % (WM * WC);
@@ -450,7 +446,7 @@ linear_tile_kernel(moe_host::LinearArgs g) {
               store8(g.out, at, v);
             }
           }
-          if (with_bias) {
+          if (SUM && with_bias) {
             float s = colsum[m];
             s += __shfl_xor(s, 16, 64);
             s += __shfl_xor(s, 32, 64);
@@ -560,11 +556,11 @@ linear_tile_kernel(moe_host::LinearArgs g) {
 }
 
 // A persistent grid for at most `items` items.
-template <typename Elem, LinearOp OP, typename S>
+template <typename Elem, LinearOp OP, typename S, bool SUM = false>
 static hipError_t launch_linear_tile(const moe_host::LinearArgs& a, long items, int cus, hipStream_t s) {
   const long most = (long)cus * S::kOccupancy, grid = items < most ? items : most;
   if (grid <= 0) return hipSuccess;
-  hipLaunchKernelGGL((linear_tile_kernel<Elem, OP, S>), dim3((unsigned)grid), dim3(S::kThreads), 0, s, a);
+  hipLaunchKernelGGL((linear_tile_kernel<Elem, OP, S, SUM>), dim3((unsigned)grid), dim3(S::kThreads), 0, s, a);
   return hipGetLastError();
 }
 
