@@ -123,15 +123,14 @@ struct OperandTile {
 };
 
 // A tile of BM by BC, WM by WC waves, KG groups of them that take the
-// sub-steps of a stage in turn and add their sums at the end.
-template <int BM_, int BC_, int WM_, int WC_, int KG_>
+// sub-steps of a stage in turn and add their sums at the end; NS stages in LDS.
+template <int BM_, int BC_, int WM_, int WC_, int KG_, int NS_>
 struct LinearShape {
-  static constexpr int BM = BM_, BC = BC_, WM = WM_, WC = WC_, KG = KG_;
+  static constexpr int BM = BM_, BC = BC_, WM = WM_, WC = WC_, KG = KG_, kStages = NS_;
   static constexpr int kWaves = WM * WC * KG, kThreads = kWaves * 64;
   static constexpr int MB = BM / WM / 16, CB = BC / WC / 16;   // 16 x 16 blocks of a wave
   static constexpr int kSub = (BM + BC) * kStepQ * 2;          // bytes of a sub-step
   static constexpr int kStage = kSub * KG;
-  static constexpr int kStages = 2;
   static constexpr int kRanges = 3 * 4 * (kMaxExperts + 1);    // first item and rows of every expert
   static constexpr int kLds = kStage * kStages + kRanges;
   // workgroups that share a CU's LDS, and the waves on a SIMD that they make

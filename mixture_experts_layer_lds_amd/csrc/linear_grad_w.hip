@@ -3,7 +3,7 @@
 
 namespace moe {
 
-typedef LinearShape<256, 256, 2, 4, 1> Tile128;
+typedef LinearShape<256, 256, 2, 4, 1, 2> Tile128;
 
 template <typename Elem>
 static hipError_t grad_w(const moe_host::LinearArgs& a, int cus, hipStream_t s) {

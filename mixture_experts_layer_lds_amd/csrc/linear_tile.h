@@ -6,8 +6,8 @@
 //    the sizes alone.  Neighbouring items share an operand's tile; workgroups
 //    are renumbered so that an XCD takes a run of them.
 //  * A stage is KG sub-steps of 64 q of both operands, copied straight to LDS
-//    while the stage before is multiplied; the copies of an item's first stages
-//    go out ahead of the item before's epilogue.  Rows behind an expert's last,
+//    while the stages before are multiplied, on from item to item without a
+//    pause.  Rows behind an expert's last,
 //    and q behind the end, are outside the copy's buffer range and come as zeros.
 //  * An expert's rows are cut into tiles of nearly equal height, and the blocks
 //    of 16 rows go to the waves in turn, so that a tile of few rows costs few
@@ -45,6 +45,13 @@ __device__ __forceinline__ int xcd_order(int b, int G) {
 
 // Every vector-memory and LDS operation of this wave is done.
 __device__ __forceinline__ void wait_all() { __builtin_amdgcn_s_waitcnt(0x0070); }
+
+// All but the youngest N vector-memory operations are, and every LDS one.
+template <int N>
+__device__ __forceinline__ void wait_but() {
+  static_assert(N >= 0 && N < 64, "vmcnt is a 6-bit field");
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | (0x7 << 4) | ((N >> 4) << 14));
+}
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
@@ -124,10 +131,12 @@ linear_tile_kernel(moe_host::LinearArgs g) {
   typedef typename Row::elem elem;
   constexpr bool TR = OP == kGradW, TC = OP != kForward;
   constexpr int BM = S::BM, BC = S::BC, KG = S::KG, WM = S::WM, WC = S::WC, MB = S::MB, CB = S::CB;
-  typedef OperandTile<TR, BM> TileR;
+  // the operand of m in two halves, that of c in one piece, in this order in a sub-step
+  typedef OperandTile<TR, BM / 2> HalfR;
   typedef OperandTile<TC, BC> TileC;
-  static_assert(KG * TileR::kCopies % S::kWaves == 0 && KG * TileC::kCopies % S::kWaves == 0, "whole copies a wave");
-  constexpr int NR = KG * TileR::kCopies / S::kWaves, NC = KG * TileC::kCopies / S::kWaves;
+  static_assert(KG * HalfR::kCopies % S::kWaves == 0 && KG * TileC::kCopies % S::kWaves == 0, "whole copies a wave");
+  constexpr int NH = KG * HalfR::kCopies / S::kWaves, NC = KG * TileC::kCopies / S::kWaves;   // copies of a wave
+  constexpr int NA = NC + NH, NALL = NC + 2 * NH;
   __shared__ __attribute__((aligned(1024))) char lds[S::kLds];
   Experts* const experts = reinterpret_cast<Experts*>(lds + S::kStage * S::kStages);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void*)lds;
@@ -149,20 +158,14 @@ linear_tile_kernel(moe_host::LinearArgs g) {
   __syncthreads();
   const int total = uniform(experts->first[g.E]);
 
-  // --- an item's tile, and where its operands are
+  // --- an item's tile
   struct Tile {
     int e, begin, rows;   // rows: of m (forward, grad x: of the tile; grad w: N, all of them)
     int m0, c0, tc;
     int Q, steps;
   };
-  Tile t;
-  const char* baseR;
-  const char* baseC;
-  uint32_t bytesR, bytesC;        // of the operands that are contiguous in q
-  uint32_t offR[NR], offC[NC];    // a lane's offset of each of its copies, but for the stage's
-  const size_t ldR = OP == kForward ? (size_t)K * 2 : (size_t)N * 2, ldC = (size_t)K * 2;   // bytes a row in memory
-
-  auto locate = [&](int item) {
+  auto decode = [&](int item) {
+    Tile t;
     t.e = find_expert(experts, g.E, item, lane);
     const int at = item - uniform(experts->first[t.e]);
     const int begin = uniform(experts->rows[t.e].begin), rows = uniform(experts->rows[t.e].end) - begin;
@@ -180,101 +183,140 @@ linear_tile_kernel(moe_host::LinearArgs g) {
     t.rows = OP == kGradW ? N : min(rows, t.m0 + height);
     t.Q = OP == kForward ? K : OP == kGradX ? N : rows;
     t.steps = (t.Q + kStepQ * KG - 1) / (kStepQ * KG);
+    return t;
+  };
+
+  // --- the copies run kStages stages ahead of the multiplications, on into the
+  // next item: `from` is the tile they are in, from_step its next stage
+  Tile from;
+  int from_item, from_step;
+  const char* baseR;
+  const char* baseC;
+  uint32_t bytesR, bytesC;        // of the operands that are contiguous in q
+  uint32_t offR[2 * NH], offC[NC];   // a lane's offset of each of its copies, but for the stage's
+  const size_t ldR = OP == kForward ? (size_t)K * 2 : (size_t)N * 2, ldC = (size_t)K * 2;   // bytes a row in memory
+  const int G = gridDim.x;
+
+  // gate and up rows alternate, 16 by 16, so that a wave has both of a column
+  auto weight_row = [&](int row) { return gated ? (row / 32) * 16 + row % 16 + ((row / 16) % 2) * (N / 2) : row; };
+
+  // The copies go to item `item`, or to the first behind it that has any.
+  auto enter = [&](int item) {
+    from_step = 0;
+    for (; item < total; item += G) {
+      from = decode(item);
+      if (from.steps > 0) break;
+    }
+    from_item = item;
+    if (item >= total) {
+      from.steps = 1 << 30;   // copies of nothing
+      from.Q = 0;
+      return;
+    }
     bytesR = bytesC = 0;
     if constexpr (OP == kGradW) {
-      baseR = static_cast<const char*>(g.rows_in) + (size_t)begin * ldR + t.m0 * 2;
-      baseC = static_cast<const char*>(g.x) + (size_t)begin * ldC + t.c0 * 2;
+      baseR = static_cast<const char*>(g.rows_in) + (size_t)from.begin * ldR + from.m0 * 2;
+      baseC = static_cast<const char*>(g.x) + (size_t)from.begin * ldC + from.c0 * 2;
     } else {
-      baseR = static_cast<const char*>(g.rows_in) + (size_t)(begin + t.m0) * ldR;
-      bytesR = (uint32_t)((t.rows - t.m0) * ldR);
-      const char* w = static_cast<const char*>(g.w) + (size_t)t.e * N * ldC;
+      baseR = static_cast<const char*>(g.rows_in) + (size_t)(from.begin + from.m0) * ldR;
+      bytesR = (uint32_t)((from.rows - from.m0) * ldR);
+      const char* w = static_cast<const char*>(g.w) + (size_t)from.e * N * ldC;
       if constexpr (OP == kForward) {
-        baseC = w + (size_t)t.c0 * ldC;
-        bytesC = (uint32_t)((size_t)(N - t.c0) * ldC);
+        baseC = w + (size_t)from.c0 * ldC;
+        bytesC = (uint32_t)((size_t)(N - from.c0) * ldC);
       } else {
-        baseC = w + (size_t)t.c0 * 2;
+        baseC = w + (size_t)from.c0 * 2;
       }
     }
     baseR = uniform_ptr(baseR);
     baseC = uniform_ptr(baseC);
 #pragma unroll
-    for (int j = 0; j < NR; j++) {
-      const int id = j * S::kWaves + wave, sub = id / TileR::kCopies, i = id % TileR::kCopies;
-      const int row = TileR::copy_row(i, lane) + (TR ? sub * kStepQ : 0);
-      offR[j] = (uint32_t)(row * ldR) + TileR::copy_byte(i, lane) + (TR ? 0 : sub * 128);
+    for (int j = 0; j < 2 * NH; j++) {
+      const int id = j % NH * S::kWaves + wave, sub = id / HalfR::kCopies, i = id % HalfR::kCopies, half = j / NH * (BM / 2);
+      const int row = HalfR::copy_row(i, lane) + (TR ? sub * kStepQ : half);
+      offR[j] = (uint32_t)(row * ldR) + HalfR::copy_byte(i, lane) + (TR ? half * 2 : sub * 128);
     }
 #pragma unroll
     for (int j = 0; j < NC; j++) {
       const int id = j * S::kWaves + wave, sub = id / TileC::kCopies, i = id % TileC::kCopies;
-      int row = TileC::copy_row(i, lane) + (TC ? sub * kStepQ : 0);
-      // gate and up rows alternate, 16 by 16, so that a wave has both of a column
-      if (gated) row = (row / 32) * 16 + row % 16 + ((row / 16) % 2) * (N / 2);
+      const int row = TC ? TileC::copy_row(i, lane) + sub * kStepQ : weight_row(TileC::copy_row(i, lane));
       offC[j] = (uint32_t)(row * ldC) + TileC::copy_byte(i, lane) + (TC ? 0 : sub * 128);
     }
   };
 
-  // The copies of a stage: where they come from, and copy j of the wave.
+  // The copies of the stage at from_step: where they come from, and copy j of the wave.
   struct Source {
     __amdgpu_buffer_rsrc_t r, c;
     int q2;
     char* stage;
   };
-  auto source = [&](int step) {
-    Source from;
-    const int q0 = step * kStepQ * KG, left = min(t.Q - q0, kStepQ * KG);
-    const bool any = left > 0;   // stages behind the last one are copies of nothing
+  auto source = [&](int slot) {
+    Source s;
+    const int q0 = from_step * kStepQ * KG, left = min(from.Q - q0, kStepQ * KG);
+    const bool any = left > 0;
     // an operand that is contiguous in q moves along its rows; the other's range moves over them
-    from.r = TR ? range_rsrc(baseR + (size_t)q0 * ldR, any ? (uint32_t)(left * ldR) - t.m0 * 2 : 0) : range_rsrc(baseR, any ? bytesR : 0);
-    from.c = TC ? range_rsrc(baseC + (size_t)q0 * ldC, any ? (uint32_t)(left * ldC) - t.c0 * 2 : 0) : range_rsrc(baseC, any ? bytesC : 0);
-    from.q2 = q0 * 2;
-    from.stage = lds + (step % S::kStages) * S::kStage;
-    return from;
+    const char* const r = TR ? baseR + (size_t)q0 * ldR : baseR;
+    const char* const c = TC ? baseC + (size_t)q0 * ldC : baseC;
+    const uint32_t in_r = TR ? (uint32_t)(left * ldR) - from.m0 * 2 : bytesR, in_c = TC ? (uint32_t)(left * ldC) - from.c0 * 2 : bytesC;
+    s.r = range_rsrc(uniform_ptr(r), uniform(any ? in_r : 0));
+    s.c = range_rsrc(uniform_ptr(c), uniform(any ? in_c : 0));
+    s.q2 = q0 * 2;
+    s.stage = lds + slot * S::kStage;
+    return s;
   };
-  auto copy_one = [&](const Source& from, auto at) {
-    constexpr int j = at;
-    if constexpr (j < NR) {
-      const int id = j * S::kWaves + wave, sub = id / TileR::kCopies, i = id % TileR::kCopies;
-      range_dma16(from.r, offR[j], TR ? 0 : from.q2, from.stage + sub * S::kSub + i * 1024);
+  // copy j: those of c, then of the halves of m
+  auto copy_one = [&](const Source& s, auto at) {
+    constexpr int j = at, r = j - NC;
+    if constexpr (j < NC) {
+      const int id = j * S::kWaves + wave, sub = id / TileC::kCopies, i = id % TileC::kCopies;
+      range_dma16(s.c, offC[j], TC ? 0 : s.q2, s.stage + sub * S::kSub + BM * 128 + i * 1024);
     } else {
-      const int id = (j - NR) * S::kWaves + wave, sub = id / TileC::kCopies, i = id % TileC::kCopies;
-      range_dma16(from.c, offC[j - NR], TC ? 0 : from.q2, from.stage + sub * S::kSub + BM * 128 + i * 1024);
+      const int id = r % NH * S::kWaves + wave, sub = id / HalfR::kCopies, i = id % HalfR::kCopies;
+      range_dma16(s.r, offR[r], TR ? 0 : s.q2, s.stage + sub * S::kSub + r / NH * (BM / 2 * 128) + i * 1024);
     }
   };
-  // Ahead of the last stage's copies: no q behind the end.
-  auto cut = [&]() {
-    const int q2 = (t.steps - 1) * kStepQ * KG * 2;
-    if constexpr (!TR) {
+  // Ahead of the copies at from_step: into the next item behind the last stage
+  // (`ahead`; else to nothing), and no q behind the end at the last.
+  auto advance = [&](bool ahead) {
+    if (from_step == from.steps) enter(ahead ? from_item + G : total);
+    if (from_step == from.steps - 1) {
+      const int q2 = from_step * kStepQ * KG * 2;
+      if constexpr (!TR) {
 #pragma unroll
-      for (int j = 0; j < NR; j++) {
-        const int id = j * S::kWaves + wave;
-        if (q2 + id / TileR::kCopies * 128 + TileR::copy_byte(id % TileR::kCopies, lane) >= t.Q * 2) offR[j] = kOutside;
+        for (int j = 0; j < 2 * NH; j++) {
+          const int id = j % NH * S::kWaves + wave;
+          if (q2 + id / HalfR::kCopies * 128 + HalfR::copy_byte(id % HalfR::kCopies, lane) >= from.Q * 2) offR[j] = kOutside;
+        }
+      }
+      if constexpr (!TC) {
+#pragma unroll
+        for (int j = 0; j < NC; j++) {
+          const int id = j * S::kWaves + wave;
+          if (q2 + id / TileC::kCopies * 128 + TileC::copy_byte(id % TileC::kCopies, lane) >= from.Q * 2) offC[j] = kOutside;
+        }
       }
     }
-    if constexpr (!TC) {
-#pragma unroll
-      for (int j = 0; j < NC; j++) {
-        const int id = j * S::kWaves + wave;
-        if (q2 + id / TileC::kCopies * 128 + TileC::copy_byte(id % TileC::kCopies, lane) >= t.Q * 2) offC[j] = kOutside;
-      }
-    }
   };
-  auto copy = [&](int step) {
-    if (step == t.steps - 1) cut();
-    const Source from = source(step);
-    repeat<NR + NC>([&](auto j) { copy_one(from, j); });
-  };
+  // The copies of the first stages of an item, and the wait for the first one's.
   auto start = [&](int item) {
-    locate(item);
-    if (t.steps == 0) return;
-    copy(0);
-    copy(1);
+    enter(item);
+#pragma unroll
+    for (int slot = 0; slot < S::kStages; slot++) {
+      advance(KG == 1);
+      const Source s = source(slot);
+      repeat<NALL>([&](auto j) { copy_one(s, j); });
+      from_step++;
+    }
+    wait_but<(S::kStages - 1) * NALL>();
+    barrier_nofence();
   };
 
-  const int G = gridDim.x;
   int item = xcd_order(blockIdx.x, G);
   if (item >= total) return;
   start(item);
-  for (;;) {
+  int slot = 0;   // of the stage that is multiplied
+  for (; item < total; item += G) {
+    const Tile d = decode(item);
     f32x4 acc[CB][MB];
 #pragma unroll
     for (int c = 0; c < CB; c++)
@@ -283,87 +325,98 @@ linear_tile_kernel(moe_host::LinearArgs g) {
     float colsum[MB];   // grad w: sums of dy over the rows, the bias's gradient
 #pragma unroll
     for (int m = 0; m < MB; m++) colsum[m] = 0.0f;
-    const bool with_bias = SUM && t.tc == 0 && wc == 0;
+    const bool with_bias = SUM && d.tc == 0 && wc == 0;
 
-    // The stages.  A phase multiplies CB blocks of c by MP blocks of m for 32 q,
-    // and between its multiplications reads the fragments of the next phase.  The
-    // last phase of a stage first meets the other waves: the next stage has come
-    // then, and this one, read to its end, takes the copies of the one after,
-    // issued between the multiplications too.  (Behind the last stage the same
-    // code copies and reads nothing of use: one loop, whose accumulators stay in
-    // their registers.)  MA: blocks of m that have rows.
+    // The stages.  A phase multiplies the blocks of c by up to half of the wave's
+    // blocks of m for 32 q, and between its multiplications reads the next phase's
+    // fragments and issues copies.  The order: first half of m, both 32 q; second
+    // half, both 32 q.  At the second phase the waves meet: c and the first half
+    // of m are read to the end, and take the copies of the stage kStages on; the
+    // second half has come.  At the last phase they meet again: the second half
+    // is free, and the next stage's c and first half have come.  So every copy has
+    // one and a half stages' time at two stages.  A tile without a second half
+    // meets once.  (The reads ahead of an item's end are the next one's first,
+    // read again there: one loop, whose accumulators stay in their registers.)
+    // MA: blocks of m that have rows.
+    constexpr bool SPLIT = OP == kForward && KG == 1 && MB > 4;
+    constexpr auto q_of = [](int ph, int phases) { return phases == 2 ? ph : SPLIT ? ph % 2 : ph / 2; };
+    constexpr auto m_of = [](int ph, int phases) { return phases == 2 ? 0 : SPLIT ? ph / 2 : ph % 2; };
     auto stages = [&](auto blocks) {
-      constexpr int MA = blocks, MP = MA > 4 ? MA / 2 : MA, MH = MA / MP, PHASES = 2 * MH;
-      u32x4 fa[2][CB], fb[2][MP];
+      constexpr int MA = blocks, M0 = MB <= 4 || MA <= MB / 2 ? MA : MB / 2, M1 = MA - M0, PHASES = M1 ? 4 : 2;
+      u32x4 fa[2][CB], fb[2][M0];
       const uint32_t sub = lds0 + kg * S::kSub;
-      const uint32_t placeR = sub + TileR::lane_place(wm, lane);
+      const uint32_t placeR = sub + HalfR::lane_place(wm, lane);
       const uint32_t placeC = sub + BM * 128 + TileC::lane_place(wc * CB, lane);
       uint32_t atR, atC;
-      auto turn = [&](int step) {   // the places in the stage of `step`
-        const uint32_t stage = (step % S::kStages) * S::kStage;
-        atR = placeR + stage;
-        atC = placeC + stage;
+      auto turn = [&]() {   // the places in the stage at `slot`
+        atR = placeR + slot * S::kStage;
+        atC = placeC + slot * S::kStage;
         __asm__ volatile("" : "+v"(atR), "+v"(atC));   // two registers, and not one for every block
       };
       // fragment r of the reads ahead of phase ph: the first of m, those of c, the others of m
       auto read_one = [&](auto phase, auto at) {
-        constexpr int ph = phase, h = ph / MH, mh = ph % MH, r = at, nc = mh == 0 ? CB : 0;
+        constexpr int ph = phase, h = q_of(ph, PHASES), mh = m_of(ph, PHASES), r = at, nc = mh == 0 ? CB : 0;
         if constexpr (r == 0 || r > nc) {
-          constexpr int m = r == 0 ? 0 : r - nc;
-          fb[ph % 2][m] = TileR::fragment(atR, (mh * MP + m) * WM, h);
+          constexpr int m = (r == 0 ? 0 : r - nc) + (mh == 0 ? 0 : M0), half = m / (MB / 2), in_half = m % (MB / 2);
+          fb[ph % 2][r == 0 ? 0 : r - nc] = HalfR::fragment(atR + half * (BM / 2 * 128), in_half * WM, h);
         } else {
           fa[h][r - 1] = TileC::fragment(atC, r - 1, h);
         }
       };
-      turn(0);
-      repeat<MP + CB>([&](auto r) { read_one(std::integral_constant<int, 0>{}, r); });
-      for (int step = 0; step < t.steps; step++) {
-        if (step + 3 == t.steps) cut();
+      turn();
+      repeat<M0 + CB>([&](auto r) { read_one(std::integral_constant<int, 0>{}, r); });
+      for (int step = 0; step < d.steps; step++) {
+        advance(KG == 1);
+        Source s;
         repeat<PHASES>([&](auto phase) {
-          constexpr int ph = phase, h = ph / MH, mh = ph % MH, next = (ph + 1) % PHASES;
-          constexpr bool last = ph == PHASES - 1;
-          constexpr int reads = MP + (next % MH == 0 ? CB : 0), extra = reads + (last ? NR + NC : 0), mults = MP * CB;
-          Source from;
-          if constexpr (last) {
-            wait_all();
+          constexpr int ph = phase, next = (ph + 1) % PHASES, h = q_of(ph, PHASES), mh = m_of(ph, PHASES);
+          constexpr int first_m = mh == 0 ? 0 : M0, M = mh == 0 ? M0 : M1;
+          constexpr bool last = ph == PHASES - 1, once = !SPLIT || PHASES == 2, meet = last || (!once && ph == 1);
+          constexpr int reads = (m_of(next, PHASES) == 0 ? M0 + CB : M1), mults = M * CB;
+          constexpr int copies = !meet ? 0 : once ? NALL : last ? NH : NA, first_copy = !once && last ? NA : 0;
+          constexpr int extra = reads + copies;
+          if constexpr (meet) {
+            wait_but<once ? (S::kStages - 2) * NALL + (SPLIT ? NH : 0) : (S::kStages - 1) * NALL>();
             barrier_nofence();
-            turn(step + 1);
-            from = source(step + 2);
+          }
+          if constexpr (meet && (once || !last)) s = source(slot);
+          if constexpr (last) {
+            slot = slot == S::kStages - 1 ? 0 : slot + 1;
+            turn();
+            from_step++;
           }
           __builtin_amdgcn_sched_barrier(0);
           // as many of them after each multiplication as it takes, none behind the last one
           constexpr int each = (extra + mults - 1) / mults;
           repeat<mults>([&](auto at) {
             constexpr int i = at, m = i / CB, c = i % CB;
-            acc[c][mh * MP + m] = Elem::mfma(fa[h][c], fb[ph % 2][m], acc[c][mh * MP + m]);
+            acc[c][first_m + m] = Elem::mfma(fa[h][c], fb[ph % 2][m], acc[c][first_m + m]);
             repeat<each>([&](auto x) {
               constexpr int k = i * each + x;
               if constexpr (k < reads) read_one(std::integral_constant<int, next>{}, std::integral_constant<int, k>{});
-              else if constexpr (k < extra) copy_one(from, std::integral_constant<int, k - reads>{});
+              else if constexpr (k < extra) copy_one(s, std::integral_constant<int, first_copy + k - reads>{});
             });
             __builtin_amdgcn_sched_barrier(0);
           });
           if constexpr (SUM) {
             if (with_bias) {
 #pragma unroll
-              for (int m = 0; m < MP; m++) {
+              for (int m = 0; m < M; m++) {
                 float v[8];
                 Row::unpack(fb[ph % 2][m], v);
 #pragma unroll
-                for (int i = 0; i < 8; i++) colsum[mh * MP + m] += v[i];
+                for (int i = 0; i < 8; i++) colsum[first_m + m] += v[i];
               }
             }
           }
         });
       }
     };
-    if (t.steps > 0) {
-      wait_vm<NR + NC>();   // the first stage's copies; the second's may be on their way
-      barrier_nofence();
+    if (d.steps > 0) {
       if constexpr (OP == kGradW) {
         stages(std::integral_constant<int, MB>{});
       } else {
-        const int active = (t.rows - t.m0 + 16 * WM - 1) / (16 * WM);
+        const int active = (d.rows - d.m0 + 16 * WM - 1) / (16 * WM);
         if (MB >= 2 && active <= MB / 4) stages(std::integral_constant<int, (MB >= 4 ? MB / 4 : 1)>{});
         else if (MB >= 2 && active <= MB / 2) stages(std::integral_constant<int, (MB >= 2 ? MB / 2 : 1)>{});
         else if (MB >= 8 && active <= MB / 4 * 3) stages(std::integral_constant<int, (MB >= 8 ? MB / 4 * 3 : 1)>{});
@@ -399,14 +452,11 @@ linear_tile_kernel(moe_host::LinearArgs g) {
         }
       }
       __syncthreads();
+      start(item + G);   // the stages are the copies' again
+      slot = 0;
     }
 
-    // --- the next item's first copies, then this one's epilogue
-    const Tile d = t;
-    item += G;
-    const bool more = item < total;
-    if (more) start(item);
-
+    // --- epilogue
     // A lane has row lane % 16 of every block of m, and of two blocks of c (pair_blocks)
     // the eight values from `place` on.
     const int lm = lane & 15, place = 8 * (lane >> 5) + 16 * ((lane >> 4) & 1);
@@ -551,7 +601,6 @@ linear_tile_kernel(moe_host::LinearArgs g) {
         }
       }
     }
-    if (!more) break;
   }
 }
 
