@@ -3,13 +3,21 @@
 
 namespace moe {
 
-typedef LinearShape<256, 256, 2, 4, 1, 2> Tile128;
+typedef LinearShape<256, 256, 2, 4, 1, 2> Tile256;
+typedef LinearShape<128, 128, 2, 2, 1, 2> Tile128;
+
+template <typename Elem, typename S>
+static hipError_t grad_w(const moe_host::LinearArgs& a, int cus, hipStream_t s) {
+  const long items = (long)a.E * ((a.N + S::BM - 1) / S::BM) * ((a.K + S::BC - 1) / S::BC);
+  return a.dbias ? launch_linear_tile<Elem, kGradW, S, true>(a, items, cus, s)
+                 : launch_linear_tile<Elem, kGradW, S, false>(a, items, cus, s);
+}
 
 template <typename Elem>
 static hipError_t grad_w(const moe_host::LinearArgs& a, int cus, hipStream_t s) {
-  const long items = (long)a.E * ((a.N + 255) / 256) * ((a.K + 255) / 256);
-  return a.dbias ? launch_linear_tile<Elem, kGradW, Tile128, true>(a, items, cus, s)
-                 : launch_linear_tile<Elem, kGradW, Tile128, false>(a, items, cus, s);
+  auto blocks = [](long n, long size) { return (n + size - 1) / size; };
+  const long large = a.E * blocks(a.N, 256) * blocks(a.K, 256), small = a.E * blocks(a.N, 128) * blocks(a.K, 128);
+  return blocks(large, cus) * 1.6 <= blocks(small, 2 * cus) ? grad_w<Elem, Tile256>(a, cus, s) : grad_w<Elem, Tile128>(a, cus, s);
 }
 
 }  // namespace moe

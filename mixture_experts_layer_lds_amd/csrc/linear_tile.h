@@ -123,6 +123,52 @@ __device__ __forceinline__ void pair_blocks(const f32x4& a, const f32x4& b, floa
   }
 }
 
+// The forward product's epilogue on eight neighbouring sums of a row, from
+// column n of expert e's N on: bias, z, activation, residual, the one rounding.
+template <typename Elem>
+__device__ __forceinline__ void add8(const void* p, size_t at, float (&v)[8]) {
+  typedef typename Elem::Row Row;
+  float b[8];
+  row_load<Row>(static_cast<const typename Row::elem*>(p) + at, b);
+#pragma unroll
+  for (int i = 0; i < 8; i++) v[i] += b[i];
+}
+template <typename Elem>
+__device__ __forceinline__ void store8(void* p, size_t at, const float (&v)[8]) {
+  typedef typename Elem::Row Row;
+  row_store<Row>(static_cast<typename Row::elem*>(p) + at, v);
+}
+template <typename Elem>
+__device__ __forceinline__ void forward_out(const moe_host::LinearArgs& g, int e, size_t row, int n, float (&v)[8]) {
+  const size_t o = row * g.N + n;
+  if (g.bias) add8<Elem>(g.bias, (size_t)e * g.N + n, v);
+  if (g.z_out) store8<Elem>(g.z_out, o, v);
+  if (g.act != MOE_ACT_NONE) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] = activate(v[i], g.act);
+  }
+  if (g.residual) add8<Elem>(g.residual, o, v);
+  store8<Elem>(g.out, o, v);
+}
+// SwiGLU: gate and up sums of output column n.
+template <typename Elem>
+__device__ __forceinline__ void forward_out(const moe_host::LinearArgs& g, int e, size_t row, int n, float (&gate)[8], float (&up)[8]) {
+  const int M = g.N / 2;
+  if (g.bias) {
+    add8<Elem>(g.bias, (size_t)e * g.N + n, gate);
+    add8<Elem>(g.bias, (size_t)e * g.N + M + n, up);
+  }
+  if (g.z_out) {
+    store8<Elem>(g.z_out, row * g.N + n, gate);
+    store8<Elem>(g.z_out, row * g.N + M + n, up);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i++) up[i] *= silu(gate[i]);
+  const size_t o = row * M + n;
+  if (g.residual) add8<Elem>(g.residual, o, up);
+  store8<Elem>(g.out, o, up);
+}
+
 // SUM: grad w with the bias's gradient.
 template <typename Elem, LinearOp OP, typename S, bool SUM>
 __global__ void __launch_bounds__(S::kThreads, S::kWavesASimd)
@@ -417,10 +463,9 @@ linear_tile_kernel(moe_host::LinearArgs g) {
         stages(std::integral_constant<int, MB>{});
       } else {
         const int active = (d.rows - d.m0 + 16 * WM - 1) / (16 * WM);
-        if (MB >= 2 && active <= MB / 4) stages(std::integral_constant<int, (MB >= 4 ? MB / 4 : 1)>{});
-        else if (MB >= 2 && active <= MB / 2) stages(std::integral_constant<int, (MB >= 2 ? MB / 2 : 1)>{});
-        else if (MB >= 8 && active <= MB / 4 * 3) stages(std::integral_constant<int, (MB >= 8 ? MB / 4 * 3 : 1)>{});
-        else stages(std::integral_constant<int, MB>{});
+        repeat<MB>([&](auto i) {
+          if (active == i + 1) stages(std::integral_constant<int, i + 1>{});
+        });
       }
     }
 
@@ -461,7 +506,6 @@ linear_tile_kernel(moe_host::LinearArgs g) {
     // the eight values from `place` on.
     const int lm = lane & 15, place = 8 * (lane >> 5) + 16 * ((lane >> 4) & 1);
     auto load8 = [](const void* p, size_t at, float (&v)[8]) { row_load<Row>(static_cast<const elem*>(p) + at, v); };
-    auto store8 = [](void* p, size_t at, const float (&v)[8]) { row_store<Row>(static_cast<elem*>(p) + at, v); };
     if (kg == 0) {
 #pragma unroll
       for (int m = 0; m < MB; m++) {
@@ -488,12 +532,9 @@ linear_tile_kernel(moe_host::LinearArgs g) {
               if (r >= N || k >= K) continue;
               const size_t at = ((size_t)d.e * N + r) * K + k;
               if (g.accumulate) {
-                float b[8];
-                load8(g.out, at, b);
-#pragma unroll
-                for (int i = 0; i < 8; i++) v[i] += b[i];
+                add8<Elem>(g.out, at, v);
               }
-              store8(g.out, at, v);
+              store8<Elem>(g.out, at, v);
             }
           }
           if (SUM && with_bias) {
@@ -518,34 +559,12 @@ linear_tile_kernel(moe_host::LinearArgs g) {
               // blocks of gate and up values in turn: two of each give eight columns
 #pragma unroll
               for (int c = 0; c + 3 < CB; c += 4) {
-                float gate[8], up[8], y[8];
+                float gate[8], up[8];
                 pair_blocks(acc[c][m], acc[c + 2][m], gate);
                 pair_blocks(acc[c + 1][m], acc[c + 3][m], up);
                 const int n = d.c0 + (wc * CB + c) * 8 + place;
                 if (r >= d.rows || n >= width_c) continue;
-                if (g.bias) {
-                  float b[8];
-                  load8(g.bias, (size_t)d.e * N + n, b);
-#pragma unroll
-                  for (int i = 0; i < 8; i++) gate[i] += b[i];
-                  load8(g.bias, (size_t)d.e * N + width_c + n, b);
-#pragma unroll
-                  for (int i = 0; i < 8; i++) up[i] += b[i];
-                }
-                if (g.z_out) {
-                  store8(g.z_out, row * N + n, gate);
-                  store8(g.z_out, row * N + width_c + n, up);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; i++) y[i] = silu(gate[i]) * up[i];
-                const size_t o = row * width_c + n;
-                if (g.residual) {
-                  float b[8];
-                  load8(g.residual, o, b);
-#pragma unroll
-                  for (int i = 0; i < 8; i++) y[i] += b[i];
-                }
-                store8(g.out, o, y);
+                forward_out<Elem>(g, d.e, row, n, gate, up);
               }
               continue;
             }
@@ -558,24 +577,7 @@ linear_tile_kernel(moe_host::LinearArgs g) {
             if (r >= d.rows || n >= width_c) continue;
             const size_t o = row * width_c + n;
             if constexpr (OP == kForward) {
-              if (g.bias) {
-                float b[8];
-                load8(g.bias, (size_t)d.e * N + n, b);
-#pragma unroll
-                for (int i = 0; i < 8; i++) v[i] += b[i];
-              }
-              if (g.z_out) store8(g.z_out, o, v);
-              if (g.act != MOE_ACT_NONE) {
-#pragma unroll
-                for (int i = 0; i < 8; i++) v[i] = activate(v[i], g.act);
-              }
-              if (g.residual) {
-                float b[8];
-                load8(g.residual, o, b);
-#pragma unroll
-                for (int i = 0; i < 8; i++) v[i] += b[i];
-              }
-              store8(g.out, o, v);
+              forward_out<Elem>(g, d.e, row, n, v);
             } else if (g.act == MOE_ACT_SWIGLU) {
               const size_t oz = row * 2 * width_c + n;
               float gate[8], up[8];
@@ -586,8 +588,8 @@ linear_tile_kernel(moe_host::LinearArgs g) {
                 y[i] = v[i] * silu(gate[i]);
                 v[i] = v[i] * up[i] * silu_slope(gate[i]);
               }
-              store8(g.out, oz, v);
-              store8(g.out, oz + width_c, y);
+              store8<Elem>(g.out, oz, v);
+              store8<Elem>(g.out, oz + width_c, y);
             } else {
               if (g.act != MOE_ACT_NONE) {
                 float z[8];
@@ -595,7 +597,7 @@ linear_tile_kernel(moe_host::LinearArgs g) {
 #pragma unroll
                 for (int i = 0; i < 8; i++) v[i] *= act_slope(z[i], g.act);
               }
-              store8(g.out, o, v);
+              store8<Elem>(g.out, o, v);
             }
           }
         }

@@ -495,6 +495,8 @@ struct LinearArgs {
   bool out_fp32, accumulate;      // grad w
 };
 hipError_t launch_linear(const LinearArgs& a, int row_type, int cus, hipStream_t s);
+// ... of few rows per expert: items of 16 nb weight rows by 16 mb rows (linear_stream.hip)
+hipError_t launch_linear_stream(const LinearArgs& a, int row_type, int nb, int mb, int cus, hipStream_t s);
 hipError_t launch_linear_grad_x(const LinearArgs& a, int row_type, int cus, hipStream_t s);
 hipError_t launch_linear_grad_w(const LinearArgs& a, int row_type, int cus, hipStream_t s);
 // dz = dy act'(z): dy and dz rows of M values (SwiGLU: z and dz of 2 M).
