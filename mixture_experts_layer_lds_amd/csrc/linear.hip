@@ -33,7 +33,9 @@ static hipError_t forward(const moe_host::LinearArgs& a, int cus, hipStream_t s)
 }
 
 template <typename Elem>
-static hipError_t grad_x(const moe_host::LinearArgs& a, int cus, hipStream_t s) {
+static hipError_t grad_x(moe_host::LinearArgs a, int cus, hipStream_t s) {
+  const size_t z = a.act == MOE_ACT_NONE ? 1 : a.act == MOE_ACT_SWIGLU ? 4 : 2;   // dx, and z as wide
+  a.stream_out = past_caches(2 * ((size_t)a.rows * (a.N + z * a.K) + (size_t)a.E * a.N * a.K));
   if (large_tiles(a, a.K, cus))
     return launch_linear_tile<Elem, kGradX, Tile256>(a, max_tiles(a, 256) * blocks(a.K, 256), cus, s);
   return launch_linear_tile<Elem, kGradX, Tile128>(a, max_tiles(a, 128) * blocks(a.K, 128), cus, s);

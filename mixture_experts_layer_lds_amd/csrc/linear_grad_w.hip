@@ -14,7 +14,8 @@ static hipError_t grad_w(const moe_host::LinearArgs& a, int cus, hipStream_t s) 
 }
 
 template <typename Elem>
-static hipError_t grad_w(const moe_host::LinearArgs& a, int cus, hipStream_t s) {
+static hipError_t grad_w(moe_host::LinearArgs a, int cus, hipStream_t s) {
+  a.stream_out = past_caches(2 * (size_t)a.rows * (a.N + a.K) + (size_t)a.E * a.N * a.K * (a.out_fp32 ? 4 : 2));
   auto blocks = [](long n, long size) { return (n + size - 1) / size; };
   const long large = a.E * blocks(a.N, 256) * blocks(a.K, 256), small = a.E * blocks(a.N, 128) * blocks(a.K, 128);
   return blocks(large, cus) * 1.6 <= blocks(small, 2 * cus) ? grad_w<Elem, Tile256>(a, cus, s) : grad_w<Elem, Tile128>(a, cus, s);

@@ -13,6 +13,7 @@
 namespace moe {
 
 constexpr int kStreamWaves = 4;
+constexpr int kStepQ = 64;   // q of a chunk: 128 bytes a row
 
 template <int NB_, int MB_, int NS_>
 struct StreamShape {

@@ -493,6 +493,7 @@ struct LinearArgs {
   int rows, E, N, K;              // rows: T * k, or the plain rows
   int act;                        // moe_act_t
   bool out_fp32, accumulate;      // grad w
+  bool stream_out;                // outputs that no cache holds: stores past the caches
 };
 hipError_t launch_linear(const LinearArgs& a, int row_type, int cus, hipStream_t s);
 // ... of few rows per expert: items of 16 nb weight rows by 16 mb rows (linear_stream.hip)
