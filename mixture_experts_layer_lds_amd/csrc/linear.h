@@ -76,7 +76,7 @@ __device__ __forceinline__ void range_dma16(__amdgpu_buffer_rsrc_t r, uint32_t o
 //
 // TRANS true: QS rows (q) of TILE values; block b (16 values, 32 bytes) of row
 // q at place b ^ f(q), f the row's two low bits and its bit 3 (64 values: its
-// bits 1 and 3), so that the eight rows which half a wave reads at once stand
+// bits 1 and 3; 32: bit 3), so that the eight rows which half a wave reads at once stand
 // in different banks.  A fragment is two ds_read_b64_tr_b16: 16 lanes read four
 // rows of a block and get four q of their own column each.
 template <bool TRANS, int TILE, int QS = 64>
@@ -88,7 +88,7 @@ struct OperandTile {
   static constexpr int kRowsACopy = 1024 / kPitch;
 
   static __device__ __forceinline__ int swizzle(int q) {
-    return TILE >= 128 ? (q & 3) | ((q >> 3) & 1) << 2 : ((q >> 1) & 1) | ((q >> 3) & 1) << 1;
+    return TILE >= 128 ? (q & 3) | ((q >> 3) & 1) << 2 : TILE == 64 ? ((q >> 1) & 1) | ((q >> 3) & 1) << 1 : (q >> 3) & 1;
   }
   // The row of the tile that a lane of copy i takes, and its byte in that row.
   static __device__ __forceinline__ int copy_row(int i, int lane) { return i * kRowsACopy + lane / (kPitch / 16); }

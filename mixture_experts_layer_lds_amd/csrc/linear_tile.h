@@ -677,4 +677,60 @@ static inline long max_tiles(const moe_host::LinearArgs& a, int BM) {
   return a.expert_offsets ? a.rows / BM + (a.rows < a.E ? a.rows : a.E) : (a.rows + BM - 1) / BM;
 }
 
+static inline long blocks(long n, long size) { return (n + size - 1) / size; }
+
+// Experts that have rows at most, and the rows of one were they spread evenly.
+static inline int used_groups(const moe_host::LinearArgs& a) {
+  return !a.expert_offsets ? 1 : a.rows < a.E ? a.rows : a.E;
+}
+static inline int mean_rows(const moe_host::LinearArgs& a) {
+  return a.expert_offsets ? (int)blocks(a.rows, a.E) : a.rows;
+}
+
+// The four shapes, and how long one takes for `groups` products of m x c over q:
+// the rounds of its items over the chip, times an item's stages and what it has
+// besides.  Measured, us a stage with every CU at work and us an item besides:
+//                               stage of          stage   besides
+//   Tile256  256 x 256          64 q              1.75    3.5
+//   Tile128  128 x 128, two a CU  64 q              1.08    2.5
+//   Pair64   64 x 64, two a CU    2 x 64 q          1.4     3
+//   Quad64   64 x 64            4 x 64 q          2.0     2.3
+// The large tiles do most work a round, the small ones fill the chip where the
+// product is small.  us by shape in that order, the rule's choice by *:
+//   forward     8192 x 4096 x 2048 (rows, N, K)     105*  125   -     -
+//               2048 x 2048 x 1024                  29    15.6* 22.7  35.9
+//               4096 x 512 x 1024                   26.9  13.7  13.6* 19.0
+//               256 x 4096 x 7168                   131   81    44    37*
+//   gradient of the matrices, 8192 x 1024 x 512     207   116   56    47*
+struct ShapeCost {
+  int BM, BC, q, occupancy;
+  float stage, besides;
+  float of(long groups, long m, long c, long q_len, int cus) const {
+    const long rounds = blocks(groups * blocks(m, BM) * blocks(c, BC), (long)cus * occupancy);
+    return rounds * (blocks(q_len, q) * stage + besides);
+  }
+};
+constexpr ShapeCost kShapeCosts[] = {
+    {256, 256, 64, 1, 1.75f, 3.5f}, {128, 128, 64, 2, 1.08f, 2.5f}, {64, 64, 128, 2, 1.4f, 3.0f}, {64, 64, 256, 1, 2.0f, 2.3f}};
+typedef LinearShape<256, 256, 2, 4, 1, 2> Tile256;
+typedef LinearShape<128, 128, 2, 2, 1, 2> Tile128;
+typedef LinearShape<64, 64, 2, 1, 2, 2> Pair64;
+typedef LinearShape<64, 64, 2, 1, 4, 2> Quad64;
+static_assert(Tile256::kOccupancy == 1 && Tile128::kOccupancy == 2 && Pair64::kOccupancy == 2 && Quad64::kOccupancy == 1,
+              "the workgroups of a CU that the costs are of");
+
+// f(shape) with the shape that takes least.
+template <typename F>
+static hipError_t with_shape(long groups, long m, long c, long q, int cus, F&& f) {
+  int best = 0;
+  for (int i = 1; i < 4; i++)
+    if (kShapeCosts[i].of(groups, m, c, q, cus) < kShapeCosts[best].of(groups, m, c, q, cus)) best = i;
+  switch (best) {
+    case 0: return f(Tile256{});
+    case 1: return f(Tile128{});
+    case 2: return f(Pair64{});
+    default: return f(Quad64{});
+  }
+}
+
 }  // namespace moe
