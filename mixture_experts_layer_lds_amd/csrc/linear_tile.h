@@ -486,31 +486,32 @@ linear_tile_kernel(moe_host::LinearArgs g) {
       }
     }
 
-    // --- the groups' sums, in ascending order
+    // --- the groups' sums, in ascending order, of blocks m in group m % KG
     if constexpr (KG > 1) {
       wait_all();
       barrier_nofence();   // no copy is on its way, the stages are free
       f32x4* const part = reinterpret_cast<f32x4*>(lds);
-      float* const part_sum = reinterpret_cast<float*>(lds + (KG - 1) * WM * WC * CB * MB * 1024);
+      float* const part_sum = reinterpret_cast<float*>(lds + S::kWaves * CB * MB * 1024);
       const int w = wave % (WM * WC);
-      static_assert((KG - 1) * WM * WC * MB * (CB * 1024 + 256) <= S::kStage * S::kStages, "partial sums fit");
-      if (kg > 0) {
+      static_assert(S::kWaves * MB * (CB * 1024 + 256) <= S::kStage * S::kStages, "partial sums fit");
 #pragma unroll
-        for (int c = 0; c < CB; c++)
+      for (int m = 0; m < MB; m++) {
 #pragma unroll
-          for (int m = 0; m < MB; m++) part[((((kg - 1) * WM * WC + w) * CB + c) * MB + m) * 64 + lane] = acc[c][m];
-#pragma unroll
-        for (int m = 0; m < MB; m++) part_sum[(((kg - 1) * WM * WC + w) * MB + m) * 64 + lane] = colsum[m];
+        for (int c = 0; c < CB; c++) part[((wave * CB + c) * MB + m) * 64 + lane] = acc[c][m];
+        if (SUM) part_sum[(wave * MB + m) * 64 + lane] = colsum[m];
       }
       __syncthreads();
-      if (kg == 0) {
-        for (int k = 0; k < KG - 1; k++) {
 #pragma unroll
-          for (int c = 0; c < CB; c++)
+      for (int m = 0; m < MB; m++) {
+        if (m % KG != kg) continue;
 #pragma unroll
-            for (int m = 0; m < MB; m++) acc[c][m] += part[(((k * WM * WC + w) * CB + c) * MB + m) * 64 + lane];
+        for (int c = 0; c < CB; c++) acc[c][m] = part[((w * CB + c) * MB + m) * 64 + lane];
+        if (SUM) colsum[m] = part_sum[(w * MB + m) * 64 + lane];
+        for (int k = 1; k < KG; k++) {
+          const int other = k * WM * WC + w;
 #pragma unroll
-          for (int m = 0; m < MB; m++) colsum[m] += part_sum[((k * WM * WC + w) * MB + m) * 64 + lane];
+          for (int c = 0; c < CB; c++) acc[c][m] += part[((other * CB + c) * MB + m) * 64 + lane];
+          if (SUM) colsum[m] += part_sum[(other * MB + m) * 64 + lane];
         }
       }
       __syncthreads();
@@ -524,131 +525,130 @@ linear_tile_kernel(moe_host::LinearArgs g) {
     char* const scratch = lds + S::kLds - (S::kWaves - wave) * S::kScratch;
     const int lm = lane & 15, place = 8 * (lane >> 5) + 16 * ((lane >> 4) & 1);
     auto load8 = [](const void* p, size_t at, float (&v)[8]) { row_load<Row>(static_cast<const elem*>(p) + at, v); };
-    if (kg == 0) {
 #pragma unroll
-      for (int m = 0; m < MB; m++) {
-        const int r = d.m0 + (m * WM + wm) * 16 + lm;
-        if constexpr (OP == kGradW) {
-          // 16 rows of 128 bytes at a time, through LDS, so that eight lanes store a
-          // whole line; piece p (16 bytes) of a row at place p ^ (row % 8)
-          auto line_out = [&](int c1) {   // from column c1 of the wave's on
+    for (int m = 0; m < MB; m++) {
+      if (KG > 1 && m % KG != kg) continue;
+      const int r = d.m0 + (m * WM + wm) * 16 + lm;
+      if constexpr (OP == kGradW) {
+        // 16 rows of 128 bytes at a time, through LDS, so that eight lanes store a
+        // whole line; piece p (16 bytes) of a row at place p ^ (row % 8)
+        auto line_out = [&](int c1) {   // from column c1 of the wave's on
 #pragma unroll
-            for (int part = 0; part < 2; part++) {
-              const int row = 8 * part + (lane >> 3), n = d.m0 + (m * WM + wm) * 16 + row;
-              u32x4 q = *reinterpret_cast<const u32x4*>(scratch + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
-              const int k = d.c0 + wc * CB * 16 + c1 + (lane & 7) * (g.out_fp32 ? 4 : 8);
-              if (n >= N || k >= K) continue;
-              const size_t at = ((size_t)d.e * N + n) * K + k;
-              u32x4* const to = reinterpret_cast<u32x4*>(static_cast<char*>(g.out) + at * (g.out_fp32 ? 4 : 2));
-              if (g.accumulate) q = __builtin_bit_cast(u32x4, *reinterpret_cast<const f32x4*>(to) + __builtin_bit_cast(f32x4, q));
-              store_line(to, q, g.stream_out);
-            }
-          };
-          if (g.out_fp32) {
-#pragma unroll
-            for (int c = 0; c < CB; c += 2) {
-#pragma unroll
-              for (int i = 0; i < 2; i++)
-                *reinterpret_cast<f32x4*>(scratch + lm * 128 + (((4 * i + (lane >> 4)) ^ (lm & 7)) << 4)) = acc[c + i][m];
-              line_out(c * 16);
-            }
-          } else if (!g.accumulate) {
-#pragma unroll
-            for (int c = 0; c < CB; c += 4) {
-#pragma unroll
-              for (int i = 0; i < 4; i++) {
-                const float v[4] = {acc[c + i][m][0], acc[c + i][m][1], acc[c + i][m][2], acc[c + i][m][3]};
-                *reinterpret_cast<u32x2*>(scratch + lm * 128 + (((2 * i + (lane >> 5)) ^ (lm & 7)) << 4) + 8 * ((lane >> 4) & 1)) = Elem::pack4(v);
-              }
-              line_out(c * 16);
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < CB; c += 2) {
-              float v[8];
-              pair_blocks(acc[c][m], acc[c + 1][m], v);
-              const int k = d.c0 + (wc * CB + c) * 16 + place;
-              if (r >= N || k >= K) continue;
-              const size_t at = ((size_t)d.e * N + r) * K + k;
-              add8<Elem>(g.out, at, v);
-              store8<Elem>(g.out, at, v);
-            }
+          for (int part = 0; part < 2; part++) {
+            const int row = 8 * part + (lane >> 3), n = d.m0 + (m * WM + wm) * 16 + row;
+            u32x4 q = *reinterpret_cast<const u32x4*>(scratch + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+            const int k = d.c0 + wc * CB * 16 + c1 + (lane & 7) * (g.out_fp32 ? 4 : 8);
+            if (n >= N || k >= K) continue;
+            const size_t at = ((size_t)d.e * N + n) * K + k;
+            u32x4* const to = reinterpret_cast<u32x4*>(static_cast<char*>(g.out) + at * (g.out_fp32 ? 4 : 2));
+            if (g.accumulate) q = __builtin_bit_cast(u32x4, *reinterpret_cast<const f32x4*>(to) + __builtin_bit_cast(f32x4, q));
+            store_line(to, q, g.stream_out);
           }
-          if (SUM && with_bias) {
-            float s = colsum[m];
-            s += __shfl_xor(s, 16, 64);
-            s += __shfl_xor(s, 32, 64);
-            if (lane < 16 && r < N) {
-              const size_t at = (size_t)d.e * N + r;
-              if (g.out_fp32) {
-                float* const p = static_cast<float*>(g.dbias) + at;
-                *p = g.accumulate ? *p + s : s;
-              } else {
-                elem* const p = static_cast<elem*>(g.dbias) + at;
-                *p = Elem::round(g.accumulate ? Elem::widen(*p) + s : s);
-              }
-            }
+        };
+        if (g.out_fp32) {
+#pragma unroll
+          for (int c = 0; c < CB; c += 2) {
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+              *reinterpret_cast<f32x4*>(scratch + lm * 128 + (((4 * i + (lane >> 4)) ^ (lm & 7)) << 4)) = acc[c + i][m];
+            line_out(c * 16);
           }
-        } else if constexpr (OP == kForward) {
-          const size_t row = (size_t)d.begin + r;
-          if (gated) {
-            // blocks of gate and up values in turn: two of each give eight columns
+        } else if (!g.accumulate) {
 #pragma unroll
-            for (int c = 0; c + 3 < CB; c += 4) {
-              float gate[8], up[8];
-              pair_blocks(acc[c][m], acc[c + 2][m], gate);
-              pair_blocks(acc[c + 1][m], acc[c + 3][m], up);
-              const int n = d.c0 + (wc * CB + c) * 8 + place;
-              if (r < d.rows && n < width_c) forward_out<Elem>(g, d.e, row, n, gate, up);
-            }
-          } else {
+          for (int c = 0; c < CB; c += 4) {
 #pragma unroll
-            for (int c = 0; c < CB; c += 2) {
-              float v[8];
-              pair_blocks(acc[c][m], acc[c + 1][m], v);
-              const int n = d.c0 + (wc * CB + c) * 16 + place;
-              if (r < d.rows && n < width_c) forward_out<Elem>(g, d.e, row, n, v);
+            for (int i = 0; i < 4; i++) {
+              const float v[4] = {acc[c + i][m][0], acc[c + i][m][1], acc[c + i][m][2], acc[c + i][m][3]};
+              *reinterpret_cast<u32x2*>(scratch + lm * 128 + (((2 * i + (lane >> 5)) ^ (lm & 7)) << 4) + 8 * ((lane >> 4) & 1)) = Elem::pack4(v);
             }
+            line_out(c * 16);
           }
         } else {
-          // eight rows of 64 values at a time, through LDS, so that eight lanes have a row
-          // (a line of the output); the pieces of 16 bytes change places by 2 (row % 8)
-          static_assert(CB == 4, "a wave's columns are 64");
 #pragma unroll
-          for (int half = 0; half < 2; half++) {
-            if ((lm >> 3) == half) {
-#pragma unroll
-              for (int c = 0; c < CB; c++)
-                *reinterpret_cast<f32x4*>(scratch + (lm & 7) * 256 + (((4 * c + (lane >> 4)) ^ (2 * (lm & 7))) << 4)) = acc[c][m];
-            }
-            const int r8 = lane >> 3, rh = d.m0 + (m * WM + wm) * 16 + 8 * half + r8;
-            const int n = d.c0 + wc * CB * 16 + 8 * (lane & 7);
-            const char* const from_row = scratch + r8 * 256 + (((2 * (lane & 7)) ^ (2 * r8)) << 4);
-            const f32x4 v0 = *reinterpret_cast<const f32x4*>(from_row), v1 = *reinterpret_cast<const f32x4*>(from_row + 16);
-            if (rh >= d.rows || n >= width_c) continue;
-            float v[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]}, y[8];
-            const size_t row = (size_t)d.begin + rh, o = row * width_c + n;
-            if (g.act == MOE_ACT_SWIGLU) {
-              const size_t oz = row * 2 * width_c + n;
-              float gate[8], up[8];
-              load8(g.z_in, oz, gate);
-              load8(g.z_in, oz + width_c, up);
-#pragma unroll
-              for (int i = 0; i < 8; i++) {
-                y[i] = v[i] * silu(gate[i]);
-                v[i] = v[i] * up[i] * silu_slope(gate[i]);
-              }
-              store8<Elem>(g.out, oz, v, g.stream_out);
-              store8<Elem>(g.out, oz + width_c, y, g.stream_out);
+          for (int c = 0; c < CB; c += 2) {
+            float v[8];
+            pair_blocks(acc[c][m], acc[c + 1][m], v);
+            const int k = d.c0 + (wc * CB + c) * 16 + place;
+            if (r >= N || k >= K) continue;
+            const size_t at = ((size_t)d.e * N + r) * K + k;
+            add8<Elem>(g.out, at, v);
+            store8<Elem>(g.out, at, v);
+          }
+        }
+        if (SUM && with_bias) {
+          float s = colsum[m];
+          s += __shfl_xor(s, 16, 64);
+          s += __shfl_xor(s, 32, 64);
+          if (lane < 16 && r < N) {
+            const size_t at = (size_t)d.e * N + r;
+            if (g.out_fp32) {
+              float* const p = static_cast<float*>(g.dbias) + at;
+              *p = g.accumulate ? *p + s : s;
             } else {
-              if (g.act != MOE_ACT_NONE) {
-                float z[8];
-                load8(g.z_in, o, z);
-#pragma unroll
-                for (int i = 0; i < 8; i++) v[i] *= act_slope(z[i], g.act);
-              }
-              store8<Elem>(g.out, o, v, g.stream_out);
+              elem* const p = static_cast<elem*>(g.dbias) + at;
+              *p = Elem::round(g.accumulate ? Elem::widen(*p) + s : s);
             }
+          }
+        }
+      } else if constexpr (OP == kForward) {
+        const size_t row = (size_t)d.begin + r;
+        if (gated) {
+          // blocks of gate and up values in turn: two of each give eight columns
+#pragma unroll
+          for (int c = 0; c + 3 < CB; c += 4) {
+            float gate[8], up[8];
+            pair_blocks(acc[c][m], acc[c + 2][m], gate);
+            pair_blocks(acc[c + 1][m], acc[c + 3][m], up);
+            const int n = d.c0 + (wc * CB + c) * 8 + place;
+            if (r < d.rows && n < width_c) forward_out<Elem>(g, d.e, row, n, gate, up);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < CB; c += 2) {
+            float v[8];
+            pair_blocks(acc[c][m], acc[c + 1][m], v);
+            const int n = d.c0 + (wc * CB + c) * 16 + place;
+            if (r < d.rows && n < width_c) forward_out<Elem>(g, d.e, row, n, v);
+          }
+        }
+      } else {
+        // eight rows of 64 values at a time, through LDS, so that eight lanes have a row
+        // (a line of the output); the pieces of 16 bytes change places by 2 (row % 8)
+        static_assert(CB == 4, "a wave's columns are 64");
+#pragma unroll
+        for (int half = 0; half < 2; half++) {
+          if ((lm >> 3) == half) {
+#pragma unroll
+            for (int c = 0; c < CB; c++)
+              *reinterpret_cast<f32x4*>(scratch + (lm & 7) * 256 + (((4 * c + (lane >> 4)) ^ (2 * (lm & 7))) << 4)) = acc[c][m];
+          }
+          const int r8 = lane >> 3, rh = d.m0 + (m * WM + wm) * 16 + 8 * half + r8;
+          const int n = d.c0 + wc * CB * 16 + 8 * (lane & 7);
+          const char* const from_row = scratch + r8 * 256 + (((2 * (lane & 7)) ^ (2 * r8)) << 4);
+          const f32x4 v0 = *reinterpret_cast<const f32x4*>(from_row), v1 = *reinterpret_cast<const f32x4*>(from_row + 16);
+          if (rh >= d.rows || n >= width_c) continue;
+          float v[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]}, y[8];
+          const size_t row = (size_t)d.begin + rh, o = row * width_c + n;
+          if (g.act == MOE_ACT_SWIGLU) {
+            const size_t oz = row * 2 * width_c + n;
+            float gate[8], up[8];
+            load8(g.z_in, oz, gate);
+            load8(g.z_in, oz + width_c, up);
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+              y[i] = v[i] * silu(gate[i]);
+              v[i] = v[i] * up[i] * silu_slope(gate[i]);
+            }
+            store8<Elem>(g.out, oz, v, g.stream_out);
+            store8<Elem>(g.out, oz + width_c, y, g.stream_out);
+          } else {
+            if (g.act != MOE_ACT_NONE) {
+              float z[8];
+              load8(g.z_in, o, z);
+#pragma unroll
+              for (int i = 0; i < 8; i++) v[i] *= act_slope(z[i], g.act);
+            }
+            store8<Elem>(g.out, o, v, g.stream_out);
           }
         }
       }
