@@ -58,7 +58,9 @@ struct ElemFp16 {
   static __device__ __forceinline__ float widen(_Float16 v) { return (float)v; }
 };
 
-constexpr uint32_t kOutside = 0xfffffff0u;       // a buffer offset that is out of every range: the copy writes zeros
+// A buffer offset that is out of every range (they end at 2^31) and stays so with the
+// stage's added: the copy writes zeros.
+constexpr uint32_t kOutside = 0x80000000u;
 
 // A buffer of `bytes` from base: copies from behind it write zeros.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t range_rsrc(const char* base, uint32_t bytes) {

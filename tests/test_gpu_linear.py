@@ -375,26 +375,38 @@ def test_layer_of_own_experts(lib, dtype):
     # row on any path (xs is exact), each by half a step of the norm through maps of bounded gain;
     # 32 half steps cover paths that add and slopes above one
     leaves = [v.double().requires_grad_() for v in (x, tw, W1, b1, W2, S1, S2)]
-    xd, wd, A1, c1, A2, B1, B2 = leaves
     T, H = x.shape
     token = torch.arange(T, device="cuda").repeat_interleave(k)
     rows = torch.zeros(T * k, dtype=torch.long, device="cuda")
     rows[pos.cuda()] = torch.arange(T * k, device="cuda")   # the pair of every sorted row
-    xs = xd[token[rows]]
-    ys = []
-    for e, a, b in ref.spans(off):
-        gate, up = (xs[a:b] @ A1[e].t() + c1[e]).chunk(2, 1)
-        ys.append((gate * torch.sigmoid(gate) * up) @ A2[e].t())
-    y = torch.cat(ys) * wd.flatten()[rows[:n]][:, None]
-    v = xd @ B1.t()
-    out = torch.zeros(T, H, dtype=torch.float64, device="cuda").index_add(0, token[rows[:n]], y) + (v * ref.cdf(v)) @ B2.t()
+
+    def forward(xd, wd, A1, c1, A2, B1, B2):
+        xs, ys = xd[token[rows]], []
+        for e, a, b in ref.spans(off):
+            gate, up = (xs[a:b] @ A1[e].t() + c1[e]).chunk(2, 1)
+            ys.append((gate * torch.sigmoid(gate) * up) @ A2[e].t())
+        y = torch.cat(ys) * wd.flatten()[rows[:n]][:, None]
+        v = xd @ B1.t()
+        return torch.zeros(T, H, dtype=torch.float64, device="cuda").index_add(0, token[rows[:n]], y) + (v * ref.cdf(v)) @ B2.t()
+
+    out = forward(*leaves)
     out.backward(dout.double())
     got = (t["dx"].double() + t["dxsh"].double(), t["dw"], t["dW1"], t["db1"], t["dW2"], t["dS1"], t["dS2"])
     out = out.detach()
-    assert float((t["out"].double() - out).norm() / out.norm()) < 32 * ref.half_step(dtype)
+    bound = 32 * ref.half_step(dtype)
+    assert float((t["out"].double() - out).norm() / out.norm()) < bound
+    # and central differences of the whole along a direction of each leaf, h small against the
+    # leaf and large against 64 bits: h^2 times a third derivative is far below the bound
+    g = gen(77)
     for name, a, leaf in zip(("x", "w", "W1", "b1", "W2", "S1", "S2"), got, leaves):
         rel = float((a.double() - leaf.grad).norm() / leaf.grad.norm())
-        assert rel < 32 * ref.half_step(dtype), (name, rel)
+        assert rel < bound, (name, rel)
+        d = torch.randn(leaf.shape, generator=g, device="cuda", dtype=torch.float64)
+        h = 1e-5
+        with torch.no_grad():
+            ends = [float((forward(*[v + s * h * d if v is leaf else v for v in leaves]) * dout.double()).sum()) for s in (1, -1)]
+        slope = (ends[0] - ends[1]) / (2 * h)
+        assert abs(float((a.double() * d).sum()) - slope) < bound * float(leaf.grad.norm() * d.norm()), name
 
 
 def test_layer_in_a_graph(lib):
