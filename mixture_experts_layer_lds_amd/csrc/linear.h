@@ -70,23 +70,24 @@ __device__ __forceinline__ void range_dma16(__amdgpu_buffer_rsrc_t r, uint32_t o
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 16, off, soff, 0, 0);
 }
 
-// One operand's tile in LDS: TILE values of m or c by QS of q, 64 or, transposed, 32.
+constexpr int kStepQ = 64;   // q of a sub-step, and of a chunk of the streamed weights: 128 bytes
+
+// One operand's tile in LDS: TILE values of m or c by kStepQ of q.
 //
 // TRANS false: TILE rows of 128 bytes, piece p (16 bytes) of row r at place
 // p ^ (r % 8).  A copy instruction takes 8 rows.  A fragment (row lane % 16,
 // piece lane / 16 of the 64-byte half) is one ds_read_b128.
 //
-// TRANS true: QS rows (q) of TILE values; block b (16 values, 32 bytes) of row
+// TRANS true: 64 rows (q) of TILE values; block b (16 values, 32 bytes) of row
 // q at place b ^ f(q), f the row's two low bits and its bit 3 (64 values: its
 // bits 1 and 3; 32: bit 3), so that the eight rows which half a wave reads at once stand
 // in different banks.  A fragment is two ds_read_b64_tr_b16: 16 lanes read four
 // rows of a block and get four q of their own column each.
-template <bool TRANS, int TILE, int QS = 64>
+template <bool TRANS, int TILE>
 struct OperandTile {
-  static_assert(QS == 64 || (TRANS && QS == 32), "rows of 64 q are 128 bytes");
-  static constexpr int kBytes = TILE * QS * 2;
+  static constexpr int kBytes = TILE * kStepQ * 2;
   static constexpr int kCopies = kBytes / 1024;                    // wave instructions
-  static constexpr int kPitch = TRANS ? TILE * 2 : QS * 2;     // bytes a row
+  static constexpr int kPitch = TRANS ? TILE * 2 : kStepQ * 2;     // bytes a row
   static constexpr int kRowsACopy = 1024 / kPitch;
 
   static __device__ __forceinline__ int swizzle(int q) {
@@ -126,12 +127,12 @@ struct OperandTile {
 
 // A tile of BM by BC, WM by WC waves, KG groups of them that take the
 // sub-steps of a stage in turn and add their sums at the end; NS stages in LDS.
-template <int BM_, int BC_, int WM_, int WC_, int KG_, int NS_, int QS_ = 64>
+template <int BM_, int BC_, int WM_, int WC_, int KG_, int NS_>
 struct LinearShape {
-  static constexpr int BM = BM_, BC = BC_, WM = WM_, WC = WC_, KG = KG_, kStages = NS_, QS = QS_;
+  static constexpr int BM = BM_, BC = BC_, WM = WM_, WC = WC_, KG = KG_, kStages = NS_;
   static constexpr int kWaves = WM * WC * KG, kThreads = kWaves * 64;
   static constexpr int MB = BM / WM / 16, CB = BC / WC / 16;   // 16 x 16 blocks of a wave
-  static constexpr int kSub = (BM + BC) * QS * 2;          // bytes of a sub-step
+  static constexpr int kSub = (BM + BC) * kStepQ * 2;          // bytes of a sub-step
   static constexpr int kStage = kSub * KG;
   static constexpr int kRanges = 3 * 4 * (kMaxExperts + 1);    // first item and rows of every expert
   static constexpr int kScratch = 2048;                        // of a wave: 16 rows of 128 bytes

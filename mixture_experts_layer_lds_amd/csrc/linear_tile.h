@@ -7,13 +7,26 @@
 //    are renumbered so that an XCD takes a run of them.
 //  * A stage is KG sub-steps of 64 q of both operands, copied straight to LDS
 //    while the stages before are multiplied, on from item to item without a
-//    pause.  Rows behind an expert's last,
+//    pause (8192 x 4096 x 2048 forward 133 -> 112 us, with the fragments' reads
+//    and the copies between the multiplications).  Rows behind an expert's last,
 //    and q behind the end, are outside the copy's buffer range and come as zeros.
 //  * An expert's rows are cut into tiles of nearly equal height, and the blocks
 //    of 16 rows go to the waves in turn, so that a tile of few rows costs few
 //    multiplications on every wave.
 //  * Sums are fp32; bias, activation, residual and the one rounding happen on
 //    the accumulators.
+//
+// Measured (us; TFLOP/s): 8192^3 forward 880 (1250), gradient of the rows 901
+// (1220), of the matrices 1012 (1086); torch's library products of the same in
+// one session 840, 957 and 1086.  SQ_LDS_BANK_CONFLICT is 0 in all three.  The
+// matrix units are busy half of the cycles at the 2.0 GHz that the card then runs
+// at.  Copies of the kernel without the copies ran the first in 784 us, without the
+// LDS reads in 826, without both in 645.  Few rows an expert are bound by the
+// weights' way from HBM: 32 experts of 256 rows, 7168 x 2048, take 297 us forward
+// (3.2 TB/s of weights), 221 where all experts share one matrix: a stage's copies
+// are late by more than the stage and a half that LDS can hold ahead.  Loads ahead
+// of them into L2 made it slower (358 us: they share the CU's address path), and so
+// did other orders of q by column (306).
 #pragma once
 
 #include <type_traits>
@@ -23,9 +36,6 @@
 namespace moe {
 
 constexpr int kXcds = 8;
-
-typedef std::integral_constant<bool, true> Yes;
-typedef std::integral_constant<bool, false> No;
 
 // f(0), f(1) .. f(N - 1), each number a constant of its own type.
 template <int N, int I = 0, typename F>
@@ -188,10 +198,10 @@ linear_tile_kernel(moe_host::LinearArgs g) {
   typedef typename Elem::Row Row;
   typedef typename Row::elem elem;
   constexpr bool TR = OP == kGradW, TC = OP != kForward;
-  constexpr int BM = S::BM, BC = S::BC, KG = S::KG, WM = S::WM, WC = S::WC, MB = S::MB, CB = S::CB, QS = S::QS;
+  constexpr int BM = S::BM, BC = S::BC, KG = S::KG, WM = S::WM, WC = S::WC, MB = S::MB, CB = S::CB;
   // the operand of m in two halves, that of c in one piece, in this order in a sub-step
-  typedef OperandTile<TR, BM / 2, QS> HalfR;
-  typedef OperandTile<TC, BC, QS> TileC;
+  typedef OperandTile<TR, BM / 2> HalfR;
+  typedef OperandTile<TC, BC> TileC;
   static_assert(KG * HalfR::kCopies % S::kWaves == 0 && KG * TileC::kCopies % S::kWaves == 0, "whole copies a wave");
   constexpr int NH = KG * HalfR::kCopies / S::kWaves, NC = KG * TileC::kCopies / S::kWaves;   // copies of a wave
   constexpr int NA = NC + NH, NALL = NC + 2 * NH;
@@ -240,7 +250,7 @@ linear_tile_kernel(moe_host::LinearArgs g) {
     t.begin = begin;
     t.rows = OP == kGradW ? N : min(rows, t.m0 + height);
     t.Q = OP == kForward ? K : OP == kGradX ? N : rows;
-    t.steps = (t.Q + QS * KG - 1) / (QS * KG);
+    t.steps = (t.Q + kStepQ * KG - 1) / (kStepQ * KG);
     return t;
   };
 
@@ -291,13 +301,13 @@ linear_tile_kernel(moe_host::LinearArgs g) {
 #pragma unroll
     for (int j = 0; j < 2 * NH; j++) {
       const int id = j % NH * S::kWaves + wave, sub = id / HalfR::kCopies, i = id % HalfR::kCopies, half = j / NH * (BM / 2);
-      const int row = HalfR::copy_row(i, lane) + (TR ? sub * QS : half);
+      const int row = HalfR::copy_row(i, lane) + (TR ? sub * kStepQ : half);
       offR[j] = (uint32_t)(row * ldR) + HalfR::copy_byte(i, lane) + (TR ? half * 2 : sub * 128);
     }
 #pragma unroll
     for (int j = 0; j < NC; j++) {
       const int id = j * S::kWaves + wave, sub = id / TileC::kCopies, i = id % TileC::kCopies;
-      const int row = TC ? TileC::copy_row(i, lane) + sub * QS : weight_row(TileC::copy_row(i, lane));
+      const int row = TC ? TileC::copy_row(i, lane) + sub * kStepQ : weight_row(TileC::copy_row(i, lane));
       offC[j] = (uint32_t)(row * ldC) + TileC::copy_byte(i, lane) + (TC ? 0 : sub * 128);
     }
   };
@@ -310,7 +320,7 @@ linear_tile_kernel(moe_host::LinearArgs g) {
   };
   auto source = [&](int slot) {
     Source s;
-    const int q0 = from_step * QS * KG, left = min(from.Q - q0, QS * KG);
+    const int q0 = from_step * kStepQ * KG, left = min(from.Q - q0, kStepQ * KG);
     const bool any = left > 0;
     // an operand that is contiguous in q moves along its rows; the other's range moves over them
     const char* const r = TR ? baseR + (size_t)q0 * ldR : baseR;
@@ -327,10 +337,10 @@ linear_tile_kernel(moe_host::LinearArgs g) {
     constexpr int j = at, r = j - NC;
     if constexpr (j < NC) {
       const int id = j * S::kWaves + wave, sub = id / TileC::kCopies, i = id % TileC::kCopies;
-      range_dma16(s.c, offC[j], TC ? 0 : s.q2, s.stage + sub * S::kSub + BM * QS * 2 + i * 1024);
+      range_dma16(s.c, offC[j], TC ? 0 : s.q2, s.stage + sub * S::kSub + BM * kStepQ * 2 + i * 1024);
     } else {
       const int id = r % NH * S::kWaves + wave, sub = id / HalfR::kCopies, i = id % HalfR::kCopies;
-      range_dma16(s.r, offR[r], TR ? 0 : s.q2, s.stage + sub * S::kSub + r / NH * (BM * QS) + i * 1024);
+      range_dma16(s.r, offR[r], TR ? 0 : s.q2, s.stage + sub * S::kSub + r / NH * (BM * kStepQ) + i * 1024);
     }
   };
   // Ahead of the copies at from_step: into the next item behind the last stage
@@ -338,7 +348,7 @@ linear_tile_kernel(moe_host::LinearArgs g) {
   auto advance = [&](bool ahead) {
     if (from_step == from.steps) enter(ahead ? from_item + G : total);
     if (from_step == from.steps - 1) {
-      const int q2 = from_step * QS * KG * 2;
+      const int q2 = from_step * kStepQ * KG * 2;
       if constexpr (!TR) {
 #pragma unroll
         for (int j = 0; j < 2 * NH; j++) {
@@ -392,19 +402,22 @@ linear_tile_kernel(moe_host::LinearArgs g) {
     // of m are read to the end, and take the copies of the stage kStages on; the
     // second half has come.  At the last phase they meet again: the second half
     // is free, and the next stage's c and first half have come.  So every copy has
-    // one and a half stages' time at two stages.  A tile without a second half
-    // meets once.  (The reads ahead of an item's end are the next one's first,
+    // one and a half stages' time at two stages (the ragged 32 experts 380 -> 353 us).
+    // A tile without a second half meets once, and so do the gradients (first q of
+    // both halves, then the second): with a transposed operand's reads, two for one,
+    // the first two phases are short of LDS (8192^3 gradient of the matrices 1142 us
+    // in the forward's order, 1061 in theirs).  (The reads ahead of an item's end are the next one's first,
     // read again there: one loop, whose accumulators stay in their registers.)
     // MA: blocks of m that have rows.
     constexpr bool SPLIT = OP == kForward && KG == 1 && MB > 4;
-    constexpr auto q_of = [](int ph, int phases) { return phases == QS / 32 ? ph : SPLIT ? ph % 2 : ph / 2; };
-    constexpr auto m_of = [](int ph, int phases) { return phases == QS / 32 ? 0 : SPLIT ? ph / 2 : ph % 2; };
+    constexpr auto q_of = [](int ph, int phases) { return phases == 2 ? ph : SPLIT ? ph % 2 : ph / 2; };
+    constexpr auto m_of = [](int ph, int phases) { return phases == 2 ? 0 : SPLIT ? ph / 2 : ph % 2; };
     auto stages = [&](auto blocks) {
-      constexpr int MA = blocks, M0 = MB <= 4 || MA <= MB / 2 ? MA : MB / 2, M1 = MA - M0, PHASES = QS / 32 * (M1 ? 2 : 1);
+      constexpr int MA = blocks, M0 = MB <= 4 || MA <= MB / 2 ? MA : MB / 2, M1 = MA - M0, PHASES = M1 ? 4 : 2;
       u32x4 fa[2][CB], fb[2][M0];
       const uint32_t sub = lds0 + kg * S::kSub;
       const uint32_t placeR = sub + HalfR::lane_place(wm, lane);
-      const uint32_t placeC = sub + BM * QS * 2 + TileC::lane_place(wc * CB, lane);
+      const uint32_t placeC = sub + BM * kStepQ * 2 + TileC::lane_place(wc * CB, lane);
       uint32_t atR, atC;
       auto turn = [&]() {   // the places in the stage at `slot`
         atR = placeR + slot * S::kStage;
@@ -412,18 +425,17 @@ linear_tile_kernel(moe_host::LinearArgs g) {
         __asm__ volatile("" : "+v"(atR), "+v"(atC));   // two registers, and not one for every block
       };
       // fragment r of the reads ahead of phase ph: the first of m, those of c, the others of m
-      auto read_one = [&](auto phase, auto at, auto ahead) {
+      auto read_one = [&](auto phase, auto at) {
         constexpr int ph = phase, h = q_of(ph, PHASES), mh = m_of(ph, PHASES), r = at, nc = mh == 0 ? CB : 0;
         if constexpr (r == 0 || r > nc) {
           constexpr int m = (r == 0 ? 0 : r - nc) + (mh == 0 ? 0 : M0), half = m / (MB / 2), in_half = m % (MB / 2);
-          fb[ph % 2][r == 0 ? 0 : r - nc] = HalfR::fragment(atR + half * (BM * QS), in_half * WM, h);
+          fb[ph % 2][r == 0 ? 0 : r - nc] = HalfR::fragment(atR + half * (BM * kStepQ), in_half * WM, h);
         } else {
-          // at 32 q the next stage's are read while this one's of the same q are multiplied
-          fa[QS == 32 && ahead() ? 1 : h][r - 1] = TileC::fragment(atC, r - 1, h);
+          fa[h][r - 1] = TileC::fragment(atC, r - 1, h);
         }
       };
       turn();
-      repeat<M0 + CB>([&](auto r) { read_one(std::integral_constant<int, 0>{}, r, No{}); });
+      repeat<M0 + CB>([&](auto r) { read_one(std::integral_constant<int, 0>{}, r); });
       for (int step = 0; step < d.steps; step++) {
         advance(KG == 1);
         Source s;
@@ -452,7 +464,7 @@ linear_tile_kernel(moe_host::LinearArgs g) {
             acc[c][first_m + m] = Elem::mfma(fa[h][c], fb[ph % 2][m], acc[c][first_m + m]);
             repeat<each>([&](auto x) {
               constexpr int k = i * each + x;
-              if constexpr (k < reads) read_one(std::integral_constant<int, next>{}, std::integral_constant<int, k>{}, std::integral_constant<bool, last>{});
+              if constexpr (k < reads) read_one(std::integral_constant<int, next>{}, std::integral_constant<int, k>{});
               else if constexpr (k < extra) copy_one(s, std::integral_constant<int, first_copy + k - reads>{});
             });
             __builtin_amdgcn_sched_barrier(0);
@@ -467,10 +479,6 @@ linear_tile_kernel(moe_host::LinearArgs g) {
                 for (int i = 0; i < 8; i++) colsum[first_m + m] += v[i];
               }
             }
-          }
-          if constexpr (QS == 32 && last) {
-#pragma unroll
-            for (int c = 0; c < CB; c++) fa[0][c] = fa[1][c];
           }
         });
       }
