@@ -601,10 +601,11 @@ int moe_router_topk_grad(const float *logits, const int32_t *topk_ids, const flo
  *
  * Rows behind the last valid one take no part and are not written.  An Inf or
  * NaN in a row stays in that row's outputs (in the gradient of w: in its
- * expert's); SiLU and GELU of -Inf are NaN.  The order of every sum depends on
- * the sizes and on the expert's number of rows alone, so results repeat bit for
- * bit.  rows == 0 (T == 0) returns MOE_OK with no launch, but for the gradient
- * of w, which then is 0 (accumulate: unchanged).
+ * expert's); SiLU and GELU of -Inf are NaN, and so are their slopes at both
+ * infinities.  The order of every sum depends on the sizes and on the expert's
+ * number of rows alone, so results repeat bit for bit.  rows == 0 (T == 0)
+ * returns MOE_OK with no launch, but for the gradient of w, which then is 0
+ * (accumulate: unchanged).
  * Requires N and K (M) positive multiples of 8, at most 65536, N * K at most
  * 2^30; SWIGLU in the forward call N a multiple of 16, in the gradient of x K at
  * most 32768, in the gradient of the activation M at most 32768; 1 <= k <= 16,

@@ -16,9 +16,9 @@
 //  * Sums are fp32; bias, activation, residual and the one rounding happen on
 //    the accumulators.
 //
-// Measured (us; TFLOP/s): 8192^3 forward 880 (1250), gradient of the rows 901
-// (1220), of the matrices 1012 (1086); torch's library products of the same in
-// one session 840, 957 and 1086.  SQ_LDS_BANK_CONFLICT is 0 in all three.  The
+// Measured (us; TFLOP/s), one session: 8192^3 forward 910 (1208), gradient of the
+// rows 826 (1330), of the matrices 892 (1233); torch's library products of the same
+// 814, 971 and 1086.  SQ_LDS_BANK_CONFLICT is 0 in all three.  The
 // matrix units are busy half of the cycles at the 2.0 GHz that the card then runs
 // at.  Copies of the kernel without the copies ran the first in 784 us, without the
 // LDS reads in 826, without both in 645.  Few rows an expert are bound by the
@@ -661,7 +661,7 @@ linear_tile_kernel(moe_host::LinearArgs g) {
         }
       }
     }
-  }
+  }  wait_all();   // no copy may reach LDS that is another workgroup's by then
 }
 
 // Whether what a call reads and writes is more than the 256 MiB that the last

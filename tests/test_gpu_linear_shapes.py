@@ -119,6 +119,33 @@ def test_outputs_past_the_caches(lib):
     grad_w(lib, gen(5), routing, k, off, T * k, E, N, K, dtype, dtype)
 
 
+def test_most_rows(lib):
+    """2^24 plain rows, and 65536 sorted ones of 511 experts."""
+    dtype, rows = torch.bfloat16, 1 << 24
+    g = gen(6)
+    x, w = normal(g, rows, 8), normal(g, 16, 8)
+    y = lib.moe_linear(x, w, act="swiglu")
+    at = torch.tensor([0, 1, 4095, rows // 2, rows - 65, rows - 1], device="cuda")
+    want, ez = ref.product(x[at], w[None], [0, len(at)])
+    v, ev = ref.value(want, ez, "swiglu")
+    ref.within(y[at], v, ev + ref.rounding(v, dtype), "y")
+    dx = lib.moe_linear_grad_x(y, w[:8].contiguous())
+    want, e = ref.product(y[at], w[:8].t()[None], [0, len(at)])
+    ref.within(dx[at], want, e + ref.rounding(want, dtype), "dx")
+    dw, db = lib.moe_linear_grad_w(y, x, want_bias=True, dtype=torch.float32)
+    want, ew, wantb, eb = ref.outer(y, x, [0, rows], 1)
+    ref.within(dw, want[0], ew[0] + ref.rounding(want[0], torch.float32), "dw")
+    ref.within(db, wantb[0], eb[0] + ref.rounding(wantb[0], torch.float32), "dbias")
+    with pytest.raises(lib.MoeError) as err:
+        lib.moe_act_grad(torch.empty(rows + 1, 8, dtype=dtype, device="cuda"), torch.empty(rows + 1, 8, dtype=dtype, device="cuda"), "silu")
+    assert err.value.status == -2
+    T, k, E, N, K = 4096, 16, 511, 136, 72
+    routing, off = grouping(lib, T, k, E, 9, 0.01)
+    forward(lib, gen(7), routing, k, off, T * k, E, N, K, "gelu", dtype)
+    grad_x(lib, gen(8), routing, k, off, T * k, E, N, K, "silu", dtype)
+    grad_w(lib, gen(9), routing, k, off, T * k, E, N, K, dtype, dtype)
+
+
 def test_back_to_back_calls(lib):
     """Calls of different shapes one after another on one stream, none waited for: each result is
     that of the call alone."""
