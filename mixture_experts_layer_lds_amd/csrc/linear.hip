@@ -6,7 +6,7 @@ namespace moe {
 
 template <typename Elem>
 static hipError_t forward(const moe_host::LinearArgs& a, int cus, hipStream_t s) {
-  return with_shape(used_groups(a), mean_rows(a), a.N, a.K, cus, [&](auto shape) {
+  return with_shape(used_groups(a), mean_rows(a), a.expert_offsets != nullptr, a.N, a.K, cus, [&](auto shape) {
     typedef decltype(shape) S;
     const long tiles_c = a.act == MOE_ACT_SWIGLU ? blocks(a.N / 2, S::BC / 2) : blocks(a.N, S::BC);
     return launch_linear_tile<Elem, kForward, S>(a, max_tiles(a, S::BM) * tiles_c, cus, s);

@@ -188,7 +188,8 @@ linear_stream_kernel(moe_host::LinearArgs g) {
         forward_out<Elem>(g, d.e, (size_t)d.begin + row, n, v);
       }
     }
-  }  wait_all();   // no copy may reach LDS that is another workgroup's by then
+  }
+  wait_all();   // no copy may reach LDS that is another workgroup's by then
 }
 
 template <typename Elem, typename S>

@@ -29,6 +29,8 @@
 // did other orders of q by column (306).
 #pragma once
 
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "linear.h"
@@ -189,6 +191,35 @@ __device__ __forceinline__ void forward_out(const moe_host::LinearArgs& g, int e
   const size_t o = row * M + n;
   if (g.residual) add8<Elem>(g.residual, o, up);
   store8<Elem>(g.out, o, up);
+}
+
+// The epilogue of the gradient of the rows on eight sums of a row, from column k on.
+template <typename Elem>
+__device__ __forceinline__ void grad_x_out(const moe_host::LinearArgs& g, size_t row, int k, float (&v)[8]) {
+  typedef typename Elem::Row Row;
+  const typename Row::elem* const z = static_cast<const typename Row::elem*>(g.z_in);
+  const size_t o = row * g.K + k;
+  if (g.act == MOE_ACT_SWIGLU) {
+    const size_t oz = 2 * row * g.K + k;
+    float gate[8], up[8], y[8];
+    row_load<Row>(z + oz, gate);
+    row_load<Row>(z + oz + g.K, up);
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      y[i] = v[i] * silu(gate[i]);
+      v[i] = v[i] * up[i] * silu_slope(gate[i]);
+    }
+    store8<Elem>(g.out, oz, v, g.stream_out);
+    store8<Elem>(g.out, oz + g.K, y, g.stream_out);
+    return;
+  }
+  if (g.act != MOE_ACT_NONE) {
+    float at[8];
+    row_load<Row>(z + o, at);
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] *= act_slope(at[i], g.act);
+  }
+  store8<Elem>(g.out, o, v, g.stream_out);
 }
 
 // SUM: grad w with the bias's gradient.
@@ -532,7 +563,6 @@ linear_tile_kernel(moe_host::LinearArgs g) {
     // the eight values from `place` on.
     char* const scratch = lds + S::kLds - (S::kWaves - wave) * S::kScratch;
     const int lm = lane & 15, place = 8 * (lane >> 5) + 16 * ((lane >> 4) & 1);
-    auto load8 = [](const void* p, size_t at, float (&v)[8]) { row_load<Row>(static_cast<const elem*>(p) + at, v); };
 #pragma unroll
     for (int m = 0; m < MB; m++) {
       if (KG > 1 && m % KG != kg) continue;
@@ -635,33 +665,13 @@ linear_tile_kernel(moe_host::LinearArgs g) {
           const char* const from_row = scratch + r8 * 256 + (((2 * (lane & 7)) ^ (2 * r8)) << 4);
           const f32x4 v0 = *reinterpret_cast<const f32x4*>(from_row), v1 = *reinterpret_cast<const f32x4*>(from_row + 16);
           if (rh >= d.rows || n >= width_c) continue;
-          float v[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]}, y[8];
-          const size_t row = (size_t)d.begin + rh, o = row * width_c + n;
-          if (g.act == MOE_ACT_SWIGLU) {
-            const size_t oz = row * 2 * width_c + n;
-            float gate[8], up[8];
-            load8(g.z_in, oz, gate);
-            load8(g.z_in, oz + width_c, up);
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-              y[i] = v[i] * silu(gate[i]);
-              v[i] = v[i] * up[i] * silu_slope(gate[i]);
-            }
-            store8<Elem>(g.out, oz, v, g.stream_out);
-            store8<Elem>(g.out, oz + width_c, y, g.stream_out);
-          } else {
-            if (g.act != MOE_ACT_NONE) {
-              float z[8];
-              load8(g.z_in, o, z);
-#pragma unroll
-              for (int i = 0; i < 8; i++) v[i] *= act_slope(z[i], g.act);
-            }
-            store8<Elem>(g.out, o, v, g.stream_out);
-          }
+          float v[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
+          grad_x_out<Elem>(g, (size_t)d.begin + rh, n, v);
         }
       }
     }
-  }  wait_all();   // no copy may reach LDS that is another workgroup's by then
+  }
+  wait_all();   // no copy may reach LDS that is another workgroup's by then
 }
 
 // Whether what a call reads and writes is more than the 256 MiB that the last
@@ -703,6 +713,10 @@ static inline int mean_rows(const moe_host::LinearArgs& a) {
 //   Tile128  128 x 128, two a CU  64 q              1.08    2.5
 //   Pair64   64 x 64, two a CU    2 x 64 q          1.4     3
 //   Quad64   64 x 64            4 x 64 q          2.0     2.3
+// A tile of few rows takes 0.4 of a full one and more by its rows.  Rows of experts
+// spread: m is their mean, its root the deviation, and the tiles are the expected
+// number (64 experts of 100 rows, 4096 -> 1024: one of them with more than 128 is a
+// second round of Tile128, 171 us, and none of Tile256, 128).
 // The large tiles do most work a round, the small ones fill the chip where the
 // product is small.  us by shape in that order, the rule's choice by *:
 //   forward     8192 x 4096 x 2048 (rows, N, K)     105*  125   -     -
@@ -712,14 +726,21 @@ static inline int mean_rows(const moe_host::LinearArgs& a) {
 //   gradient of the matrices, 8192 x 1024 x 512     207   116   56    47*
 struct ShapeCost {
   int BM, BC, q, occupancy;
-  float stage, besides;
-  float of(long groups, long m, long c, long q_len, int cus) const {
-    const long rounds = blocks(groups * blocks(m, BM) * blocks(c, BC), (long)cus * occupancy);
-    return rounds * (blocks(q_len, q) * stage + besides);
+  double stage, besides;
+  double of(long groups, long m, bool spread, long c, long q_len, int cus) const {
+    double tiles = (double)blocks(m, BM);
+    if (spread) {
+      const double deviation = std::sqrt((double)m);
+      tiles = 1.0;
+      for (long at = BM; at < m + 4 * deviation; at += BM) tiles += 0.5 * std::erfc((at - m) / (deviation * 1.41421356));
+    }
+    const double fill = std::min(1.0, m / (tiles * BM));
+    const double rounds = std::ceil(groups * tiles * blocks(c, BC) / ((double)cus * occupancy));
+    return rounds * (blocks(q_len, q) * stage * (0.4 + 0.6 * fill) + besides);
   }
 };
 constexpr ShapeCost kShapeCosts[] = {
-    {256, 256, 64, 1, 1.75f, 3.5f}, {128, 128, 64, 2, 1.08f, 2.5f}, {64, 64, 128, 2, 1.4f, 3.0f}, {64, 64, 256, 1, 2.0f, 2.3f}};
+    {256, 256, 64, 1, 1.75, 3.5}, {128, 128, 64, 2, 1.08, 2.5}, {64, 64, 128, 2, 1.4, 3.0}, {64, 64, 256, 1, 2.0, 2.3}};
 typedef LinearShape<256, 256, 2, 4, 1, 2> Tile256;
 typedef LinearShape<128, 128, 2, 2, 1, 2> Tile128;
 typedef LinearShape<64, 64, 2, 1, 2, 2> Pair64;
@@ -729,10 +750,13 @@ static_assert(Tile256::kOccupancy == 1 && Tile128::kOccupancy == 2 && Pair64::kO
 
 // f(shape) with the shape that takes least.
 template <typename F>
-static hipError_t with_shape(long groups, long m, long c, long q, int cus, F&& f) {
+static hipError_t with_shape(long groups, long m, bool spread, long c, long q, int cus, F&& f) {
   int best = 0;
-  for (int i = 1; i < 4; i++)
-    if (kShapeCosts[i].of(groups, m, c, q, cus) < kShapeCosts[best].of(groups, m, c, q, cus)) best = i;
+  double least = kShapeCosts[0].of(groups, m, spread, c, q, cus);
+  for (int i = 1; i < 4; i++) {
+    const double cost = kShapeCosts[i].of(groups, m, spread, c, q, cus);
+    if (cost < least) least = cost, best = i;
+  }
   switch (best) {
     case 0: return f(Tile256{});
     case 1: return f(Tile128{});
