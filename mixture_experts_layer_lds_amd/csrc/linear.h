@@ -132,11 +132,14 @@ struct LinearShape {
   static constexpr int BM = BM_, BC = BC_, WM = WM_, WC = WC_, KG = KG_, kStages = NS_;
   static constexpr int kWaves = WM * WC * KG, kThreads = kWaves * 64;
   static constexpr int MB = BM / WM / 16, CB = BC / WC / 16;   // 16 x 16 blocks of a wave
+  static constexpr int MB0 = (MB + 1) / 2;                     // ... of m in the first part of its operand
+  static constexpr int kRows0 = MB0 * WM * 16, kRows1 = BM - kRows0;
   static constexpr int kSub = (BM + BC) * kStepQ * 2;          // bytes of a sub-step
   static constexpr int kStage = kSub * KG;
   static constexpr int kRanges = 3 * 4 * (kMaxExperts + 1);    // first item and rows of every expert
   static constexpr int kScratch = 2048;                        // of a wave: 16 rows of 128 bytes
-  static constexpr int kLds = kStage * kStages + kRanges + kWaves * kScratch;
+  static constexpr int kSpare = 1024;                          // where copies go that a wave has too many
+  static constexpr int kLds = kStage * kStages + kRanges + kSpare + kWaves * kScratch;
   // workgroups that share a CU's LDS, and the waves on a SIMD that they make
   static constexpr int kOccupancy = kLds <= 80 * 1024 && kThreads <= 256 ? 2 : 1;
   static constexpr int kWavesASimd = kOccupancy * kWaves / 4;

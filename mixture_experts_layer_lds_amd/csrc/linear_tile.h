@@ -230,12 +230,17 @@ linear_tile_kernel(moe_host::LinearArgs g) {
   typedef typename Row::elem elem;
   constexpr bool TR = OP == kGradW, TC = OP != kForward;
   constexpr int BM = S::BM, BC = S::BC, KG = S::KG, WM = S::WM, WC = S::WC, MB = S::MB, CB = S::CB;
-  // the operand of m in two halves, that of c in one piece, in this order in a sub-step
-  typedef OperandTile<TR, BM / 2> HalfR;
+  // the operand of m in two parts, that of c in one, in this order in a sub-step
+  typedef OperandTile<TR, S::kRows0> Part0;
+  typedef OperandTile<TR, S::kRows1> Part1;
   typedef OperandTile<TC, BC> TileC;
-  static_assert(KG * HalfR::kCopies % S::kWaves == 0 && KG * TileC::kCopies % S::kWaves == 0, "whole copies a wave");
-  constexpr int NH = KG * HalfR::kCopies / S::kWaves, NC = KG * TileC::kCopies / S::kWaves;   // copies of a wave
-  constexpr int NA = NC + NH, NALL = NC + 2 * NH;
+  // copies of a wave; where the first part's do not go round, some copy nothing
+  constexpr int N0 = (KG * Part0::kCopies + S::kWaves - 1) / S::kWaves, N1 = KG * Part1::kCopies / S::kWaves;
+  constexpr int NC = KG * TileC::kCopies / S::kWaves;
+  static_assert(KG * Part1::kCopies % S::kWaves == 0 && KG * TileC::kCopies % S::kWaves == 0, "whole copies a wave");
+  static_assert(!TR || S::kRows0 == S::kRows1, "a lane's place in a transposed part goes by its width");
+  constexpr bool UNEVEN = KG * Part0::kCopies % S::kWaves != 0;
+  constexpr int NA = NC + N0, NALL = NA + N1;
   __shared__ __attribute__((aligned(1024))) char lds[S::kLds];
   Experts* const experts = reinterpret_cast<Experts*>(lds + S::kStage * S::kStages);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void*)lds;
@@ -292,7 +297,7 @@ linear_tile_kernel(moe_host::LinearArgs g) {
   const char* baseR;
   const char* baseC;
   uint32_t bytesR, bytesC;        // of the operands that are contiguous in q
-  uint32_t offR[2 * NH], offC[NC];   // a lane's offset of each of its copies, but for the stage's
+  uint32_t offR[N0 + N1], offC[NC];   // a lane's offset of each of its copies, but for the stage's
   const size_t ldR = OP == kForward ? (size_t)K * 2 : (size_t)N * 2, ldC = (size_t)K * 2;   // bytes a row in memory
   const int G = gridDim.x;
 
@@ -329,12 +334,14 @@ linear_tile_kernel(moe_host::LinearArgs g) {
     }
     baseR = uniform_ptr(baseR);
     baseC = uniform_ptr(baseC);
-#pragma unroll
-    for (int j = 0; j < 2 * NH; j++) {
-      const int id = j % NH * S::kWaves + wave, sub = id / HalfR::kCopies, i = id % HalfR::kCopies, half = j / NH * (BM / 2);
-      const int row = HalfR::copy_row(i, lane) + (TR ? sub * kStepQ : half);
-      offR[j] = (uint32_t)(row * ldR) + HalfR::copy_byte(i, lane) + (TR ? half * 2 : sub * 128);
-    }
+    repeat<N0 + N1>([&](auto at) {
+      constexpr int j = at, part = j < N0 ? 0 : 1, first = part ? S::kRows0 : 0;
+      typedef std::conditional_t<part == 0, Part0, Part1> Part;
+      const int id = (part ? j - N0 : j) * S::kWaves + wave, sub = id / Part::kCopies, i = id % Part::kCopies;
+      const int row = Part::copy_row(i, lane) + (TR ? sub * kStepQ : first);
+      offR[j] = (uint32_t)(row * ldR) + Part::copy_byte(i, lane) + (TR ? first * 2 : sub * 128);
+      if (UNEVEN && part == 0 && id >= KG * Part0::kCopies) offR[j] = kOutside;
+    });
 #pragma unroll
     for (int j = 0; j < NC; j++) {
       const int id = j * S::kWaves + wave, sub = id / TileC::kCopies, i = id % TileC::kCopies;
@@ -363,15 +370,18 @@ linear_tile_kernel(moe_host::LinearArgs g) {
     s.stage = lds + slot * S::kStage;
     return s;
   };
-  // copy j: those of c, then of the halves of m
+  // copy j: those of c, then of the parts of m
   auto copy_one = [&](const Source& s, auto at) {
-    constexpr int j = at, r = j - NC;
+    constexpr int j = at, r = j - NC, part = r < N0 ? 0 : 1;
     if constexpr (j < NC) {
       const int id = j * S::kWaves + wave, sub = id / TileC::kCopies, i = id % TileC::kCopies;
       range_dma16(s.c, offC[j], TC ? 0 : s.q2, s.stage + sub * S::kSub + BM * kStepQ * 2 + i * 1024);
     } else {
-      const int id = r % NH * S::kWaves + wave, sub = id / HalfR::kCopies, i = id % HalfR::kCopies;
-      range_dma16(s.r, offR[r], TR ? 0 : s.q2, s.stage + sub * S::kSub + r / NH * (BM * kStepQ) + i * 1024);
+      typedef std::conditional_t<part == 0, Part0, Part1> Part;
+      const int id = (part ? r - N0 : r) * S::kWaves + wave, sub = id / Part::kCopies, i = id % Part::kCopies;
+      char* to = s.stage + sub * S::kSub + part * (S::kRows0 * kStepQ * 2) + i * 1024;
+      if (UNEVEN && part == 0 && id >= KG * Part0::kCopies) to = lds + S::kStage * S::kStages + S::kRanges;
+      range_dma16(s.r, offR[r], TR ? 0 : s.q2, to);
     }
   };
   // Ahead of the copies at from_step: into the next item behind the last stage
@@ -381,11 +391,12 @@ linear_tile_kernel(moe_host::LinearArgs g) {
     if (from_step == from.steps - 1) {
       const int q2 = from_step * kStepQ * KG * 2;
       if constexpr (!TR) {
-#pragma unroll
-        for (int j = 0; j < 2 * NH; j++) {
-          const int id = j % NH * S::kWaves + wave;
-          if (q2 + id / HalfR::kCopies * 128 + HalfR::copy_byte(id % HalfR::kCopies, lane) >= from.Q * 2) offR[j] = kOutside;
-        }
+        repeat<N0 + N1>([&](auto at) {
+          constexpr int j = at, part = j < N0 ? 0 : 1;
+          typedef std::conditional_t<part == 0, Part0, Part1> Part;
+          const int id = (part ? j - N0 : j) * S::kWaves + wave;
+          if (q2 + id / Part::kCopies * 128 + Part::copy_byte(id % Part::kCopies, lane) >= from.Q * 2) offR[j] = kOutside;
+        });
       }
       if constexpr (!TC) {
 #pragma unroll
@@ -444,10 +455,10 @@ linear_tile_kernel(moe_host::LinearArgs g) {
     constexpr auto q_of = [](int ph, int phases) { return phases == 2 ? ph : SPLIT ? ph % 2 : ph / 2; };
     constexpr auto m_of = [](int ph, int phases) { return phases == 2 ? 0 : SPLIT ? ph / 2 : ph % 2; };
     auto stages = [&](auto blocks) {
-      constexpr int MA = blocks, M0 = MB <= 4 || MA <= MB / 2 ? MA : MB / 2, M1 = MA - M0, PHASES = M1 ? 4 : 2;
+      constexpr int MA = blocks, M0 = MB <= 4 || MA <= S::MB0 ? MA : S::MB0, M1 = MA - M0, PHASES = M1 ? 4 : 2;
       u32x4 fa[2][CB], fb[2][M0];
       const uint32_t sub = lds0 + kg * S::kSub;
-      const uint32_t placeR = sub + HalfR::lane_place(wm, lane);
+      const uint32_t placeR = sub + Part0::lane_place(wm, lane);
       const uint32_t placeC = sub + BM * kStepQ * 2 + TileC::lane_place(wc * CB, lane);
       uint32_t atR, atC;
       auto turn = [&]() {   // the places in the stage at `slot`
@@ -459,8 +470,9 @@ linear_tile_kernel(moe_host::LinearArgs g) {
       auto read_one = [&](auto phase, auto at) {
         constexpr int ph = phase, h = q_of(ph, PHASES), mh = m_of(ph, PHASES), r = at, nc = mh == 0 ? CB : 0;
         if constexpr (r == 0 || r > nc) {
-          constexpr int m = (r == 0 ? 0 : r - nc) + (mh == 0 ? 0 : M0), half = m / (MB / 2), in_half = m % (MB / 2);
-          fb[ph % 2][r == 0 ? 0 : r - nc] = HalfR::fragment(atR + half * (BM * kStepQ), in_half * WM, h);
+          constexpr int m = (r == 0 ? 0 : r - nc) + (mh == 0 ? 0 : M0);
+          fb[ph % 2][r == 0 ? 0 : r - nc] = m < S::MB0 ? Part0::fragment(atR, m * WM, h)
+                                                       : Part1::fragment(atR + S::kRows0 * kStepQ * 2, (m - S::MB0) * WM, h);
         } else {
           fa[h][r - 1] = TileC::fragment(atC, r - 1, h);
         }
@@ -475,10 +487,10 @@ linear_tile_kernel(moe_host::LinearArgs g) {
           constexpr int first_m = mh == 0 ? 0 : M0, M = mh == 0 ? M0 : M1;
           constexpr bool last = ph == PHASES - 1, once = !SPLIT || M1 == 0, meet = last || (!once && ph == 1);
           constexpr int reads = (m_of(next, PHASES) == 0 ? M0 + CB : M1), mults = M * CB;
-          constexpr int copies = !meet ? 0 : once ? NALL : last ? NH : NA, first_copy = !once && last ? NA : 0;
+          constexpr int copies = !meet ? 0 : once ? NALL : last ? N1 : NA, first_copy = !once && last ? NA : 0;
           constexpr int extra = reads + copies;
           if constexpr (meet) {
-            wait_but<once ? (S::kStages - 2) * NALL + (SPLIT ? NH : 0) : (S::kStages - 1) * NALL>();
+            wait_but<once ? (S::kStages - 2) * NALL + (SPLIT ? N1 : 0) : (S::kStages - 1) * NALL>();
             barrier_nofence();
           }
           if constexpr (meet && (once || !last)) s = source(slot);
@@ -705,7 +717,7 @@ static inline int mean_rows(const moe_host::LinearArgs& a) {
   return a.expert_offsets ? (int)blocks(a.rows, a.E) : a.rows;
 }
 
-// The four shapes, and how long one takes for `groups` products of m x c over q:
+// The shapes, and how long one takes for `groups` products of m x c over q:
 // the rounds of its items over the chip, times an item's stages and what it has
 // besides.  Measured, us a stage with every CU at work and us an item besides:
 //                               stage of          stage   besides
@@ -713,10 +725,12 @@ static inline int mean_rows(const moe_host::LinearArgs& a) {
 //   Tile128  128 x 128, two a CU  64 q              1.08    2.5
 //   Pair64   64 x 64, two a CU    2 x 64 q          1.4     3
 //   Quad64   64 x 64            4 x 64 q          2.0     2.3
+//   Tile288  288 x 256          64 q              1.97    3.5
 // A tile of few rows takes 0.4 of a full one and more by its rows.  Rows of experts
 // spread: m is their mean, its root the deviation, and the tiles are the expected
-// number (64 experts of 100 rows, 4096 -> 1024: one of them with more than 128 is a
-// second round of Tile128, 171 us, and none of Tile256, 128).
+// number.  Tile288 is for them (products with rows on m): of experts with 256 rows,
+// or a multiple, on average half would need a tile more of 256 (32 such experts,
+// 4096 -> 7168 gradient of the rows 782 -> 661 us, 2048 -> 7168 forward 331 -> 307).
 // The large tiles do most work a round, the small ones fill the chip where the
 // product is small.  us by shape in that order, the rule's choice by *:
 //   forward     8192 x 4096 x 2048 (rows, N, K)     105*  125   -     -
@@ -735,25 +749,28 @@ struct ShapeCost {
       for (long at = BM; at < m + 4 * deviation; at += BM) tiles += 0.5 * std::erfc((at - m) / (deviation * 1.41421356));
     }
     const double fill = std::min(1.0, m / (tiles * BM));
-    const double rounds = std::ceil(groups * tiles * blocks(c, BC) / ((double)cus * occupancy));
+    const double rounds = std::ceil(std::round(groups * tiles) * blocks(c, BC) / ((double)cus * occupancy));
     return rounds * (blocks(q_len, q) * stage * (0.4 + 0.6 * fill) + besides);
   }
 };
 constexpr ShapeCost kShapeCosts[] = {
-    {256, 256, 64, 1, 1.75, 3.5}, {128, 128, 64, 2, 1.08, 2.5}, {64, 64, 128, 2, 1.4, 3.0}, {64, 64, 256, 1, 2.0, 2.3}};
+    {256, 256, 64, 1, 1.75, 3.5}, {128, 128, 64, 2, 1.08, 2.5}, {64, 64, 128, 2, 1.4, 3.0}, {64, 64, 256, 1, 2.0, 2.3},
+    {288, 256, 64, 1, 1.97, 3.5}};
 typedef LinearShape<256, 256, 2, 4, 1, 2> Tile256;
 typedef LinearShape<128, 128, 2, 2, 1, 2> Tile128;
 typedef LinearShape<64, 64, 2, 1, 2, 2> Pair64;
 typedef LinearShape<64, 64, 2, 1, 4, 2> Quad64;
-static_assert(Tile256::kOccupancy == 1 && Tile128::kOccupancy == 2 && Pair64::kOccupancy == 2 && Quad64::kOccupancy == 1,
+typedef LinearShape<288, 256, 2, 4, 1, 2> Tile288;
+static_assert(Tile256::kOccupancy == 1 && Tile128::kOccupancy == 2 && Pair64::kOccupancy == 2 && Quad64::kOccupancy == 1 &&
+                  Tile288::kOccupancy == 1,
               "the workgroups of a CU that the costs are of");
 
-// f(shape) with the shape that takes least.
-template <typename F>
+// f(shape) with the shape that takes least; ROWS: m are rows.
+template <bool ROWS, typename F>
 static hipError_t with_shape(long groups, long m, bool spread, long c, long q, int cus, F&& f) {
   int best = 0;
   double least = kShapeCosts[0].of(groups, m, spread, c, q, cus);
-  for (int i = 1; i < 4; i++) {
+  for (int i = 1; i < (ROWS ? 5 : 4); i++) {
     const double cost = kShapeCosts[i].of(groups, m, spread, c, q, cus);
     if (cost < least) least = cost, best = i;
   }
@@ -761,8 +778,11 @@ static hipError_t with_shape(long groups, long m, bool spread, long c, long q, i
     case 0: return f(Tile256{});
     case 1: return f(Tile128{});
     case 2: return f(Pair64{});
-    default: return f(Quad64{});
+    case 3: return f(Quad64{});
+    default: break;
   }
+  if constexpr (ROWS) return f(Tile288{});
+  else return hipErrorInvalidValue;
 }
 
 }  // namespace moe

@@ -10,7 +10,8 @@ from test_gpu_linear import ACTS, TYPES, gen, grouping, lib, normal  # noqa: F40
 
 pytestmark = pytest.mark.gpu
 #: rows by expert: every height of a partial tile, one row to several tiles, none in between
-RAGGED = [1, 16, 17, 32, 33, 0, 64, 65, 96, 97, 128, 129, 160, 161, 192, 193, 224, 0, 225, 256, 257, 320, 385, 512, 513, 770]
+RAGGED = [1, 16, 17, 32, 33, 0, 64, 65, 96, 97, 128, 129, 160, 161, 192, 193, 224, 0, 225, 256, 257, 320, 385, 512, 513, 770,
+          288, 289, 576, 577, 600, 500]
 
 
 def ragged(lib, seed):
@@ -62,7 +63,7 @@ def grad_w(lib, g, routing, k, off, R, E, N, K, out, dtype):
 
 # wide and narrow: the largest tiles, and small ones, for the product and for its gradient
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("N,K", [(4112, 264), (272, 136), (528, 1032)])
+@pytest.mark.parametrize("N,K", [(4112, 264), (2816, 264), (272, 136), (528, 1032)])
 def test_every_height(lib, N, K, dtype):
     routing, off, R, E = ragged(lib, N)
     for act in ACTS:
@@ -81,6 +82,9 @@ def test_every_height(lib, N, K, dtype):
     (100, 8, 40, 272, 264, 0.0, False),      # about 20 rows an expert
     (300, 2, 60, 1040, 136, 0.05, True),     # few rows an expert, hundreds of one
     (40, 2, 70, 2064, 72, 0.0, True),
+    (64, 4, 64, 4112, 72, 0.0, False),       # four rows an expert, many columns
+    (2048, 2, 16, 2816, 264, 0.0, False),    # 256 rows an expert, more or less
+    (2048, 2, 16, 272, 2816, 0.0, False),
 ])
 def test_many_tiles(lib, T, k, E, N, K, p_drop, hot, dtype):
     routing, off = grouping(lib, T, k, E, T, p_drop, hot)
