@@ -104,7 +104,7 @@ linear_stream_kernel(moe_host::LinearArgs g) {
     const bool any = from_item < total;
     const auto rx = range_rsrc(uniform_ptr(base_x), uniform(any ? bytes_x : 0));
     const auto rw = range_rsrc(uniform_ptr(base_w), uniform(any ? bytes_w : 0));
-    const int q2 = (from_chunk * kStreamWaves + wave) * kStepQ * 2;
+    const int q2 = any ? (from_chunk * kStreamWaves + wave) * kStepQ * 2 : 0;   // within the range, also where that is nothing
     const bool inside = q2 + byte < K * 2;   // no q behind the end
     char* const at = ring + slot * S::kSlot;
 #pragma unroll

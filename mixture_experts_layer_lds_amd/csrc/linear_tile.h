@@ -366,7 +366,7 @@ linear_tile_kernel(moe_host::LinearArgs g) {
     const uint32_t in_r = TR ? (uint32_t)(left * ldR) - from.m0 * 2 : bytesR, in_c = TC ? (uint32_t)(left * ldC) - from.c0 * 2 : bytesC;
     s.r = range_rsrc(uniform_ptr(r), uniform(any ? in_r : 0));
     s.c = range_rsrc(uniform_ptr(c), uniform(any ? in_c : 0));
-    s.q2 = q0 * 2;
+    s.q2 = any ? q0 * 2 : 0;   // never more than the range, also where that is nothing
     s.stage = lds + slot * S::kStage;
     return s;
   };
