@@ -137,7 +137,7 @@ struct LinearShape {
   static constexpr int kSub = (BM + BC) * kStepQ * 2;          // bytes of a sub-step
   static constexpr int kStage = kSub * KG;
   static constexpr int kRanges = 3 * 4 * (kMaxExperts + 1);    // first item and rows of every expert
-  static constexpr int kScratch = 2048;                        // of a wave: 16 rows of 128 bytes
+  static constexpr int kScratch = 2048;                        // of a wave: 16 rows of 128 bytes, or its columns in 64 bits
   static constexpr int kSpare = 1024;                          // where copies go that a wave has too many
   static constexpr int kLds = kStage * kStages + kRanges + kSpare + kWaves * kScratch;
   // workgroups that share a CU's LDS, and the waves on a SIMD that they make
