@@ -62,3 +62,76 @@ def test_bias_gradient_of_a_hot_expert(lib, dtype):
     _, db = lib.moe_grouped_linear_grad_w(dy, x, routing, k, E, want_bias=True, dtype=torch.float32)
     want = torch.stack([dy[off[e]:off[e + 1]].double().sum(0) for e in range(E)])
     ref.within(db, want, bias_bound(want.abs(), want, torch.float32), "dbias by expert")
+
+
+def ternary(g, rows, cols, dtype):
+    """-1, 0 or 1: every partial sum of products over at most 2^24 rows is a whole number that fp32
+    holds, so that sums are exact in any order and one row left out or taken twice is seen."""
+    v = torch.empty(rows, cols, dtype=dtype, device="cuda")
+    for a in range(0, rows, 1 << 16):
+        v[a:a + (1 << 16)] = torch.randint(-1, 2, v[a:a + (1 << 16)].shape, generator=g, device="cuda", dtype=torch.int8)
+    return v
+
+
+def whole_sums(dy, x, first, last):
+    """dw and dbias over the rows [first, last) in 64 bits."""
+    N, K = dy.shape[1], x.shape[1]
+    dw, db = torch.zeros(N, K, dtype=torch.float64, device="cuda"), torch.zeros(N, dtype=torch.float64, device="cuda")
+    step = max(1, (1 << 26) // max(N, K))
+    for a in range(first, last, step):
+        d, xe = dy[a:min(last, a + step)].double(), x[a:min(last, a + step)].double()
+        dw += d.t().contiguous() @ xe
+        db += d.sum(0)
+    return dw, db
+
+
+def rounded_once(want, dtype):
+    """Whole numbers within fp32: the one rounding of the exact sum."""
+    return want.float().to(dtype)
+
+
+# `far`: the first row that a mistake would lose (an offset past 2^32 bytes, the end of many rows)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,N,K,far", [
+    (1 << 24, 16, 8, (1 << 24) - 1),                       # the most rows; the last one of them
+    ((1 << 24) - 33, 136, 136, (1 << 32) // 272),          # both operands past 2^32 bytes
+    (70000, 32, 32768, 1 << 16),                           # x is
+    (70000, 32768, 32, 1 << 16),                           # dy is
+    (1 << 20, 2048, 2056, (1 << 32) // 4112),              # larger tiles
+])
+def test_every_row_counts(lib, rows, N, K, far, dtype):
+    g = gen(rows + K)
+    dy, x = ternary(g, rows, N, dtype), ternary(g, rows, K, dtype)
+    dy[far:, 0], x[far:, 0] = 1, 1                         # what is checked below: the far rows add up
+    near, nearb = whole_sums(dy, x, 0, far)
+    rest, restb = whole_sums(dy, x, far, rows)
+    assert float(rest[0, 0]) == rows - far and float(restb[0]) == rows - far
+    want, wantb = near + rest, nearb + restb
+    dw, db = lib.moe_linear_grad_w(dy, x, want_bias=True, dtype=torch.float32)
+    assert torch.equal(dw.double(), want) and torch.equal(db.double(), wantb)
+    assert not torch.equal(dw.double(), near) and not torch.equal(db.double(), nearb)
+    assert torch.equal(lib.moe_linear_grad_w(dy, x, dtype=torch.float32), dw)
+    if float(want.abs().max()) < torch.finfo(dtype).max:
+        assert torch.equal(lib.moe_linear_grad_w(dy, x), rounded_once(want, dtype))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("N,K", [(16, 34000), (34000, 16), (2064, 264)])
+def test_every_sorted_row_counts(lib, N, K, dtype):
+    """65536 rows of a few experts, the last ones' past 2^32 bytes."""
+    T, k, E = 32768, 2, 5
+    routing, off = grouping(lib, T, k, E, 4, 0.001, hot=True)
+    g = gen(N)
+    dy, x = ternary(g, T * k, N, dtype), ternary(g, T * k, K, dtype)
+    n = off[E]
+    dy[n:], x[n:] = float("nan"), float("nan")             # rows behind the last valid one take no part
+    if max(N, K) == 34000:
+        assert (n - 1) * 68000 > 1 << 32 and off[E - 1] < n
+    dw, db = lib.moe_grouped_linear_grad_w(dy, x, routing, k, E, want_bias=True, dtype=torch.float32)
+    for e in range(E):
+        want, wantb = whole_sums(dy, x, off[e], off[e + 1])
+        assert torch.equal(dw[e].double(), want) and torch.equal(db[e].double(), wantb), e
+    base = torch.randint(-4, 5, dw.shape, generator=g, device="cuda").float()   # whole numbers too
+    held = base.clone()
+    lib.moe_grouped_linear_grad_w(dy, x, routing, k, E, dw=held, accumulate=True)
+    assert torch.equal(held, base + dw)
