@@ -6,7 +6,7 @@ namespace moe {
 template <typename Elem>
 static hipError_t grad_w(moe_host::LinearArgs a, int cus, hipStream_t s) {
   a.stream_out = past_caches(2 * (size_t)a.rows * (a.N + a.K) + (size_t)a.E * a.N * a.K * (a.out_fp32 ? 4 : 2));
-  return with_shape<false>(a.E, a.N, false, a.K, mean_rows(a), cus, [&](auto shape) {
+  return with_shape<false>(grad_w_tile(sizes_of(a), cus), [&](auto shape) {
     typedef decltype(shape) S;
     const long items = a.E * blocks(a.N, S::BM) * blocks(a.K, S::BC);
     return a.dbias ? launch_linear_tile<Elem, kGradW, S, true>(a, items, cus, s)

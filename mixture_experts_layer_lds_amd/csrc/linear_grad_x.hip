@@ -7,7 +7,7 @@ template <typename Elem>
 static hipError_t grad_x(moe_host::LinearArgs a, int cus, hipStream_t s) {
   const size_t z = a.act == MOE_ACT_NONE ? 1 : a.act == MOE_ACT_SWIGLU ? 4 : 2;   // dx, and z as wide
   a.stream_out = past_caches(2 * ((size_t)a.rows * (a.N + z * a.K) + (size_t)a.E * a.N * a.K));
-  return with_shape<true>(used_groups(a), mean_rows(a), a.expert_offsets != nullptr, a.K, a.N, cus, [&](auto shape) {
+  return with_shape<true>(grad_x_tile(sizes_of(a), cus), [&](auto shape) {
     typedef decltype(shape) S;
     return launch_linear_tile<Elem, kGradX, S>(a, max_tiles(a, S::BM) * blocks(a.K, S::BC), cus, s);
   });

@@ -29,11 +29,10 @@
 // did other orders of q by column (306).
 #pragma once
 
-#include <algorithm>
-#include <cmath>
 #include <type_traits>
 
 #include "linear.h"
+#include "linear_shape.h"
 
 namespace moe {
 
@@ -737,78 +736,33 @@ static inline long max_tiles(const moe_host::LinearArgs& a, int BM) {
   return a.expert_offsets ? a.rows / BM + (a.rows < a.E ? a.rows : a.E) : (a.rows + BM - 1) / BM;
 }
 
-static inline long blocks(long n, long size) { return (n + size - 1) / size; }
-
-// Experts that have rows at most, and the rows of one were they spread evenly.
-static inline int used_groups(const moe_host::LinearArgs& a) {
-  return !a.expert_offsets ? 1 : a.rows < a.E ? a.rows : a.E;
-}
-static inline int mean_rows(const moe_host::LinearArgs& a) {
-  return a.expert_offsets ? (int)blocks(a.rows, a.E) : a.rows;
+inline LinearSizes sizes_of(const moe_host::LinearArgs& a) {
+  return {a.rows, a.E, a.expert_offsets != nullptr, a.N, a.K, a.act == MOE_ACT_SWIGLU};
 }
 
-// The shapes, and how long one takes for `groups` products of m x c over q:
-// the rounds of its items over the chip, times an item's stages and what it has
-// besides.  Measured, us a stage with every CU at work and us an item besides:
-//                               stage of          stage   besides
-//   Tile256  256 x 256          64 q              1.75    3.5
-//   Tile128  128 x 128, two a CU  64 q              1.08    2.5
-//   Pair64   64 x 64, two a CU    2 x 64 q          1.4     3
-//   Quad64   64 x 64            4 x 64 q          2.0     2.3
-//   Tile288  288 x 256          64 q              1.97    3.5
-// A tile of few rows takes 0.4 of a full one and more by its rows.  Rows of experts
-// spread: m is their mean, its root the deviation, and the tiles are the expected
-// number.  Tile288 is for them (products with rows on m): of experts with 256 rows,
-// or a multiple, on average half would need a tile more of 256 (32 such experts,
-// 4096 -> 7168 gradient of the rows 782 -> 661 us, 2048 -> 7168 forward 331 -> 307).
-// The large tiles do most work a round, the small ones fill the chip where the
-// product is small.  us by shape in that order, the rule's choice by *:
-//   forward     8192 x 4096 x 2048 (rows, N, K)     105*  125   -     -
-//               2048 x 2048 x 1024                  29    15.6* 22.7  35.9
-//               4096 x 512 x 1024                   26.9  13.7  13.6* 19.0
-//               256 x 4096 x 7168                   131   81    44    37*
-//   gradient of the matrices, 8192 x 1024 x 512     207   116   56    47*
-struct ShapeCost {
-  int BM, BC, q, occupancy;
-  double stage, besides;
-  double of(long groups, long m, bool spread, long c, long q_len, int cus) const {
-    double tiles = (double)blocks(m, BM);
-    if (spread) {
-      const double deviation = std::sqrt((double)m);
-      tiles = 1.0;
-      for (long at = BM; at < m + 4 * deviation; at += BM) tiles += 0.5 * std::erfc((at - m) / (deviation * 1.41421356));
-    }
-    const double fill = std::min(1.0, m / (tiles * BM));
-    const double rounds = std::ceil(std::round(groups * tiles) * blocks(c, BC) / ((double)cus * occupancy));
-    return rounds * (blocks(q_len, q) * stage * (0.4 + 0.6 * fill) + besides);
-  }
-};
-constexpr ShapeCost kShapeCosts[] = {
-    {256, 256, 64, 1, 1.75, 3.5}, {128, 128, 64, 2, 1.08, 2.5}, {64, 64, 128, 2, 1.4, 3.0}, {64, 64, 256, 1, 2.0, 2.3},
-    {288, 256, 64, 1, 1.97, 3.5}};
 typedef LinearShape<256, 256, 2, 4, 1, 2> Tile256;
 typedef LinearShape<128, 128, 2, 2, 1, 2> Tile128;
 typedef LinearShape<64, 64, 2, 1, 2, 2> Pair64;
 typedef LinearShape<64, 64, 2, 1, 4, 2> Quad64;
 typedef LinearShape<288, 256, 2, 4, 1, 2> Tile288;
-static_assert(Tile256::kOccupancy == 1 && Tile128::kOccupancy == 2 && Pair64::kOccupancy == 2 && Quad64::kOccupancy == 1 &&
-                  Tile288::kOccupancy == 1,
-              "the workgroups of a CU that the costs are of");
 
-// f(shape) with the shape that takes least; ROWS: m are rows.
+template <typename S>
+constexpr bool is_cost_of(LinearTile t) {
+  const ShapeCost& c = kShapeCosts[t];
+  return S::BM == c.BM && S::BC == c.BC && S::KG * kStepQ == c.q && S::kOccupancy == c.occupancy;
+}
+static_assert(is_cost_of<Tile256>(kTile256) && is_cost_of<Tile128>(kTile128) && is_cost_of<Pair64>(kPair64) &&
+                  is_cost_of<Quad64>(kQuad64) && is_cost_of<Tile288>(kTile288),
+              "the shapes that the costs are of");
+
+// f(shape) of a tile; ROWS: m are rows.
 template <bool ROWS, typename F>
-static hipError_t with_shape(long groups, long m, bool spread, long c, long q, int cus, F&& f) {
-  int best = 0;
-  double least = kShapeCosts[0].of(groups, m, spread, c, q, cus);
-  for (int i = 1; i < (ROWS ? 5 : 4); i++) {
-    const double cost = kShapeCosts[i].of(groups, m, spread, c, q, cus);
-    if (cost < least) least = cost, best = i;
-  }
-  switch (best) {
-    case 0: return f(Tile256{});
-    case 1: return f(Tile128{});
-    case 2: return f(Pair64{});
-    case 3: return f(Quad64{});
+static hipError_t with_shape(LinearTile tile, F&& f) {
+  switch (tile) {
+    case kTile256: return f(Tile256{});
+    case kTile128: return f(Tile128{});
+    case kPair64: return f(Pair64{});
+    case kQuad64: return f(Quad64{});
     default: break;
   }
   if constexpr (ROWS) return f(Tile288{});
