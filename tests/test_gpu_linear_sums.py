@@ -135,3 +135,46 @@ def test_every_sorted_row_counts(lib, N, K, dtype):
     held = base.clone()
     lib.moe_grouped_linear_grad_w(dy, x, routing, k, E, dw=held, accumulate=True)
     assert torch.equal(held, base + dw)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_accumulation_in_a_graph(lib, dtype):
+    """Gradients added to what dw and dbias hold, captured and replayed over new rows between
+    eager work: whole numbers, so that every replay's sums are exact."""
+    T, k, E, N, K = 1500, 2, 7, 272, 136
+    routing, off = grouping(lib, T, k, E, 6, 0.05, hot=True)
+    dy, x = torch.empty(T * k, N, dtype=dtype, device="cuda"), torch.empty(T * k, K, dtype=dtype, device="cuda")
+    dw, db = torch.zeros(E, N, K, device="cuda"), torch.zeros(E, N, device="cuda")
+    dy.zero_(), x.zero_()
+    call = lambda: lib.moe_grouped_linear_grad_w(dy, x, routing, k, E, dw=dw, dbias=db, accumulate=True)
+    call()
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        call()
+    want, wantb = torch.zeros(E, N, K, dtype=torch.float64, device="cuda"), torch.zeros(E, N, dtype=torch.float64, device="cuda")
+    for seed in range(4):
+        g = gen(seed)
+        dy.copy_(ternary(g, T * k, N, dtype)), x.copy_(ternary(g, T * k, K, dtype))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for e in range(E):
+            a, b = whole_sums(dy, x, off[e], off[e + 1])
+            want[e] += a
+            wantb[e] += b
+        assert torch.equal(dw.double(), want) and torch.equal(db.double(), wantb), seed
+
+
+def test_bias_gradient_keeps_nan_in_its_column(lib):
+    """An Inf or NaN of dy over several folds of the sum, in the gradient of its own bias alone."""
+    dtype, rows, N, K = torch.bfloat16, 70001, 264, 264
+    g = gen(8)
+    dy, x = ternary(g, rows, N, dtype), torch.zeros(rows, K, dtype=dtype, device="cuda")
+    _, clean = lib.moe_linear_grad_w(dy, x, want_bias=True, dtype=torch.float32)
+    dy[5, 3], dy[rows - 1, 200], dy[40000, 100], dy[7, 100] = float("nan"), float("inf"), float("inf"), float("-inf")
+    _, db = lib.moe_linear_grad_w(dy, x, want_bias=True, dtype=torch.float32)
+    assert bool(db[3].isnan()) and float(db[200]) == float("inf") and bool(db[100].isnan())
+    keep = torch.ones(N, dtype=torch.bool, device="cuda")
+    keep[[3, 100, 200]] = False
+    assert torch.equal(db[keep], clean[keep])
