@@ -594,8 +594,9 @@ int moe_router_topk_grad(const float *logits, const int32_t *topk_ids, const flo
  * row type or MOE_ROW_FP32.  Before the rounding dbias is within 2^-16 of the sum
  * of magnitudes, of any number of rows; dw adds the products of 32 rows at a time
  * to an fp32 sum, so that rows of one sign drift as in any such chain (measured, of
- * rows that are all alike: 3e-5 at 2^16 rows, 2e-4 at 2^20, 4e-3 at 2^24).  accumulate = 1 adds them to what dw and dbias hold
- * (one rounding of the sum), 0 overwrites.
+ * rows that are all alike: 3e-5 at 2^16 rows, 2e-4 at 2^20, 4e-3 at 2^24).
+ * accumulate = 1 adds them to what dw and dbias hold (one rounding of the sum), 0
+ * overwrites.
  * moe_grouped_act_grad: dz[r] = dy[r] act'(z[r]) for an activation that no
  * product follows; dy [T*k][M], z and dz [T*k][M] (MOE_ACT_SWIGLU: [T*k][2M]);
  * act other than MOE_ACT_NONE.

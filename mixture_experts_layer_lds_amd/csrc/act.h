@@ -30,7 +30,8 @@ __device__ __forceinline__ float silu_slope(float z) {
 // Phi(z), the normal distribution function, and e^(-z^2 / 2).  For x = |z|:
 // 1 - Phi(x) = t e^(-x^2 / 2) Q(t) / 2 with t = 1 / (1 + 0.35 x) and Q the polynomial of
 // degree 8 with the least largest relative error on [0, 40], fitted to e^(x^2 / 2)
-// erfc(x / sqrt 2) / t by linear programming: 1.5e-7, 4.7e-7 as evaluated in fp32.
+// erfc(x / sqrt 2) / t by linear programming: 1.9e-7 with coefficients rounded to fp32,
+// 4.7e-7 evaluated in it.
 // The tail at negative z keeps that precision, times 1 + z^2 for the rounded
 // argument of 2^x, as far as fp32 holds it.  (The library's erfcf takes both sides
 // of its branches in most waves, and five times the instructions.)

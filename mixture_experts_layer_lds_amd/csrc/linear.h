@@ -1,5 +1,6 @@
 // Matrix products of rows with the experts' matrices, and their gradients, on
-// LDS tiles: what linear.hip and linear_grad_w.hip share.
+// LDS tiles: what linear.hip, linear_stream.hip, linear_grad_x.hip and
+// linear_grad_w.hip share.
 //
 // Every product is D[m][c] = sum over q of R[m][q] C[c][q], c the contiguous
 // index of D.  The MFMA takes C as its rows and R as its columns, so that a

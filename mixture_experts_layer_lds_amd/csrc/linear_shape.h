@@ -33,8 +33,10 @@ inline int mean_rows(const LinearSizes& a) { return a.grouped ? (int)blocks(a.ro
 // A tile of few rows takes 0.4 of a full one and more by its rows.  Rows of experts
 // spread: m is their mean, its root the deviation, and the tiles are the expected
 // number.  Tile288 is for them (products with rows on m): of experts with 256 rows,
-// or a multiple, on average half would need a tile more of 256 (32 such experts,
-// 4096 -> 7168 gradient of the rows 782 -> 661 us, 2048 -> 7168 forward 331 -> 307).
+// or a multiple, on average half would need a tile more of 256.  us by the rule without
+// it and with it: 32 experts of 256 rows on average, 4096 -> 7168 gradient of the rows 701
+// and 556, 2048 -> 7168 forward 300-315 and 292; 8 of 1024, 4096 x 14336 forward 850 and 742,
+// 28672 x 4096 gradient of the rows 2180 and 1660, but its forward 1480 and 1490.
 // The large tiles do most work a round, the small ones fill the chip where the
 // product is small.  us by shape in that order, the rule's choice by *:
 //   forward     8192 x 4096 x 2048 (rows, N, K)     105*  125   -     -
@@ -89,6 +91,11 @@ inline LinearTile grad_w_tile(const LinearSizes& a, int cus) {
 // on 16, on 32 and on the large tiles: 8 of 32 experts of 7168 x 2048, 64 tokens, 16
 // rows an expert 337 + 176, 312 + 175, 309 + 220; 128 tokens - , 470 + 214, 313 + 223;
 // 64 skewed experts of 3584 x 640, 128 tokens 110 + 63, 108 + 69, 138 + 58).
+// The rule knows the mean alone: an expert with most of the rows reads its weights once
+// for every 32 of them here.  us on the stream and on the large tiles, with no, half,
+// three quarters and 0.95 of the rows on one expert: 96 experts of 4096 x 7168, 16 rows on
+// average 938 and 915, 1066 and 987, 1150 and 980, 886 and 664; 64 of 1280 x 3584, 8 rows
+// 101 and 136, 112 and 134, 110 and 132, 47 and 59.
 // Of items of 4, 2 or 1 blocks of weight rows those that take least: the rounds over
 // the CUs, times the blocks and a third of one for the rows' copies and the waves'
 // meeting (2 experts of 28672 x 4096, one row each: 94 us on 4 blocks, 3.5 rounds, 81

@@ -6,7 +6,7 @@
 // chunks of 64 q in turn and add their sums at the end.  Every wave has a ring
 // of NS chunks of its own in LDS, which direct copies fill ahead of the
 // multiplications, on from item to item, and waits for its own copies alone:
-// the waves meet once an item.  NS is what LDS holds, so that a CU has 56 to 96 KiB
+// the waves meet once an item.  NS is what LDS holds, so that a CU has 48 to 96 KiB
 // of weights on their way.
 //
 // Measured (us; TB/s of weights): one row of 7168 with 4096 gate and up rows 12.5

@@ -22,7 +22,7 @@
 // matrix units are busy half of the cycles at the 2.0 GHz that the card then runs
 // at.  Copies of the kernel without the copies ran the first in 784 us, without the
 // LDS reads in 826, without both in 645.  Few rows an expert are bound by the
-// weights' way from HBM: 32 experts of 256 rows, 7168 x 2048, take 297 us forward
+// weights' way from HBM: 32 experts of 256 rows, 7168 x 2048, take 292 us forward
 // (3.2 TB/s of weights), 221 where all experts share one matrix: a stage's copies
 // are late by more than the stage and a half that LDS can hold ahead.  Loads ahead
 // of them into L2 made it slower (358 us: they share the CU's address path), and so

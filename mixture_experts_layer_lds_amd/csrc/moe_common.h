@@ -478,7 +478,7 @@ hipError_t launch_router_topk_grad(const float* logits, const int32_t* ids, cons
                                    int E, int k, bool renorm, int n_shared, float* dl, hipStream_t s);
 
 // Linear layers over rows in expert order or plain rows, and their gradients
-// (linear.hip, linear_grad_w.hip, act_grad.hip).
+// (linear.hip, linear_stream.hip, linear_grad_x.hip, linear_grad_w.hip, act_grad.hip).
 struct LinearArgs {
   const void* rows_in;            // forward: x [rows][K]; gradients: dy [rows][N]
   const void* x;                  // grad w: x [rows][K]
